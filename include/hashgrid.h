@@ -56,6 +56,10 @@ extern "C" {
 /* Element types. */
 #define HG_F32 0 /* IEEE binary32                                        */
 #define HG_F16 1 /* IEEE binary16 (storage only; all arithmetic is fp32) */
+/* The residual head's operators (hashgrid_linear_*, hashgrid_rms_norm_*,
+ * hashgrid_adamw_step) also take: */
+#define HG_BF16 2 /* bfloat16                                            */
+#define HG_F8 3   /* e4m3: 4 exponent bits (bias 7), 3 mantissa bits, no infinities, largest value 448 */
 
 /* Grid description.  Field names follow the pages' constructor arguments
  * (n_levels, n_features_per_level, log2_hashmap_size, base_resolution,
@@ -365,6 +369,194 @@ typedef struct {
 #define HG_ADAM_ZERO_GRAD 1
 int hashgrid_adam_step(const hg_adam *opt, int64_t count, float *param, float *m, float *v,
                        float *grad, void *param_f16, int32_t flags, void *stream);
+
+/* ------------------------------------------------------------------------
+ * A residual head on the encoding, and the step that trains it.  The pages'
+ * head is one shape (hashgrid_mlp_forward); these are the pieces of a head of
+ * any width: linear layers with their epilogue, the norm in front of them, and
+ * AdamW over the tables and every weight at once.  Rows are points.  Strides
+ * are in elements and count from row to row; a row's elements are consecutive.
+ * Rows may start at any address that is a multiple of the element's size.
+ * Calls keep the conventions above.
+ * ------------------------------------------------------------------------ */
+
+/* Activations. */
+#define HG_ACT_NONE 0
+#define HG_ACT_RELU 1      /* max(z, 0)                                           */
+#define HG_ACT_SILU 2      /* z / (1 + exp(-z))                                   */
+#define HG_ACT_GELU_TANH 3 /* 0.5 z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3)))   */
+
+/* Linear layer with its epilogue:
+ *   z = x W^T + b,  y = act(z) + r
+ * or, with 8-bit operands, z[p][j] = (x W^T)[p][j] * x_scale[p] * w_scale[j] + b[j].
+ * Products are exact, sums are fp32; y (and pre) are rounded once, to nearest
+ * even.  m == 0 does nothing.  y may be r itself (same stride). */
+typedef struct {
+    int64_t m;             /* rows, >= 0                                              */
+    int32_t k, n;          /* inputs and outputs of the layer, 1..65536               */
+    const void *x;         /* [m][k] of x_dtype                                       */
+    int64_t x_stride;      /* >= k                                                    */
+    const void *w;         /* [n][k] of x_dtype (nn.Linear layout)                    */
+    int64_t w_stride;      /* >= k                                                    */
+    const float *x_scale;  /* [m], HG_F8 only (else NULL)                             */
+    const float *w_scale;  /* [n], HG_F8 only (else NULL)                             */
+    const float *bias;     /* [n] or NULL                                             */
+    const void *residual;  /* r: [m][n] of y_dtype, or NULL                           */
+    int64_t residual_stride;
+    void *y;               /* [m][n] of y_dtype, WRITTEN                              */
+    int64_t y_stride;
+    void *pre;             /* NULL, or [m][n] of x_dtype that receives z for the
+                              backward (HG_F16 and HG_BF16 only)                      */
+    int64_t pre_stride;
+    int32_t x_dtype;       /* HG_F16, HG_BF16 or HG_F8                                */
+    int32_t y_dtype;       /* x_dtype or HG_F32; with HG_F8: HG_F16, HG_BF16, HG_F32  */
+    int32_t act;           /* HG_ACT_*                                                */
+} hg_linear;
+/* Errors: HG_EINVAL (NULL, size, stride, alignment, act), HG_EUNSUPPORTED (a
+ * combination of types that is not listed), HG_EHIP. */
+int hashgrid_linear_forward(const hg_linear *op, void *stream);
+
+/* Backward of hashgrid_linear_forward for upstream dy = dL/dy:
+ *   dz = dy act'(z),  dx = dz W,  dw = dz^T x,  db = sum over rows of dz
+ * (the residual's gradient is dy itself).  dz is rounded to the operands' type
+ * where it enters a product; db sums it unrounded; sums are fp32, outputs are
+ * rounded once.  Where act' is 0 (ReLU below zero) dz is 0 whatever dy holds.
+ * dw and db are WRITTEN, or added to their old values with accumulate; with
+ * m == 0 they are zero (or unchanged).  The order of every sum is fixed by the
+ * sizes: results do not depend on scheduling. */
+typedef struct {
+    int64_t m;
+    int32_t k, n;
+    const void *dy;        /* [m][n] of dy_dtype                                      */
+    int64_t dy_stride;
+    const void *pre;       /* [m][n] of dtype: z as the forward left it (for ReLU, y
+                              without a residual serves too); NULL with HG_ACT_NONE   */
+    int64_t pre_stride;
+    const void *x;         /* [m][k] of dtype (needed for dw)                         */
+    int64_t x_stride;
+    const void *w;         /* [n][k] of dtype (needed for dx)                         */
+    int64_t w_stride;
+    void *dx;              /* NULL, or [m][k] of dtype, WRITTEN                       */
+    int64_t dx_stride;
+    void *dw;              /* NULL, or [n][k] of dw_dtype                             */
+    int64_t dw_stride;
+    float *db;             /* NULL, or [n]                                            */
+    int32_t dtype;         /* HG_F16 or HG_BF16                                       */
+    int32_t dy_dtype;      /* dtype or HG_F32                                         */
+    int32_t dw_dtype;      /* dtype or HG_F32                                         */
+    int32_t act;           /* HG_ACT_*                                                */
+    int32_t accumulate;    /* 1: add to dw and db                                     */
+} hg_linear_grad;
+/* Bytes of device workspace hashgrid_linear_backward needs (*bytes_out is a
+ * HOST size_t; 0 is possible, the workspace is then not looked at). */
+int hashgrid_linear_backward_workspace_size(const hg_linear_grad *op, size_t *bytes_out);
+/* workspace: 256-byte aligned, contents clobbered; concurrent calls must not
+ * share one.  Errors: as hashgrid_linear_forward, and HG_EINVAL for too small a
+ * workspace. */
+int hashgrid_linear_backward(const hg_linear_grad *op, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Root-mean-square norm with the residual's addition:
+ *   s = x + r,  q = 1 / sqrt(mean over the row of s^2 + eps),  y = s q w
+ * in fp32 between the loads and each output's one rounding (y is made from the
+ * unrounded s).  With y_dtype HG_F8 each row has a scale, y_scale = max |s q w|
+ * / 448, and y holds s q w / y_scale rounded to nearest even: the 8-bit operand
+ * and x_scale of hashgrid_linear_forward.  A row of zeros has scale 0; a row
+ * with a NaN has scale NaN.  y and sum may be x or r themselves (same stride
+ * and type). */
+typedef struct {
+    int64_t m;             /* rows, >= 0                                              */
+    int32_t c;             /* columns, 1..2^20                                        */
+    const void *x;         /* [m][c] of dtype                                         */
+    int64_t x_stride;
+    const void *residual;  /* r: [m][c] of dtype, or NULL                             */
+    int64_t residual_stride;
+    const float *w;        /* [c]                                                     */
+    void *y;               /* [m][c] of y_dtype, WRITTEN                              */
+    int64_t y_stride;
+    float *y_scale;        /* [m], HG_F8 only (else NULL), WRITTEN                    */
+    void *sum;             /* NULL, or [m][c] of dtype that receives s                */
+    int64_t sum_stride;
+    float *rstd;           /* NULL, or [m] that receives q                            */
+    float eps;             /* >= 0                                                    */
+    int32_t dtype;         /* HG_F32, HG_F16 or HG_BF16                               */
+    int32_t y_dtype;       /* dtype or HG_F8                                          */
+} hg_rms_norm;
+int hashgrid_rms_norm_forward(const hg_rms_norm *op, void *stream);
+
+/* Backward of the norm for upstream dy = dL/dy and, where s goes on as the
+ * residual stream, ds = dL/ds:
+ *   dx = q (w dy - h mean(w dy h)) + ds,  h = s q,  dw = sum over rows of dy h
+ * dx is the gradient of x and of r alike.  dw is WRITTEN, or added to with
+ * accumulate (zero or unchanged with m == 0); its order of summation is fixed by
+ * the sizes.  dx may be dy, s or ds itself (same stride) for c <= 4096. */
+typedef struct {
+    int64_t m;
+    int32_t c;
+    const void *dy;        /* [m][c] of dtype                                         */
+    int64_t dy_stride;
+    const void *sum;       /* s: [m][c] of dtype                                      */
+    int64_t sum_stride;
+    const float *w;        /* [c]                                                     */
+    const float *rstd;     /* q: [m]                                                  */
+    const void *ds;        /* NULL, or [m][c] of dtype                                */
+    int64_t ds_stride;
+    void *dx;              /* [m][c] of dtype, WRITTEN                                */
+    int64_t dx_stride;
+    float *dw;             /* NULL, or [c]                                            */
+    int32_t dtype;         /* HG_F32, HG_F16 or HG_BF16                               */
+    int32_t accumulate;    /* 1: add to dw                                            */
+} hg_rms_norm_grad;
+int hashgrid_rms_norm_backward_workspace_size(const hg_rms_norm_grad *op, size_t *bytes_out);
+int hashgrid_rms_norm_backward(const hg_rms_norm_grad *op, void *workspace, size_t workspace_bytes, void *stream);
+
+/* AdamW over many tensors at once (Adam's moments, Kingma and Ba 2015; the
+ * decay beside the gradient, Loshchilov and Hutter 2019):
+ *   m = b1 m + (1 - b1) g,  v = b2 v + (1 - b2) g^2
+ *   p = p (1 - lr wd) - lr / (1 - b1^t) m / (sqrt(v) / sqrt(1 - b2^t) + eps)
+ * in fp32 for every entry.  The pages give the hash tables no weight decay and
+ * a rate 5 to 10 times the head's (ipipp.com sections 3 and 4): lr and
+ * weight_decay are each tensor's own.
+ *
+ * state_bits 8 keeps the moments in 8 bits.  256 consecutive values (the last
+ * block of a tensor may be shorter) share a power of two 2^(e - 127), the byte
+ * e of m_exp or v_exp; a value over it is a small float:
+ *   m: sign, 4 exponent bits (bias 7), 3 mantissa bits (HG_F8's values)
+ *   v: no sign, 5 exponent bits (bias 15), 3 mantissa bits; exponent field 0 is
+ *      gradual underflow, as in m, and every other code is a finite value
+ * A block's largest |m| over its power of two lies in [2^7, 2^8), its largest v
+ * in [2^15, 2^16).  Both are rounded stochastically, by noise from `seed`, the
+ * tensor's place in the list and the value's place in the tensor; a v above
+ * zero keeps a code of at least 1.  Codes and exponents of zero are moments of
+ * zero, ready for step 1.  A gradient that is not finite makes its own entry
+ * not finite, and with 8 bits the moments of its block NaN (exponent 255). */
+typedef struct {
+    float *param;          /* [count], 4-byte aligned, UPDATED                        */
+    void *grad;            /* [count] of grad_dtype                                   */
+    void *m, *v;           /* [count] moments: fp32, or 8-bit codes                   */
+    uint8_t *m_exp, *v_exp;/* [ceil(count / 256)] with state_bits 8 (else NULL)       */
+    void *copy;            /* NULL, or [count] of copy_dtype: param rounded           */
+    int64_t count;         /* >= 0                                                    */
+    float lr, weight_decay;/* finite; weight_decay >= 0                               */
+    int32_t grad_dtype;    /* HG_F32, HG_F16 or HG_BF16                               */
+    int32_t copy_dtype;    /* HG_F16 or HG_BF16 (with a copy)                         */
+    int32_t state_bits;    /* 32 or 8                                                 */
+    int32_t reserved;      /* 0                                                       */
+} hg_adamw_tensor;
+typedef struct {
+    float beta1, beta2;    /* in [0, 1)                                               */
+    float eps;             /* >= 0                                                    */
+    int32_t step;          /* t >= 1                                                  */
+    uint32_t seed;         /* of the rounding noise: another one each step            */
+} hg_adamw;
+/*   tensors    : HOST array of n descriptions, read before the call returns;
+ *                the tensors must not overlap.
+ *   grad_scale : NULL, or a DEVICE fp32 that every gradient is multiplied by
+ *                first (loss unscaling, norm clipping); when it is not finite
+ *                the step changes nothing.
+ *   flags      : HG_ADAM_ZERO_GRAD clears the gradients.
+ * One launch takes 36 tensors of one state_bits.  Errors: HG_EINVAL, HG_EHIP. */
+int hashgrid_adamw_step(const hg_adamw *opt, const hg_adamw_tensor *tensors, int32_t n, const float *grad_scale,
+                        int32_t flags, void *stream);
 
 /* Performance knobs (launch shapes).  Two change results within rounding:
  * HG_TUNE_FWD_LANES (the order in which the blend's eight terms are added) and

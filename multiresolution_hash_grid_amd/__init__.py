@@ -32,3 +32,13 @@ from .hashgrid import (  # noqa: F401
     hashgrid_tune_get,
     load_library,
 )
+from .residual import (  # noqa: F401
+    AdamWTensor,
+    HashGridAdamWPlan,
+    RmsNormOutput,
+    hashgrid_adamw_step,
+    hashgrid_linear_backward,
+    hashgrid_linear_forward,
+    hashgrid_rms_norm_backward,
+    hashgrid_rms_norm_forward,
+)

@@ -36,7 +36,7 @@ COMMON = ["-O3", "-fPIC", "-std=c++20", f"--offload-arch={ARCH}", "-Wall", "-Wno
 
 
 def sources() -> list[str]:
-    return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".hip", ".cpp")))
+    return sorted(os.path.join(d, f) for d, _, files in os.walk(CSRC) for f in files if f.endswith((".hip", ".cpp")))
 
 
 def _compile(src: str) -> str:

@@ -17,14 +17,19 @@ namespace {
 
 thread_local std::string g_last_error;
 
-int fail(int code, const char *fmt, ...) {
+int vfail(int code, const char *fmt, va_list ap) {
     char buf[512];
-    va_list ap;
-    va_start(ap, fmt);
     vsnprintf(buf, sizeof buf, fmt, ap);
-    va_end(ap);
     g_last_error = buf;
     return code;
+}
+
+int fail(int code, const char *fmt, ...) {
+    va_list ap;
+    va_start(ap, fmt);
+    const int rc = vfail(code, fmt, ap);
+    va_end(ap);
+    return rc;
 }
 
 int ok() {
@@ -369,6 +374,18 @@ hg::MlpParams mlp_params(const hg_mlp_params *mp) {
 }
 
 }  // namespace
+
+// The same for the entry points of other files (csrc/residual/).
+namespace hg {
+int abi_fail(int code, const char *fmt, ...) {
+    va_list ap;
+    va_start(ap, fmt);
+    const int rc = vfail(code, fmt, ap);
+    va_end(ap);
+    return rc;
+}
+int abi_ok() { return ok(); }
+}  // namespace hg
 
 extern "C" {
 

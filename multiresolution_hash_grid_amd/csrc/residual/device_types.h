@@ -1,0 +1,135 @@
+// Element types and lane helpers of the residual head's kernels (gfx950).
+#pragma once
+
+#include "residual_internal.h"
+
+namespace hg {
+namespace res {
+
+typedef _Float16 f16;
+typedef __bf16 bf16;
+struct f8 {  // OCP e4m3: 4 exponent bits (bias 7), 3 mantissa bits, largest value 448
+    uint8_t bits;
+};
+
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+
+// Vectors at any alignment the element type allows: global memory takes wide
+// accesses at every address here, so rows of odd strides load as wide as
+// aligned ones.
+template <typename V>
+struct __attribute__((packed, aligned(1))) Loose {
+    V v;
+};
+template <typename V>
+__device__ __forceinline__ V load_loose(const void *p) {
+    return reinterpret_cast<const Loose<V> *>(p)->v;
+}
+template <typename V>
+__device__ __forceinline__ void store_loose(void *p, V v) {
+    reinterpret_cast<Loose<V> *>(p)->v = v;
+}
+
+// 8 consecutive elements at p as floats; only the first `left` exist (the
+// others read as zero and are not touched).
+template <typename T>
+__device__ __forceinline__ void load8(const T *p, int left, float (&v)[8]) {
+    if constexpr (sizeof(T) == 2) {
+        typedef T T8 __attribute__((ext_vector_type(8)));
+        if (left >= 8) {
+            const T8 a = load_loose<T8>(p);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = (float)a[j];
+            return;
+        }
+    } else {
+        if (left >= 8) {
+            const f32x4 a = load_loose<f32x4>(p), b = load_loose<f32x4>(p + 4);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = a[j], v[4 + j] = b[j];
+            return;
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        v[j] = 0.f;
+        if (j < left) v[j] = (float)p[j];
+    }
+}
+
+// Stores the first `left` of 8 values, each rounded to nearest even.
+template <typename T>
+__device__ __forceinline__ void store8(T *p, int left, const float (&v)[8]) {
+    if constexpr (sizeof(T) == 2) {
+        typedef T T8 __attribute__((ext_vector_type(8)));
+        T8 a;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) a[j] = (T)v[j];
+        if (left >= 8) {
+            store_loose<T8>(p, a);
+            return;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j < left) p[j] = a[j];
+    } else if constexpr (sizeof(T) == 4) {
+        if (left >= 8) {
+            store_loose<f32x4>(p, f32x4{v[0], v[1], v[2], v[3]});
+            store_loose<f32x4>(p + 4, f32x4{v[4], v[5], v[6], v[7]});
+            return;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j < left) p[j] = v[j];
+    } else {
+        int lo = 0, hi = 0;
+        lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], lo, false);
+        lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], lo, true);
+        hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[4], v[5], hi, false);
+        hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[6], v[7], hi, true);
+        if (left >= 8) {
+            store_loose<u32x2>(p, u32x2{(uint32_t)lo, (uint32_t)hi});
+            return;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j < left) p[j].bits = (uint8_t)((j < 4 ? lo : hi) >> (8 * (j & 3)));
+    }
+}
+
+// Sum over aligned groups of G lanes, in every lane of the group.
+template <int G>
+__device__ __forceinline__ float group_sum(float v) {
+#pragma unroll
+    for (int o = 1; o < G; o <<= 1) v += __shfl_xor(v, o, 64);
+    return v;
+}
+template <int G>
+__device__ __forceinline__ float group_max(float v) {
+#pragma unroll
+    for (int o = 1; o < G; o <<= 1) v = fmaxf(v, __shfl_xor(v, o, 64));
+    return v;
+}
+
+// Largest of 64 lanes' words, in a scalar register: four steps within rows of
+// 16 lanes, two row broadcasts, lane 63.
+__device__ __forceinline__ uint32_t wave_max_u32(uint32_t x) {
+    auto step = [&](auto ctrl, auto rows) {
+        const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp((int)x, (int)x, ctrl.value, rows.value, 0xF, false);
+        x = o > x ? o : x;
+    };
+    step(std::integral_constant<int, 0xB1>{}, std::integral_constant<int, 0xF>{});   // lane ^ 1
+    step(std::integral_constant<int, 0x4E>{}, std::integral_constant<int, 0xF>{});   // lane ^ 2
+    step(std::integral_constant<int, 0x141>{}, std::integral_constant<int, 0xF>{});  // mirrored half rows
+    step(std::integral_constant<int, 0x140>{}, std::integral_constant<int, 0xF>{});  // mirrored rows
+    step(std::integral_constant<int, 0x142>{}, std::integral_constant<int, 0xA>{});  // row 0 -> 1, row 2 -> 3
+    step(std::integral_constant<int, 0x143>{}, std::integral_constant<int, 0xC>{});  // row 1 -> 2 and 3
+    return (uint32_t)__builtin_amdgcn_readlane((int)x, 63);
+}
+
+}  // namespace res
+}  // namespace hg

@@ -1,0 +1,116 @@
+// What the linear kernels share: matrix-core fragments, the activations and
+// their slopes, and the upstream gradient through the activation.
+//
+// A fragment is 16 bytes a lane: lane l holds, of row l % 16 of its operand,
+// the 16-byte piece l / 16 of a 64-byte stretch of the contraction (32 binary16
+// or bfloat16 values, 64 8-bit ones).  Both operands cut the stretch alike, so
+// the order inside it does not matter.
+#pragma once
+
+#include "device_types.h"
+
+namespace hg {
+namespace res {
+
+typedef f16 f16x8 __attribute__((ext_vector_type(8)));
+typedef bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+template <typename T>
+constexpr int kStretch = 64 / (int)sizeof(T);  // elements of a row in a fragment step
+template <typename T>
+constexpr int kPiece = 16 / (int)sizeof(T);    // elements of a lane
+
+// 16 8-bit values as binary16, which holds every one of them exactly.  The
+// matrix cores' own 8-bit products sum with the smaller terms cut at about
+// 2^-14 of a step's largest (measured: errors up to 9e-5 of sum |x w|, both for
+// the 32- and the 128-deep instruction), so 8-bit operands are widened where
+// they enter a product and their sums are fp32 like the others'.
+struct Widened {
+    f16x8 lo, hi;
+};
+__device__ __forceinline__ Widened widen(u32x4 v) {
+    Widened w;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const auto a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(v[i], 1.f, false), b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(v[i], 1.f, true);
+        const auto c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(v[2 + i], 1.f, false), d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(v[2 + i], 1.f, true);
+        w.lo[4 * i] = a[0], w.lo[4 * i + 1] = a[1], w.lo[4 * i + 2] = b[0], w.lo[4 * i + 3] = b[1];
+        w.hi[4 * i] = c[0], w.hi[4 * i + 1] = c[1], w.hi[4 * i + 2] = d[0], w.hi[4 * i + 3] = d[1];
+    }
+    return w;
+}
+
+// acc[r] += sum_k a[row = 4 (lane / 16) + r][k] b[row = lane % 16][k], fp32 sums.
+template <typename T>
+__device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 acc) {
+    if constexpr (sizeof(T) == 1) {
+        const Widened x = widen(a), y = widen(b);
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(x.lo, y.lo, acc, 0, 0, 0);
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(x.hi, y.hi, acc, 0, 0, 0);
+    } else if constexpr (__is_same(T, f16)) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), acc, 0, 0, 0);
+    } else {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), acc, 0, 0, 0);
+    }
+}
+
+// The 16-byte piece at p of a row that has `left` more elements; what lies
+// past them is zero and is not touched.
+template <typename T>
+__device__ __forceinline__ u32x4 load_piece(const T *p, int left) {
+    if (left >= kPiece<T>) return load_loose<u32x4>(p);
+    u32x4 v = {0, 0, 0, 0};
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j < left) v[j / 2] |= (uint32_t)__builtin_bit_cast(uint16_t, p[j]) << (16 * (j & 1));
+    } else {
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+            if (j < left) v[j / 4] |= (uint32_t)p[j].bits << (8 * (j & 3));
+    }
+    return v;
+}
+
+// Logistic function; exp2 overflows to infinity for very negative z, whose
+// reciprocal is the right 0.
+__device__ __forceinline__ float logistic(float z) {
+    return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504f * z));
+}
+
+// act(z).  GELU is the tanh form: 0.5 z (1 + tanh u) = z logistic(2 u), with
+// u = sqrt(2 / pi) (z + 0.044715 z^3).  -inf gives 0 in both, as the limit has it.
+__device__ __forceinline__ float activate(float z, int act) {
+    if (act == HG_ACT_RELU) return z > 0.f ? z : z != z ? z : 0.f;
+    if (act == HG_ACT_SILU || act == HG_ACT_GELU_TANH) {
+        const float u = act == HG_ACT_SILU ? z : 1.59576912f * z * fmaf(0.044715f * z, z, 1.f);
+        return z == -__builtin_inff() ? 0.f : z * logistic(u);
+    }
+    return z;
+}
+
+// d act / dz.
+__device__ __forceinline__ float slope(float z, int act) {
+    if (act == HG_ACT_RELU) return z > 0.f ? 1.f : z != z ? z : 0.f;
+    if (act == HG_ACT_SILU) {
+        const float p = logistic(z), q = z * p * (1.f - p);
+        return __builtin_isinf(z) ? p : p + q;
+    }
+    if (act == HG_ACT_GELU_TANH) {
+        const float p = logistic(1.59576912f * z * fmaf(0.044715f * z, z, 1.f));
+        const float q = z * p * (1.f - p) * 1.59576912f * fmaf(0.134145f * z, z, 1.f);
+        return p == 0.f || p == 1.f ? p : p + q;
+    }
+    return 1.f;
+}
+
+struct FwdArgs {
+    int64_t m, xs, ws, rs, ys, ps;
+    int k, n, act;
+    const void *x, *w, *r;
+    const float *x_scale, *w_scale, *bias;
+    void *y, *pre;
+};
+
+}  // namespace res
+}  // namespace hg

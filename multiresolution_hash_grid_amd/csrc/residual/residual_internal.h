@@ -1,0 +1,38 @@
+// Launch descriptions of the residual head's operators (linear, RMS norm,
+// AdamW), shared by their host side and their kernels.  Not part of the
+// public ABI (include/hashgrid.h is).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "hashgrid.h"
+
+namespace hg {
+
+// Error text and return code of the C entry points (defined with the
+// encoder's entry points, so that hashgrid_last_error covers both).
+int abi_fail(int code, const char *fmt, ...);
+int abi_ok();
+
+namespace res {
+
+constexpr int kCus = 256;  // MI355X: 8 XCDs of 32 CUs
+
+inline int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+hipError_t launch_linear_forward(const hg_linear &op, hipStream_t stream);
+size_t linear_backward_bytes(const hg_linear_grad &op);
+hipError_t launch_linear_backward(const hg_linear_grad &op, void *workspace, hipStream_t stream);
+
+hipError_t launch_rms_norm_forward(const hg_rms_norm &op, hipStream_t stream);
+size_t rms_norm_backward_bytes(const hg_rms_norm_grad &op);
+hipError_t launch_rms_norm_backward(const hg_rms_norm_grad &op, void *workspace, hipStream_t stream);
+
+// Tensors per launch: their descriptions travel in the kernel's arguments.
+constexpr int kAdamwTensors = 36;
+hipError_t launch_adamw(const hg_adamw &opt, const hg_adamw_tensor *tensors, int32_t n, const float *grad_scale,
+                        bool zero_grad, hipStream_t stream);
+
+}  // namespace res
+}  // namespace hg
