@@ -40,18 +40,36 @@ __device__ __forceinline__ Widened widen(u32x4 v) {
     return w;
 }
 
+// A fragment ready for the matrix cores.
+template <typename T>
+struct Ready {
+    u32x4 v;
+};
+template <>
+struct Ready<f8> {
+    Widened v;
+};
+template <typename T>
+__device__ __forceinline__ Ready<T> ready(u32x4 v) {
+    if constexpr (sizeof(T) == 1) return {widen(v)};
+    else return {v};
+}
+
 // acc[r] += sum_k a[row = 4 (lane / 16) + r][k] b[row = lane % 16][k], fp32 sums.
 template <typename T>
-__device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 acc) {
+__device__ __forceinline__ f32x4 mma(Ready<T> a, Ready<T> b, f32x4 acc) {
     if constexpr (sizeof(T) == 1) {
-        const Widened x = widen(a), y = widen(b);
-        acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(x.lo, y.lo, acc, 0, 0, 0);
-        return __builtin_amdgcn_mfma_f32_16x16x32_f16(x.hi, y.hi, acc, 0, 0, 0);
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(a.v.lo, b.v.lo, acc, 0, 0, 0);
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(a.v.hi, b.v.hi, acc, 0, 0, 0);
     } else if constexpr (__is_same(T, f16)) {
-        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), acc, 0, 0, 0);
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a.v), __builtin_bit_cast(f16x8, b.v), acc, 0, 0, 0);
     } else {
-        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), acc, 0, 0, 0);
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a.v), __builtin_bit_cast(bf16x8, b.v), acc, 0, 0, 0);
     }
+}
+template <typename T>
+__device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 acc) {
+    return mma<T>(ready<T>(a), ready<T>(b), acc);
 }
 
 // The 16-byte piece at p of a row that has `left` more elements; what lies
@@ -72,6 +90,30 @@ __device__ __forceinline__ u32x4 load_piece(const T *p, int left) {
     return v;
 }
 
+// A row cut into pieces without branches, for rows of at least a piece: the
+// last piece of a row whose length is no multiple of a piece is read so that
+// it ends with the row, and what belongs to the piece before it (or, for
+// pieces past the row, all of it) is masked to zero.  Both operands are cut
+// alike, so products meet their partners.
+template <typename T>
+struct Cut {
+    int64_t at;   // first element of the piece as it is read
+    u32x4 mask;
+};
+template <typename T>
+__device__ __forceinline__ Cut<T> cut_piece(int k, int length) {
+    const int have = length - k < 0 ? 0 : length - k < kPiece<T> ? length - k : kPiece<T>;
+    Cut<T> c;
+    c.at = have == kPiece<T> ? k : length - kPiece<T>;
+    const int drop = (kPiece<T> - have) * (int)sizeof(T);  // bytes at the front
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int b = drop - 4 * j;
+        c.mask[j] = b >= 4 ? 0u : b <= 0 ? ~0u : ~0u << (8 * b);
+    }
+    return c;
+}
+
 // Logistic function; exp2 overflows to infinity for very negative z, whose
 // reciprocal is the right 0.
 __device__ __forceinline__ float logistic(float z) {
@@ -87,6 +129,20 @@ __device__ __forceinline__ float activate(float z, int act) {
         return z == -__builtin_inff() ? 0.f : z * logistic(u);
     }
     return z;
+}
+
+// Several of them behind one branch.
+template <int N>
+__device__ __forceinline__ void activate_all(float (&z)[N], int act) {
+    if (act == HG_ACT_RELU)
+#pragma unroll
+        for (int j = 0; j < N; ++j) z[j] = activate(z[j], HG_ACT_RELU);
+    else if (act == HG_ACT_SILU)
+#pragma unroll
+        for (int j = 0; j < N; ++j) z[j] = activate(z[j], HG_ACT_SILU);
+    else if (act == HG_ACT_GELU_TANH)
+#pragma unroll
+        for (int j = 0; j < N; ++j) z[j] = activate(z[j], HG_ACT_GELU_TANH);
 }
 
 // d act / dz.
@@ -111,6 +167,9 @@ struct FwdArgs {
     const float *x_scale, *w_scale, *bias;
     void *y, *pre;
 };
+hipError_t linear_f16(const FwdArgs &a, int y_dtype, hipStream_t stream);
+hipError_t linear_bf16(const FwdArgs &a, int y_dtype, hipStream_t stream);
+hipError_t linear_f8(const FwdArgs &a, int y_dtype, hipStream_t stream);
 
 }  // namespace res
 }  // namespace hg

@@ -1,0 +1,230 @@
+// Kernels of y = act(x W^T + b) + r for one pair of types; the sources that
+// include this instantiate one operand type each, so that they build at once.
+#pragma once
+
+#include "linear_common.h"
+
+namespace hg {
+namespace res {
+namespace {
+
+// Few rows.  A workgroup computes 16 rows by 16 outputs; its four waves share
+// the contraction and add their sums in LDS.  Both operands come straight from
+// memory as fragments.
+template <typename T, typename Y>
+__global__ __launch_bounds__(256) void linear_tile_kernel(const FwdArgs a) {
+    __shared__ f32x4 sums[4][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t m0 = (int64_t)blockIdx.y * 16;
+    const int n0 = blockIdx.x * 16;
+    const int64_t xm = m0 + (lane & 15) < a.m ? m0 + (lane & 15) : a.m - 1;
+    const int wn = n0 + (lane & 15) < a.n ? n0 + (lane & 15) : a.n - 1;
+    const T *x = (const T *)a.x + xm * a.xs, *w = (const T *)a.w + (int64_t)wn * a.ws;
+    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+    for (int k = wave * kStretch<T> + (lane >> 4) * kPiece<T>; k - (lane >> 4) * kPiece<T> < a.k; k += 4 * kStretch<T>)
+        acc = mma<T>(load_piece(w + k, a.k - k), load_piece(x + k, a.k - k), acc);
+    sums[wave][lane] = acc;
+    __syncthreads();
+    // thread t: row t / 16, output t % 16; it lies in lane (output / 4) * 16 + row, word output % 4
+    const int row = threadIdx.x >> 4, col = threadIdx.x & 15;
+    const int64_t m = m0 + row;
+    const int n = n0 + col;
+    if (m >= a.m || n >= a.n) return;
+    float z = 0.f;
+    for (int i = 0; i < 4; ++i) z += sums[i][(col >> 2) * 16 + row][col & 3];
+    if constexpr (sizeof(T) == 1) z = z * a.x_scale[m] * a.w_scale[n];
+    if (a.bias) z += a.bias[n];
+    if constexpr (sizeof(T) == 2)
+        if (a.pre) ((T *)a.pre)[m * a.ps + n] = (T)z;
+    float y = activate(z, a.act);
+    if (a.r) y += (float)((const Y *)a.r)[m * a.rs + n];
+    ((Y *)a.y)[m * a.ys + n] = (Y)y;
+}
+
+// Many rows, a weight that fits LDS in a few slices.  A workgroup keeps its
+// slice of W in LDS for good, in fragment order (a wave reads 1 KB in a row,
+// without conflicts), and its waves walk row tiles of RF * 16 rows on their
+// own: a tile's rows go straight from memory into registers as fragments, all
+// of the contraction at once, and each set of FR 16-output fragments is finished
+// -- bias, activation, residual, rounding -- before the next is begun.  No
+// barrier after the start: the waves of a CU hide each other's loads.
+// A set's outputs are dealt so that a lane has 4 * FR consecutive ones of one row:
+// row i of fragment h is output (i / 4) * 4 * FR + h * 4 + i % 4 of the set.
+// Slices of W are workgroups next to each other on one XCD that walk the same
+// rows, so x comes from HBM once.
+// kCut: 0 the contraction is whole fragments; 1 its last fragment is cut; 2 it
+// is shorter than a piece.
+template <typename T, typename Y, int KU, int RF, int WAVES, int FR, int kCut>
+__global__ __launch_bounds__(WAVES * 64) void linear_stream_kernel(const FwdArgs a, int slices, int slice_n) {
+    extern __shared__ __attribute__((aligned(16))) char lds[];
+    u32x4 *const wl = (u32x4 *)lds;
+    constexpr int kOut = 4 * FR;  // outputs of a lane in a set
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, row16 = lane & 15, group = lane >> 4;
+    // workgroups b, b + 8, b + 16, ... share an XCD
+    const int xcd = blockIdx.x & 7, in_xcd = blockIdx.x >> 3;
+    const int n0 = (in_xcd % slices) * slice_n;
+    const int walkers = (gridDim.x >> 3) / slices * 8, walker = in_xcd / slices * 8 + xcd;
+    const int nn = a.n - n0 < slice_n ? a.n - n0 : slice_n;
+    const int sets = (nn + 16 * FR - 1) / (16 * FR);
+    float *const bias = (float *)(lds + (size_t)(slice_n / 16) * KU * 1024), *const wsc = bias + slice_n;
+
+    // The last fragment's piece of this lane.
+    const Cut<T> last = cut_piece<T>((KU - 1) * kStretch<T> + group * kPiece<T>, a.k);
+    auto piece = [&](const T *row, int u) -> u32x4 {
+        if constexpr (kCut == 2) return load_piece(row + group * kPiece<T>, a.k - group * kPiece<T>);
+        if (kCut == 1 && u == KU - 1) return load_loose<u32x4>(row + last.at) & last.mask;
+        return load_loose<u32x4>(row + group * kPiece<T> + u * kStretch<T>);
+    };
+
+    for (int b = wave; b < sets * FR; b += WAVES) {
+        const int f = b % FR, s = b / FR;
+        const int n = s * 16 * FR + (row16 >> 2) * kOut + f * 4 + (row16 & 3);
+        const T *w = (const T *)a.w + (int64_t)(n0 + (n < nn ? n : nn - 1)) * a.ws;
+#pragma unroll
+        for (int u = 0; u < KU; ++u) wl[(b * KU + u) * 64 + lane] = piece(w, u);
+    }
+    for (int n = threadIdx.x; n < slice_n; n += WAVES * 64) {
+        bias[n] = a.bias && n < nn ? a.bias[n0 + n] : 0.f;
+        if constexpr (sizeof(T) == 1) wsc[n] = n < nn ? a.w_scale[n0 + n] : 0.f;
+    }
+    __syncthreads();
+
+    const int64_t tiles = (a.m + RF * 16 - 1) / (RF * 16);
+    for (int64_t tile = (int64_t)wave * walkers + walker; tile < tiles; tile += (int64_t)WAVES * walkers) {
+        const int64_t m0 = tile * (RF * 16) + row16;
+        Ready<T> x[RF][KU];
+        float xsc[RF];
+#pragma unroll
+        for (int r = 0; r < RF; ++r) {
+            const int64_t m = m0 + r * 16 < a.m ? m0 + r * 16 : a.m - 1;
+            const T *p = (const T *)a.x + m * a.xs;
+#pragma unroll
+            for (int u = 0; u < KU; ++u) x[r][u] = ready<T>(piece(p, u));
+            if constexpr (sizeof(T) == 1) xsc[r] = a.x_scale[m];
+        }
+        for (int s = 0; s < sets; ++s) {
+            f32x4 acc[FR][RF];
+#pragma unroll
+            for (int f = 0; f < FR; ++f)
+#pragma unroll
+                for (int r = 0; r < RF; ++r) acc[f][r] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int u = 0; u < KU; ++u)
+#pragma unroll
+                for (int f = 0; f < FR; ++f) {
+                    const Ready<T> w = ready<T>(wl[((s * FR + f) * KU + u) * 64 + lane]);
+#pragma unroll
+                    for (int r = 0; r < RF; ++r) acc[f][r] = mma<T>(w, x[r][u], acc[f][r]);
+                }
+            const int n = s * 16 * FR + group * kOut, left = nn - n;
+            float bs[kOut], ws[kOut];
+#pragma unroll
+            for (int j = 0; j < kOut; ++j) {
+                bs[j] = bias[n + j];
+                if constexpr (sizeof(T) == 1) ws[j] = wsc[n + j];
+            }
+#pragma unroll
+            for (int r = 0; r < RF; ++r) {
+                const int64_t m = m0 + r * 16;
+                if (m >= a.m) continue;
+                float z[kOut], res[kOut];
+                if (a.r) load_some<kOut>((const Y *)a.r + m * a.rs + n0 + n, left, res);
+#pragma unroll
+                for (int j = 0; j < kOut; ++j) {
+                    z[j] = acc[j / 4][r][j % 4];
+                    if constexpr (sizeof(T) == 1) z[j] = z[j] * xsc[r] * ws[j];
+                    z[j] += bs[j];
+                }
+                if constexpr (sizeof(T) == 2)
+                    if (a.pre) store_some<kOut>((T *)a.pre + m * a.ps + n0 + n, left, z);
+                activate_all(z, a.act);
+                if (a.r)
+#pragma unroll
+                    for (int j = 0; j < kOut; ++j) z[j] += res[j];
+                store_some<kOut>((Y *)a.y + m * a.ys + n0 + n, left, z);
+            }
+        }
+    }
+}
+
+constexpr int kLdsBytes = 160 * 1024;
+
+template <typename T, typename Y, int KU, int RF, int WAVES, int FR, int kCut>
+hipError_t stream_launch(const FwdArgs &a, int slices, int slice_n, hipStream_t stream) {
+    const auto kernel = linear_stream_kernel<T, Y, KU, RF, WAVES, FR, kCut>;
+    const size_t bytes = (size_t)(slice_n / 16) * KU * 1024 + (size_t)slice_n * 8;
+    if (bytes > 65536) {
+        const hipError_t e = hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+        if (e != hipSuccess) return e;
+    }
+    const int64_t tiles = div_up(a.m, RF * 16);
+    int64_t walkers = kCus / slices;  // workgroups that share the rows
+    if (walkers > tiles) walkers = tiles;
+    walkers = div_up(walkers, 8) * 8;
+    kernel<<<dim3((unsigned)(walkers * slices)), WAVES * 64, bytes, stream>>>(a, slices, slice_n);
+    return hipGetLastError();
+}
+
+template <typename T, typename Y, int KU, int RF, int WAVES, int kCut>
+hipError_t stream_slices(const FwdArgs &a, hipStream_t stream) {
+    if (a.n <= 16) return stream_launch<T, Y, KU, RF, WAVES, 1, kCut>(a, 1, 16, stream);
+    const int fit = (kLdsBytes - 8192) / (KU * 64 + 8) / 32 * 32;  // outputs whose weights fit LDS
+    int slices = (int)div_up(a.n, fit);
+    const int slice_n = (int)div_up(div_up(a.n, slices), 32) * 32;
+    slices = (int)div_up(a.n, slice_n);
+    return stream_launch<T, Y, KU, RF, WAVES, 2, kCut>(a, slices, slice_n, stream);
+}
+
+// hipErrorNotSupported: not a case of this kernel.
+template <typename T, typename Y>
+hipError_t run_stream(const FwdArgs &a, hipStream_t stream) {
+    constexpr int W = sizeof(T) == 1 ? 8 : 16;
+    if (a.k < kPiece<T>) return stream_slices<T, Y, 1, 2, W, 2>(a, stream);
+    const bool cut = a.k % kStretch<T> != 0;
+    switch (div_up(a.k, kStretch<T>)) {
+#define HG_STREAM(KU, RF) \
+    case KU: return cut ? stream_slices<T, Y, KU, RF, W, 1>(a, stream) : stream_slices<T, Y, KU, RF, W, 0>(a, stream);
+        HG_STREAM(1, 2)
+        HG_STREAM(2, 2)
+        HG_STREAM(3, 2)
+        HG_STREAM(4, 2)
+        HG_STREAM(5, 2)
+        HG_STREAM(6, 2)
+        HG_STREAM(7, 2)
+        HG_STREAM(8, 2)
+        HG_STREAM(9, 1)
+        HG_STREAM(10, 1)
+        HG_STREAM(11, 1)
+        HG_STREAM(12, 1)
+        HG_STREAM(13, 1)
+        HG_STREAM(14, 1)
+        HG_STREAM(15, 1)
+        HG_STREAM(16, 1)
+#undef HG_STREAM
+    }
+    return hipErrorNotSupported;
+}
+
+template <typename T, typename Y>
+hipError_t linear_run(const FwdArgs &a, hipStream_t stream) {
+    if (a.m >= 2048) {
+        const hipError_t e = run_stream<T, Y>(a, stream);
+        if (e != hipErrorNotSupported) return e;
+    }
+    FwdArgs part = a;
+    const int64_t most = 65535LL * 16;  // rows a grid's second dimension reaches
+    for (int64_t m = 0; m < a.m; m += most) {
+        part.m = a.m - m < most ? a.m - m : most;
+        part.x = (const T *)a.x + m * a.xs;
+        part.r = a.r ? (const Y *)a.r + m * a.rs : nullptr;
+        part.y = (Y *)a.y + m * a.ys;
+        part.pre = a.pre ? (T *)a.pre + m * a.ps : nullptr;
+        part.x_scale = a.x_scale ? a.x_scale + m : nullptr;
+        linear_tile_kernel<T, Y><<<dim3((unsigned)div_up(a.n, 16), (unsigned)div_up(part.m, 16)), 256, 0, stream>>>(part);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace
+}  // namespace res
+}  // namespace hg
