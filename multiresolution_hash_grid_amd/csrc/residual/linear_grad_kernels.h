@@ -1,0 +1,398 @@
+// Backward of y = act(x W^T + b) + r on the matrix cores; the sources that
+// include this instantiate one operand type each.
+//
+//   dz = dy act'(z),  dx = dz W,  dW = dz^T x,  db = sum over rows of dz
+//
+// dz is rounded to the operands' type where it enters a product, as products of
+// 16-bit operands need; db sums it unrounded.
+#pragma once
+
+#include "linear_grad.h"
+
+namespace hg {
+namespace res {
+namespace {
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+
+constexpr int kGradThreads = 512;
+
+// A 16-bit tile in LDS, [rows][C], its 16-byte pieces permuted inside eights so
+// that neither kind of read meets bank conflicts: pieces of 8 consecutive rows
+// at one column, and (transposed) 32 bytes of 4 consecutive rows.
+template <int C>
+__device__ __forceinline__ int tile_at(int row, int piece) {
+    return row * (C * 2) + ((piece ^ (((row & 3) << 1) | ((row >> 2) & 1))) << 4);
+}
+
+// The fragment of columns 16 q .. of a tile's rows m .. m + 31, transposed: lane
+// (i, g) gets column i, rows m + 8 g .. m + 8 g + 7.  The transposing read hands
+// lane i of 16 the i-th column of four rows of 16 whose 8-byte parts the lanes'
+// addresses name, four lanes a row (found by reading a tile of known values).
+template <int C>
+__device__ __forceinline__ u32x4 tile_columns(char *tile, int m, int q, int lane) {
+    const int i = lane & 15, row = m + (lane >> 4) * 8 + (i >> 2);
+    union {
+        s16x4 h[2];
+        u32x4 v;
+    } r;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        r.h[h] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (lds_s16x4 *)(tile + tile_at<C>(row + 4 * h, 2 * q + ((i >> 1) & 1)) + (i & 1) * 8));
+    return r.v;
+}
+
+// One piece of dz: 8 values from dy and z; those past `left` columns are zero.
+template <typename T, typename D>
+struct RawDz {
+    u32x4 dy[sizeof(D) == 4 ? 2 : 1], pre;
+};
+template <typename T, typename D>
+__device__ __forceinline__ RawDz<T, D> load_dz(const GradArgs &a, int64_t m, int n, bool there) {
+    RawDz<T, D> v;
+    const int left = there ? a.n - n : 0;
+    const D *dy = (const D *)a.dy + m * a.dys + n;
+    if constexpr (sizeof(D) == 4) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            v.dy[h] = u32x4{0, 0, 0, 0};
+            if (left >= 4 * h + 4) v.dy[h] = load_loose<u32x4>(dy + 4 * h);
+            else
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (4 * h + j < left) v.dy[h][j] = __float_as_uint(dy[4 * h + j]);
+        }
+    } else {
+        v.dy[0] = load_piece(dy, left);
+    }
+    v.pre = u32x4{0, 0, 0, 0};
+    if (a.act != HG_ACT_NONE) v.pre = load_piece((const T *)a.pre + m * a.ps + n, left);
+    return v;
+}
+template <typename T, typename D>
+__device__ __forceinline__ void dz_of(const RawDz<T, D> &v, int act, float (&dz)[8]) {
+    typedef T T8 __attribute__((ext_vector_type(8)));
+    const T8 z = __builtin_bit_cast(T8, v.pre);
+    if constexpr (sizeof(D) == 4) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) dz[j] = __uint_as_float(v.dy[j / 4][j % 4]);
+    } else {
+        const T8 d = __builtin_bit_cast(T8, v.dy[0]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) dz[j] = (float)d[j];
+    }
+    auto times = [&](auto kind) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float s = slope((float)z[j], decltype(kind)::value);
+            dz[j] = s == 0.f ? 0.f : dz[j] * s;
+        }
+    };
+    if (act == HG_ACT_RELU) times(std::integral_constant<int, HG_ACT_RELU>{});
+    else if (act == HG_ACT_SILU) times(std::integral_constant<int, HG_ACT_SILU>{});
+    else if (act == HG_ACT_GELU_TANH) times(std::integral_constant<int, HG_ACT_GELU_TANH>{});
+}
+template <typename T>
+__device__ __forceinline__ u32x4 pack8(const float (&v)[8]) {
+    typedef T T8 __attribute__((ext_vector_type(8)));
+    T8 p;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) p[j] = (T)v[j];
+    return __builtin_bit_cast(u32x4, p);
+}
+
+// W^T of rows n < NT, columns k0 .. k0 + KT in LDS as fragments for dx: block
+// (pair s of 16-column fragments, fragment f, step u of 32 rows n), lane (i, g):
+// column 32 s + (i / 4) 8 + 4 f + i % 4, rows 32 u + 8 g .. + 7.  A thread turns
+// 8 x 8 values: eight pieces of eight rows, two rows' halves merged at a time.
+template <typename T, int NT, int KT>
+__device__ __forceinline__ void stage_wt(const GradArgs &a, int k0, u32x4 *wt) {
+    for (int b = threadIdx.x; b < NT / 8 * (KT / 8); b += kGradThreads) {
+        const int k8 = b % (KT / 8), n8 = b / (KT / 8);
+        u32x4 row[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+            const int n = n8 * 8 + r;
+            row[r] = load_piece((const T *)a.w + (int64_t)n * a.ws + k0 + k8 * 8, n < a.n ? a.k - k0 - k8 * 8 : 0);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            u32x4 v;
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                const uint32_t lo = row[2 * h][j / 2], hi = row[2 * h + 1][j / 2];
+                v[h] = j & 1 ? (lo >> 16) | (hi & 0xFFFF0000u) : (lo & 0xFFFFu) | (hi << 16);
+            }
+            const int i = (k8 & 3) * 4 + (j & 3), f = j >> 2, s = k8 >> 2, u = n8 >> 2, g = n8 & 3;
+            wt[((s * 2 + f) * (NT / 32) + u) * 64 + g * 16 + i] = v;
+        }
+    }
+}
+
+// The whole backward of up to NT outputs by KT inputs in one pass over the rows:
+// dy, z and x are read once, dz lives in LDS only.  A workgroup a CU walks steps
+// of R rows.  In a step each thread turns the pieces it loaded a step ahead into
+// dz (adding its columns up for db) and lays dz and x into LDS; then each wave
+// adds the step's product to its part of dW, which stays in registers to the
+// end (4 x 2 waves over NT x KT), and makes one 32 x 32 block of dx from dz and
+// the W^T fragments held in LDS.  dW and db leave as one partial per workgroup,
+// joined in a fixed order by grad_join_kernel.
+// Wider layers: tiles of NT x KT (blockIdx.y over outputs, .z over inputs)
+// make dW and db alone, and the first column of tiles writes dz for dx's sake.
+template <typename T, typename D, int NT, int KT, bool kDx>
+__global__ __launch_bounds__(kGradThreads) void grad_kernel(const GradArgs a0, float *part, T *dz_out) {
+    constexpr int R = grad_rows(NT, KT), FN = NT / 64, FK = KT / 32;  // fragments of a wave: FN outputs x FK inputs
+    constexpr int PN = NT / 8, PK = KT / 8;                       // pieces of a row
+    constexpr int LN = R * PN / kGradThreads, LK = R * PK / kGradThreads;  // pieces of a thread
+    extern __shared__ __attribute__((aligned(16))) char lds[];
+    char *const dzt = lds, *const xt = lds + R * NT * 2;
+    u32x4 *const wt = (u32x4 *)(lds + R * (NT + KT) * 2);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wn = wave >> 1, wk = wave & 1;
+
+    GradArgs a = a0;
+    const int n0 = blockIdx.y * NT, k0 = blockIdx.z * KT;
+    a.n = a0.n - n0 < NT ? a0.n - n0 : NT;
+    a.k = a0.k - k0 < KT ? a0.k - k0 : KT;
+    a.dy = (const D *)a0.dy + n0;
+    a.pre = (const T *)a0.pre + n0;
+    const bool store_dz = !kDx && dz_out && blockIdx.z == 0;
+
+    if constexpr (kDx) stage_wt<T, NT, KT>(a, 0, wt);
+
+    f32x4 acc[FN][FK];
+#pragma unroll
+    for (int i = 0; i < FN; ++i)
+#pragma unroll
+        for (int j = 0; j < FK; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    float db[8] = {};
+
+    RawDz<T, D> nz[LN];
+    u32x4 nx[LK];
+    auto fetch = [&](int64_t step) {
+#pragma unroll
+        for (int i = 0; i < LN; ++i) {
+            const int p = threadIdx.x + i * kGradThreads;
+            const int64_t m = step * R + p / PN;
+            nz[i] = load_dz<T, D>(a, m, p % PN * 8, m < a.m);
+        }
+#pragma unroll
+        for (int i = 0; i < LK; ++i) {
+            const int p = threadIdx.x + i * kGradThreads;
+            const int64_t m = step * R + p / PK;
+            const int k = k0 + p % PK * 8;
+            nx[i] = load_piece((const T *)a.x + m * a.xs + k, a.dw && m < a.m ? a0.k - k : 0);
+        }
+    };
+
+    const int64_t steps = (a.m + R - 1) / R;
+    if (blockIdx.x < steps) fetch(blockIdx.x);
+    for (int64_t step = blockIdx.x; step < steps; step += gridDim.x) {
+        __syncthreads();  // the last step's reads of the tiles are done
+#pragma unroll
+        for (int i = 0; i < LN; ++i) {
+            const int p = threadIdx.x + i * kGradThreads;
+            float dz[8];
+            dz_of<T, D>(nz[i], a.act, dz);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) db[j] += dz[j];
+            const u32x4 v = pack8<T>(dz);
+            *(u32x4 *)(dzt + tile_at<NT>(p / PN, p % PN)) = v;
+            if (store_dz) {
+                const int64_t m = step * R + p / PN;
+                const int n = p % PN * 8;
+                if (m < a.m) store8(dz_out + m * a0.n + n0 + n, a.n - n, dz);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < LK; ++i) {
+            const int p = threadIdx.x + i * kGradThreads;
+            *(u32x4 *)(xt + tile_at<KT>(p / PK, p % PK)) = nx[i];
+        }
+        if (step + gridDim.x < steps) fetch(step + gridDim.x);
+        __syncthreads();
+        if (a.dw) {
+#pragma unroll
+            for (int m = 0; m < R; m += 32) {
+                u32x4 dzf[FN];
+#pragma unroll
+                for (int i = 0; i < FN; ++i) dzf[i] = tile_columns<NT>(dzt, m, wn * FN + i, lane);
+#pragma unroll
+                for (int j = 0; j < FK; ++j) {
+                    const u32x4 xf = tile_columns<KT>(xt, m, wk * FK + j, lane);
+#pragma unroll
+                    for (int i = 0; i < FN; ++i) acc[i][j] = mma<T>(xf, dzf[i], acc[i][j]);
+                }
+            }
+        }
+        if constexpr (kDx) {
+            const int row = lane & 15, g = lane >> 4;
+#pragma unroll
+            for (int block = wave; block < KT / 32 * (R / 32); block += 8) {
+                const int s = block % (KT / 32), m = block / (KT / 32) * 32;
+                f32x4 d[2][2] = {};
+#pragma unroll
+                for (int u = 0; u < NT / 32; ++u) {
+                    u32x4 z[2];
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) z[r] = *(const u32x4 *)(dzt + tile_at<NT>(m + r * 16 + row, u * 4 + g));
+#pragma unroll
+                    for (int f = 0; f < 2; ++f) {
+                        const u32x4 w = wt[((s * 2 + f) * (NT / 32) + u) * 64 + lane];
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) d[f][r] = mma<T>(w, z[r], d[f][r]);
+                    }
+                }
+                const int k = s * 32 + g * 8;
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const int64_t at = step * R + m + r * 16 + row;
+                    if (at >= a.m) continue;
+                    const float v[8] = {d[0][r][0], d[0][r][1], d[0][r][2], d[0][r][3],
+                                        d[1][r][0], d[1][r][1], d[1][r][2], d[1][r][3]};
+                    store8((T *)a.dx + at * a.dxs + k, a.k - k, v);
+                }
+            }
+        }
+    }
+
+    // Partials: dW as fragments, [tile][workgroup][NT x KT], then db, [output tile][workgroup][NT].
+    const int tile = blockIdx.y * gridDim.z + blockIdx.z;
+    if (a.dw) {
+        float *p = part + ((int64_t)tile * gridDim.x + blockIdx.x) * (NT * KT);
+#pragma unroll
+        for (int i = 0; i < FN; ++i)
+#pragma unroll
+            for (int j = 0; j < FK; ++j)
+                *(f32x4 *)(p + ((wn * FN + i) * (KT / 16) + wk * FK + j) * 256 + lane * 4) = acc[i][j];
+    }
+    if (a.db && blockIdx.z == 0) {
+        float *const sums = (float *)lds;  // [512 / PN][NT]
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sums[threadIdx.x * 8 + j] = db[j];
+        __syncthreads();
+        float *p = part + (a.dw ? (int64_t)gridDim.y * gridDim.z * gridDim.x * (NT * KT) : 0) +
+                   ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * NT;
+        for (int n = threadIdx.x; n < NT; n += kGradThreads) {
+            float t = 0.f;
+            for (int r = 0; r < kGradThreads / PN; ++r) t += sums[r * NT + n];
+            p[n] = t;
+        }
+    }
+}
+
+// dW = (dW +) the partials' sum, rounded once; db alike.  A workgroup takes 64
+// groups of four values; its four waves share the partials and add up in order.
+template <typename G>
+__global__ __launch_bounds__(256) void grad_join_kernel(const float *part, int parts, int nt, int kt, int ny, int nz, GradArgs a) {
+    __shared__ f32x4 lds[4][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t quads = a.dw ? (int64_t)ny * nz * nt * kt / 4 : 0, all = quads + (a.db ? ny * nt / 4 : 0);
+    const int64_t q = (int64_t)blockIdx.x * 64 + lane;
+    const int64_t per = q < quads ? nt * kt / 4 : nt / 4;      // quads of a partial
+    const int64_t local = q < quads ? q : q - quads;
+    const float *p = part + (q < quads ? 0 : quads * 4 * parts) + (local / per * per * parts + local % per) * 4;
+    f32x4 t = {0.f, 0.f, 0.f, 0.f};
+    if (q < all)
+#pragma unroll 8
+        for (int i = wave; i < parts; i += 4) t += *(const f32x4 *)(p + i * per * 4);
+    lds[wave][lane] = t;
+    __syncthreads();
+    if (wave || q >= all) return;
+    for (int i = 1; i < 4; ++i) t += lds[i][lane];
+    if (q < quads) {
+        const int tile = (int)(local / per), e = (int)(local % per), frag = e / 64, l = e % 64;
+        const int n = tile / nz * nt + frag / (kt / 16) * 16 + (l & 15);
+        const int k = tile % nz * kt + frag % (kt / 16) * 16 + (l >> 4) * 4;
+        if (n >= a.n) return;
+        G *w = (G *)a.dw + (int64_t)n * a.dws + k;
+        for (int j = 0; j < 4; ++j)
+            if (k + j < a.k) w[j] = (G)(a.accumulate ? (float)w[j] + t[j] : t[j]);
+    } else {
+        for (int j = 0; j < 4; ++j) {
+            const int64_t n = local * 4 + j;
+            if (n < a.n) a.db[n] = a.accumulate ? a.db[n] + t[j] : t[j];
+        }
+    }
+}
+
+// W^T [k][n] of W [n][k], for dx of wide layers through the forward's kernels.
+template <typename T>
+__global__ __launch_bounds__(256) void transpose_kernel(const T *w, int64_t ws, int n, int k, T *wt) {
+    __shared__ T tile[32][33];
+    const int c = threadIdx.x & 31, r0 = threadIdx.x >> 5;
+    for (int r = r0; r < 32; r += 8) {
+        const int i = blockIdx.y * 32 + r, j = blockIdx.x * 32 + c;
+        if (i < n && j < k) tile[r][c] = w[(int64_t)i * ws + j];
+    }
+    __syncthreads();
+    for (int r = r0; r < 32; r += 8) {
+        const int j = blockIdx.x * 32 + r, i = blockIdx.y * 32 + c;
+        if (i < n && j < k) wt[(int64_t)j * n + i] = tile[c][r];
+    }
+}
+
+template <typename T, typename D, int NT, int KT, bool kDx>
+hipError_t grad_launch(const GradArgs &a, const GradPlan &p, float *part, T *dz, hipStream_t stream) {
+    const auto kernel = grad_kernel<T, D, NT, KT, kDx>;
+    const int bytes = grad_rows(NT, KT) * (NT + KT) * 2 + (kDx ? NT * KT * 2 : 0);
+    if (bytes > 65536) {
+        const hipError_t e = hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e != hipSuccess) return e;
+    }
+    kernel<<<dim3((unsigned)p.parts, (unsigned)p.ny, (unsigned)p.nz), kGradThreads, bytes, stream>>>(a, part, dz);
+    return hipGetLastError();
+}
+
+template <typename T, typename D, bool kDx>
+hipError_t grad_pick(const GradArgs &a, const GradPlan &p, float *part, T *dz, hipStream_t stream) {
+#define HG_GRAD(NT, KT) \
+    if (p.nt == NT && p.kt == KT) return grad_launch<T, D, NT, KT, kDx>(a, p, part, dz, stream);
+    HG_GRAD(64, 64)
+    HG_GRAD(64, 128)
+    HG_GRAD(64, 256)
+    HG_GRAD(128, 64)
+    HG_GRAD(128, 128)
+    HG_GRAD(128, 256)
+    HG_GRAD(256, 64)
+    HG_GRAD(256, 128)
+    HG_GRAD(256, 256)
+#undef HG_GRAD
+    return hipErrorInvalidValue;
+}
+
+template <typename T, typename D>
+hipError_t grad_run(const GradArgs &a, bool dw_f32, const GradPlan &p, char *workspace, hipStream_t stream,
+                    hipError_t (*forward)(const FwdArgs &, int, hipStream_t), int dtype) {
+    float *const part = (float *)workspace;
+    T *const dz = (T *)(workspace + p.dz_at), *const wt = (T *)(workspace + p.wt_at);
+    hipError_t e;
+    if (a.m > 0) {
+        e = p.fused ? grad_pick<T, D, true>(a, p, part, nullptr, stream)
+                    : grad_pick<T, D, false>(a, p, part, a.dx ? dz : nullptr, stream);
+        if (e != hipSuccess) return e;
+    }
+    if (a.dw || a.db) {
+        const int64_t quads = (a.dw ? (int64_t)p.ny * p.nz * p.nt * p.kt : 0) / 4 + (a.db ? p.ny * p.nt / 4 : 0);
+        const int parts = a.m > 0 ? p.parts : 0;
+        const auto join = dw_f32 ? grad_join_kernel<float> : grad_join_kernel<T>;
+        join<<<dim3((unsigned)div_up(quads, 64)), 256, 0, stream>>>(part, parts, p.nt, p.kt, p.ny, p.nz, a);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    if (a.dx && a.m > 0 && !p.fused) {
+        transpose_kernel<T><<<dim3((unsigned)div_up(a.k, 32), (unsigned)div_up(a.n, 32)), 256, 0, stream>>>((const T *)a.w, a.ws, a.n,
+                                                                                                       a.k, wt);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+        FwdArgs f{};
+        f.m = a.m, f.xs = a.n, f.ws = a.n, f.ys = a.dxs, f.k = a.n, f.n = a.k, f.act = HG_ACT_NONE;
+        f.x = dz, f.w = wt, f.y = a.dx;
+        return forward(f, dtype, stream);
+    }
+    return hipSuccess;
+}
+
+}  // namespace
+}  // namespace res
+}  // namespace hg
