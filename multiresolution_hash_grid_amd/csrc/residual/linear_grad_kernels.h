@@ -44,35 +44,59 @@ __device__ __forceinline__ u32x4 tile_columns(char *tile, int m, int q, int lane
     return r.v;
 }
 
-// One piece of dz: 8 values from dy and z; those past `left` columns are zero.
+// The columns of one piece of a row of `width` columns.  Loads are the same for
+// every piece, without branches, so that the compiler can count them and a step
+// waits for its own loads alone: the piece that the row's end cuts is read so
+// that it ends with the row, and its first `drop` slots, which the piece before
+// holds, are zeroed where the piece is used (all 8 of a piece past the row).
+// Slots therefore stand for column at + slot; the join knows.  Rows of less
+// than a piece are read value by value.
+struct Columns {
+    int at, drop;
+};
+__device__ __forceinline__ Columns columns_of(int nominal, int width) {
+    if (width < 8) return {nominal, nominal < width ? 0 : 8};
+    const int at = nominal < width - 8 ? nominal : width - 8;
+    return {at, nominal - at};
+}
+// The column of a slot, or -1 of a zeroed one.
+__device__ __forceinline__ int column_of(int slot, int width) {
+    const Columns c = columns_of(slot / 8 * 8, width);
+    const int j = slot % 8;
+    return j < c.drop || c.at + j >= width ? -1 : c.at + j;
+}
+
+template <typename T>
+__device__ __forceinline__ u32x4 load_columns(const T *row, Columns c, int width) {
+    if (width >= 8) return load_loose<u32x4>(row + c.at);
+    return load_piece(row + c.at, c.drop ? 0 : width);
+}
+
+// One piece of dz: 8 values from dy and z.
 template <typename T, typename D>
 struct RawDz {
     u32x4 dy[sizeof(D) == 4 ? 2 : 1], pre;
 };
 template <typename T, typename D>
-__device__ __forceinline__ RawDz<T, D> load_dz(const GradArgs &a, int64_t m, int n, bool there) {
+__device__ __forceinline__ RawDz<T, D> load_dz(const GradArgs &a, int64_t m, Columns c) {
     RawDz<T, D> v;
-    const int left = there ? a.n - n : 0;
-    const D *dy = (const D *)a.dy + m * a.dys + n;
+    const D *dy = (const D *)a.dy + m * a.dys;
     if constexpr (sizeof(D) == 4) {
+        if (a.n >= 8) {
+            v.dy[0] = load_loose<u32x4>(dy + c.at), v.dy[1] = load_loose<u32x4>(dy + c.at + 4);
+        } else {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            v.dy[h] = u32x4{0, 0, 0, 0};
-            if (left >= 4 * h + 4) v.dy[h] = load_loose<u32x4>(dy + 4 * h);
-            else
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (4 * h + j < left) v.dy[h][j] = __float_as_uint(dy[4 * h + j]);
+            for (int j = 0; j < 8; ++j) v.dy[j / 4][j % 4] = c.drop == 0 && j < a.n ? __float_as_uint(dy[j]) : 0u;
         }
     } else {
-        v.dy[0] = load_piece(dy, left);
+        v.dy[0] = load_columns(dy, c, a.n);
     }
     v.pre = u32x4{0, 0, 0, 0};
-    if (a.act != HG_ACT_NONE) v.pre = load_piece((const T *)a.pre + m * a.ps + n, left);
+    if (a.act != HG_ACT_NONE) v.pre = load_columns((const T *)a.pre + m * a.ps, c, a.n);
     return v;
 }
 template <typename T, typename D>
-__device__ __forceinline__ void dz_of(const RawDz<T, D> &v, int act, float (&dz)[8]) {
+__device__ __forceinline__ void dz_of(const RawDz<T, D> &v, int act, int drop, float (&dz)[8]) {
     typedef T T8 __attribute__((ext_vector_type(8)));
     const T8 z = __builtin_bit_cast(T8, v.pre);
     if constexpr (sizeof(D) == 4) {
@@ -93,6 +117,9 @@ __device__ __forceinline__ void dz_of(const RawDz<T, D> &v, int act, float (&dz)
     if (act == HG_ACT_RELU) times(std::integral_constant<int, HG_ACT_RELU>{});
     else if (act == HG_ACT_SILU) times(std::integral_constant<int, HG_ACT_SILU>{});
     else if (act == HG_ACT_GELU_TANH) times(std::integral_constant<int, HG_ACT_GELU_TANH>{});
+    if (drop > 0)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) dz[j] = j < drop ? 0.f : dz[j];
 }
 template <typename T>
 __device__ __forceinline__ u32x4 pack8(const float (&v)[8]) {
@@ -114,8 +141,8 @@ __device__ __forceinline__ void stage_wt(const GradArgs &a, int k0, u32x4 *wt) {
         u32x4 row[8];
 #pragma unroll
         for (int r = 0; r < 8; ++r) {
-            const int n = n8 * 8 + r;
-            row[r] = load_piece((const T *)a.w + (int64_t)n * a.ws + k0 + k8 * 8, n < a.n ? a.k - k0 - k8 * 8 : 0);
+            const int n = column_of(n8 * 8 + r, a.n);
+            row[r] = load_piece((const T *)a.w + (int64_t)n * a.ws + k0 + k8 * 8, n >= 0 ? a.k - k0 - k8 * 8 : 0);
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -142,7 +169,7 @@ __device__ __forceinline__ void stage_wt(const GradArgs &a, int k0, u32x4 *wt) {
 // Wider layers: tiles of NT x KT (blockIdx.y over outputs, .z over inputs)
 // make dW and db alone, and the first column of tiles writes dz for dx's sake.
 template <typename T, typename D, int NT, int KT, bool kDx>
-__global__ __launch_bounds__(kGradThreads) void grad_kernel(const GradArgs a0, float *part, T *dz_out) {
+__global__ __launch_bounds__(kGradThreads) void grad_kernel(const GradArgs a, float *part, T *dz_out) {
     constexpr int R = grad_rows(NT, KT), FN = NT / 64, FK = KT / 32;  // fragments of a wave: FN outputs x FK inputs
     constexpr int PN = NT / 8, PK = KT / 8;                       // pieces of a row
     constexpr int LN = R * PN / kGradThreads, LK = R * PK / kGradThreads;  // pieces of a thread
@@ -151,13 +178,13 @@ __global__ __launch_bounds__(kGradThreads) void grad_kernel(const GradArgs a0, f
     u32x4 *const wt = (u32x4 *)(lds + R * (NT + KT) * 2);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wn = wave >> 1, wk = wave & 1;
 
-    GradArgs a = a0;
     const int n0 = blockIdx.y * NT, k0 = blockIdx.z * KT;
-    a.n = a0.n - n0 < NT ? a0.n - n0 : NT;
-    a.k = a0.k - k0 < KT ? a0.k - k0 : KT;
-    a.dy = (const D *)a0.dy + n0;
-    a.pre = (const T *)a0.pre + n0;
     const bool store_dz = !kDx && dz_out && blockIdx.z == 0;
+    const Columns cn = columns_of(n0 + threadIdx.x % PN * 8, a.n), ck = columns_of(k0 + threadIdx.x % PK * 8, a.k);
+    u32x4 keep_k;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        keep_k[j] = 2 * j >= ck.drop ? ~0u : 2 * j + 1 >= ck.drop ? 0xFFFF0000u : 0u;
 
     if constexpr (kDx) stage_wt<T, NT, KT>(a, 0, wt);
 
@@ -173,43 +200,73 @@ __global__ __launch_bounds__(kGradThreads) void grad_kernel(const GradArgs a0, f
     auto fetch = [&](int64_t step) {
 #pragma unroll
         for (int i = 0; i < LN; ++i) {
-            const int p = threadIdx.x + i * kGradThreads;
-            const int64_t m = step * R + p / PN;
-            nz[i] = load_dz<T, D>(a, m, p % PN * 8, m < a.m);
+            const int64_t m = step * R + threadIdx.x / PN + i * (kGradThreads / PN);
+            nz[i] = load_dz<T, D>(a, m < a.m ? m : a.m - 1, cn);
         }
+        if (a.dw)
 #pragma unroll
-        for (int i = 0; i < LK; ++i) {
-            const int p = threadIdx.x + i * kGradThreads;
-            const int64_t m = step * R + p / PK;
-            const int k = k0 + p % PK * 8;
-            nx[i] = load_piece((const T *)a.x + m * a.xs + k, a.dw && m < a.m ? a0.k - k : 0);
+            for (int i = 0; i < LK; ++i) {
+                const int64_t m = step * R + threadIdx.x / PK + i * (kGradThreads / PK);
+                nx[i] = load_columns((const T *)a.x + (m < a.m ? m : a.m - 1) * a.xs, ck, a.k);
+            }
+    };
+
+    // dx of a step is stored in the next one, between the use of the loads that
+    // were made a step ahead and the next such loads: a wait for those loads then
+    // has no younger stores to wait for.
+    constexpr int kBlocks = KT / 32 * (R / 32) / 8;  // 32 x 32 blocks of dx a wave makes
+    u32x4 late[kBlocks][2];
+    auto store_late = [&](int64_t step) {
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b) {
+            const int block = wave + b * 8, k = block % (KT / 32) * 32 + (lane >> 4) * 8, left = a.k - k;
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const int64_t m = step * R + block / (KT / 32) * 32 + r * 16 + (lane & 15);
+                T *const p = (T *)a.dx + m * a.dxs + k;
+                if (m < a.m) {
+                    if (left >= 8) store_loose<u32x4>(p, late[b][r]);
+                    else
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            if (j < left) p[j] = __builtin_bit_cast(T, (uint16_t)(late[b][r][j / 2] >> (16 * (j & 1))));
+                }
+            }
         }
     };
 
     const int64_t steps = (a.m + R - 1) / R;
     if (blockIdx.x < steps) fetch(blockIdx.x);
     for (int64_t step = blockIdx.x; step < steps; step += gridDim.x) {
+        const bool whole = (step + 1) * R <= a.m;
         __syncthreads();  // the last step's reads of the tiles are done
 #pragma unroll
         for (int i = 0; i < LN; ++i) {
-            const int p = threadIdx.x + i * kGradThreads;
+            const int r = threadIdx.x / PN + i * (kGradThreads / PN);
             float dz[8];
-            dz_of<T, D>(nz[i], a.act, dz);
+            dz_of<T, D>(nz[i], a.act, whole || step * R + r < a.m ? cn.drop : 8, dz);
 #pragma unroll
             for (int j = 0; j < 8; ++j) db[j] += dz[j];
-            const u32x4 v = pack8<T>(dz);
-            *(u32x4 *)(dzt + tile_at<NT>(p / PN, p % PN)) = v;
-            if (store_dz) {
-                const int64_t m = step * R + p / PN;
-                const int n = p % PN * 8;
-                if (m < a.m) store8(dz_out + m * a0.n + n0 + n, a.n - n, dz);
+            *(u32x4 *)(dzt + tile_at<NT>(r, threadIdx.x % PN)) = pack8<T>(dz);
+            if (store_dz && step * R + r < a.m) {
+                T *const p = dz_out + (step * R + r) * a.n + cn.at;
+                if (cn.drop == 0) store8(p, a.n < 8 ? a.n : 8, dz);
+                else
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (j >= cn.drop) p[j] = (T)dz[j];
             }
         }
+        if (a.dw)
 #pragma unroll
-        for (int i = 0; i < LK; ++i) {
-            const int p = threadIdx.x + i * kGradThreads;
-            *(u32x4 *)(xt + tile_at<KT>(p / PK, p % PK)) = nx[i];
-        }
+            for (int i = 0; i < LK; ++i) {
+                const int r = threadIdx.x / PK + i * (kGradThreads / PK);
+                u32x4 v = nx[i];
+                if (ck.drop > 0) v &= keep_k;
+                if (!whole && step * R + r >= a.m) v = u32x4{0, 0, 0, 0};
+                *(u32x4 *)(xt + tile_at<KT>(r, threadIdx.x % PK)) = v;
+            }
+        if (kDx && step != blockIdx.x) store_late(step - gridDim.x);
         if (step + gridDim.x < steps) fetch(step + gridDim.x);
         __syncthreads();
         if (a.dw) {
@@ -229,8 +286,8 @@ __global__ __launch_bounds__(kGradThreads) void grad_kernel(const GradArgs a0, f
         if constexpr (kDx) {
             const int row = lane & 15, g = lane >> 4;
 #pragma unroll
-            for (int block = wave; block < KT / 32 * (R / 32); block += 8) {
-                const int s = block % (KT / 32), m = block / (KT / 32) * 32;
+            for (int b = 0; b < kBlocks; ++b) {
+                const int block = wave + b * 8, s = block % (KT / 32), m = block / (KT / 32) * 32;
                 f32x4 d[2][2] = {};
 #pragma unroll
                 for (int u = 0; u < NT / 32; ++u) {
@@ -244,18 +301,16 @@ __global__ __launch_bounds__(kGradThreads) void grad_kernel(const GradArgs a0, f
                         for (int r = 0; r < 2; ++r) d[f][r] = mma<T>(w, z[r], d[f][r]);
                     }
                 }
-                const int k = s * 32 + g * 8;
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    const int64_t at = step * R + m + r * 16 + row;
-                    if (at >= a.m) continue;
                     const float v[8] = {d[0][r][0], d[0][r][1], d[0][r][2], d[0][r][3],
                                         d[1][r][0], d[1][r][1], d[1][r][2], d[1][r][3]};
-                    store8((T *)a.dx + at * a.dxs + k, a.k - k, v);
+                    late[b][r] = pack8<T>(v);
                 }
             }
         }
     }
+    if (kDx && blockIdx.x < steps) store_late(blockIdx.x + (steps - 1 - blockIdx.x) / gridDim.x * gridDim.x);
 
     // Partials: dW as fragments, [tile][workgroup][NT x KT], then db, [output tile][workgroup][NT].
     const int tile = blockIdx.y * gridDim.z + blockIdx.z;
@@ -304,16 +359,18 @@ __global__ __launch_bounds__(256) void grad_join_kernel(const float *part, int p
     for (int i = 1; i < 4; ++i) t += lds[i][lane];
     if (q < quads) {
         const int tile = (int)(local / per), e = (int)(local % per), frag = e / 64, l = e % 64;
-        const int n = tile / nz * nt + frag / (kt / 16) * 16 + (l & 15);
-        const int k = tile % nz * kt + frag % (kt / 16) * 16 + (l >> 4) * 4;
-        if (n >= a.n) return;
-        G *w = (G *)a.dw + (int64_t)n * a.dws + k;
-        for (int j = 0; j < 4; ++j)
-            if (k + j < a.k) w[j] = (G)(a.accumulate ? (float)w[j] + t[j] : t[j]);
+        const int n = column_of(tile / nz * nt + frag / (kt / 16) * 16 + (l & 15), a.n);
+        const int k0 = tile % nz * kt + frag % (kt / 16) * 16 + (l >> 4) * 4;
+        if (n < 0) return;
+        G *w = (G *)a.dw + (int64_t)n * a.dws;
+        for (int j = 0; j < 4; ++j) {
+            const int k = column_of(k0 + j, a.k);
+            if (k >= 0) w[k] = (G)(a.accumulate ? (float)w[k] + t[j] : t[j]);
+        }
     } else {
         for (int j = 0; j < 4; ++j) {
-            const int64_t n = local * 4 + j;
-            if (n < a.n) a.db[n] = a.accumulate ? a.db[n] + t[j] : t[j];
+            const int n = column_of((int)local * 4 + j, a.n);
+            if (n >= 0) a.db[n] = a.accumulate ? a.db[n] + t[j] : t[j];
         }
     }
 }
