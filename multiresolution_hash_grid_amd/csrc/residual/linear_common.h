@@ -149,13 +149,13 @@ __device__ __forceinline__ void activate_all(float (&z)[N], int act) {
 __device__ __forceinline__ float slope(float z, int act) {
     if (act == HG_ACT_RELU) return z > 0.f ? 1.f : z != z ? z : 0.f;
     if (act == HG_ACT_SILU) {
-        const float p = logistic(z), q = z * p * (1.f - p);
-        return __builtin_isinf(z) ? p : p + q;
+        const float p = logistic(z);
+        return __builtin_isinf(z) ? p : p * fmaf(z, 1.f - p, 1.f);
     }
     if (act == HG_ACT_GELU_TANH) {
         const float p = logistic(1.59576912f * z * fmaf(0.044715f * z, z, 1.f));
-        const float q = z * p * (1.f - p) * 1.59576912f * fmaf(0.134145f * z, z, 1.f);
-        return p == 0.f || p == 1.f ? p : p + q;
+        const float q = 1.59576912f * z * fmaf(0.134145f * z, z, 1.f);
+        return p == 0.f || p == 1.f ? p : p * fmaf(q, 1.f - p, 1.f);
     }
     return 1.f;
 }

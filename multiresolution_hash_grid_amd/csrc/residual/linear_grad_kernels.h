@@ -18,12 +18,14 @@ typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
 constexpr int kGradThreads = 512;
 
-// A 16-bit tile in LDS, [rows][C], its 16-byte pieces permuted inside eights so
-// that neither kind of read meets bank conflicts: pieces of 8 consecutive rows
-// at one column, and (transposed) 32 bytes of 4 consecutive rows.
+// A 16-bit tile in LDS, [rows][C], its 16-byte pieces permuted so that 256 bytes
+// at a time come from 64 different banks in both kinds of read: one piece of 16
+// rows, and (transposed) 32 bytes of rows r .. r + 3 and r + 8 .. r + 11.
 template <int C>
 __device__ __forceinline__ int tile_at(int row, int piece) {
-    return row * (C * 2) + ((piece ^ (((row & 3) << 1) | ((row >> 2) & 1))) << 4);
+    const int turn = C == 64 ? (row & 2) | ((row >> 1) & 4) | ((row >> 2) & 1)
+                             : ((row & 3) << 1) | ((row >> 2) & 1) | (row & 8);
+    return row * (C * 2) + ((piece ^ turn) << 4);
 }
 
 // The fragment of columns 16 q .. of a tile's rows m .. m + 31, transposed: lane
@@ -111,7 +113,7 @@ __device__ __forceinline__ void dz_of(const RawDz<T, D> &v, int act, int drop, f
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const float s = slope((float)z[j], decltype(kind)::value);
-            dz[j] = s == 0.f ? 0.f : dz[j] * s;
+            dz[j] = decltype(kind)::value == HG_ACT_RELU && s == 0.f ? 0.f : dz[j] * s;
         }
     };
     if (act == HG_ACT_RELU) times(std::integral_constant<int, HG_ACT_RELU>{});
@@ -339,10 +341,10 @@ __global__ __launch_bounds__(kGradThreads) void grad_kernel(const GradArgs a, fl
 }
 
 // dW = (dW +) the partials' sum, rounded once; db alike.  A workgroup takes 64
-// groups of four values; its four waves share the partials and add up in order.
+// groups of four values; its eight waves share the partials and add up in order.
 template <typename G>
-__global__ __launch_bounds__(256) void grad_join_kernel(const float *part, int parts, int nt, int kt, int ny, int nz, GradArgs a) {
-    __shared__ f32x4 lds[4][64];
+__global__ __launch_bounds__(512) void grad_join_kernel(const float *part, int parts, int nt, int kt, int ny, int nz, GradArgs a) {
+    __shared__ f32x4 lds[8][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t quads = a.dw ? (int64_t)ny * nz * nt * kt / 4 : 0, all = quads + (a.db ? ny * nt / 4 : 0);
     const int64_t q = (int64_t)blockIdx.x * 64 + lane;
@@ -352,11 +354,11 @@ __global__ __launch_bounds__(256) void grad_join_kernel(const float *part, int p
     f32x4 t = {0.f, 0.f, 0.f, 0.f};
     if (q < all)
 #pragma unroll 8
-        for (int i = wave; i < parts; i += 4) t += *(const f32x4 *)(p + i * per * 4);
+        for (int i = wave; i < parts; i += 8) t += *(const f32x4 *)(p + i * per * 4);
     lds[wave][lane] = t;
     __syncthreads();
     if (wave || q >= all) return;
-    for (int i = 1; i < 4; ++i) t += lds[i][lane];
+    for (int i = 1; i < 8; ++i) t += lds[i][lane];
     if (q < quads) {
         const int tile = (int)(local / per), e = (int)(local % per), frag = e / 64, l = e % 64;
         const int n = column_of(tile / nz * nt + frag / (kt / 16) * 16 + (l & 15), a.n);
@@ -435,7 +437,7 @@ hipError_t grad_run(const GradArgs &a, bool dw_f32, const GradPlan &p, char *wor
         const int64_t quads = (a.dw ? (int64_t)p.ny * p.nz * p.nt * p.kt : 0) / 4 + (a.db ? p.ny * p.nt / 4 : 0);
         const int parts = a.m > 0 ? p.parts : 0;
         const auto join = dw_f32 ? grad_join_kernel<float> : grad_join_kernel<T>;
-        join<<<dim3((unsigned)div_up(quads, 64)), 256, 0, stream>>>(part, parts, p.nt, p.kt, p.ny, p.nz, a);
+        join<<<dim3((unsigned)div_up(quads, 64)), 512, 0, stream>>>(part, parts, p.nt, p.kt, p.ny, p.nz, a);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     if (a.dx && a.m > 0 && !p.fused) {
