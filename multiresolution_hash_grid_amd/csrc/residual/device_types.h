@@ -138,6 +138,27 @@ __device__ __forceinline__ void store_some(T *p, int left, const float (&v)[N]) 
     }
 }
 
+// N values as they lie in memory, to be held until they are used.
+template <int N, typename T>
+struct Held {
+    T v __attribute__((ext_vector_type(N)));
+};
+template <int N, typename T>
+__device__ __forceinline__ Held<N, T> hold(const T *p, int left) {
+    typedef T V __attribute__((ext_vector_type(N)));
+    Held<N, T> h;
+    if (left >= N) {
+        h.v = load_loose<V>(p);
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            h.v[j] = (T)0.f;
+            if (j < left) h.v[j] = p[j];
+        }
+    }
+    return h;
+}
+
 // Sum over aligned groups of G lanes, in every lane of the group.
 template <int G>
 __device__ __forceinline__ float group_sum(float v) {

@@ -26,50 +26,37 @@ constexpr int kPiece = 16 / (int)sizeof(T);    // elements of a lane
 // the 32- and the 128-deep instruction), so 8-bit operands are widened where
 // they enter a product and their sums are fp32 like the others'.
 struct Widened {
-    f16x8 lo, hi;
+    u32x4 lo, hi;
 };
 __device__ __forceinline__ Widened widen(u32x4 v) {
     Widened w;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const auto a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(v[i], 1.f, false), b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(v[i], 1.f, true);
-        const auto c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(v[2 + i], 1.f, false), d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(v[2 + i], 1.f, true);
-        w.lo[4 * i] = a[0], w.lo[4 * i + 1] = a[1], w.lo[4 * i + 2] = b[0], w.lo[4 * i + 3] = b[1];
-        w.hi[4 * i] = c[0], w.hi[4 * i + 1] = c[1], w.hi[4 * i + 2] = d[0], w.hi[4 * i + 3] = d[1];
+        w.lo[2 * i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(v[i], 1.f, false));
+        w.lo[2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(v[i], 1.f, true));
+        w.hi[2 * i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(v[2 + i], 1.f, false));
+        w.hi[2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(v[2 + i], 1.f, true));
     }
     return w;
 }
 
-// A fragment ready for the matrix cores.
 template <typename T>
-struct Ready {
-    u32x4 v;
-};
-template <>
-struct Ready<f8> {
-    Widened v;
-};
-template <typename T>
-__device__ __forceinline__ Ready<T> ready(u32x4 v) {
-    if constexpr (sizeof(T) == 1) return {widen(v)};
-    else return {v};
+__device__ __forceinline__ f32x4 mma16(u32x4 a, u32x4 b, f32x4 acc) {
+    if constexpr (__is_same(T, bf16))
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), acc, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), acc, 0, 0, 0);
 }
 
 // acc[r] += sum_k a[row = 4 (lane / 16) + r][k] b[row = lane % 16][k], fp32 sums.
 template <typename T>
-__device__ __forceinline__ f32x4 mma(Ready<T> a, Ready<T> b, f32x4 acc) {
-    if constexpr (sizeof(T) == 1) {
-        acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(a.v.lo, b.v.lo, acc, 0, 0, 0);
-        return __builtin_amdgcn_mfma_f32_16x16x32_f16(a.v.hi, b.v.hi, acc, 0, 0, 0);
-    } else if constexpr (__is_same(T, f16)) {
-        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a.v), __builtin_bit_cast(f16x8, b.v), acc, 0, 0, 0);
-    } else {
-        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a.v), __builtin_bit_cast(bf16x8, b.v), acc, 0, 0, 0);
-    }
-}
-template <typename T>
 __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 acc) {
-    return mma<T>(ready<T>(a), ready<T>(b), acc);
+    if constexpr (sizeof(T) == 1) {
+        const Widened x = widen(a), y = widen(b);
+        return mma16<f16>(x.hi, y.hi, mma16<f16>(x.lo, y.lo, acc));
+    } else {
+        return mma16<T>(a, b, acc);
+    }
 }
 
 // The 16-byte piece at p of a row that has `left` more elements; what lies

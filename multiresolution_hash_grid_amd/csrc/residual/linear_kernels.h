@@ -43,22 +43,28 @@ __global__ __launch_bounds__(256) void linear_tile_kernel(const FwdArgs a) {
 
 // Many rows, a weight that fits LDS in a few slices.  A workgroup keeps its
 // slice of W in LDS for good, in fragment order (a wave reads 1 KB in a row,
-// without conflicts), and its waves walk row tiles of RF * 16 rows on their
-// own: a tile's rows go straight from memory into registers as fragments, all
-// of the contraction at once, and each set of FR 16-output fragments is finished
-// -- bias, activation, residual, rounding -- before the next is begun.  No
-// barrier after the start: the waves of a CU hide each other's loads.
-// A set's outputs are dealt so that a lane has 4 * FR consecutive ones of one row:
-// row i of fragment h is output (i / 4) * 4 * FR + h * 4 + i % 4 of the set.
+// without conflicts; 8-bit weights are widened once, here), and its waves walk
+// row tiles of RF * 16 rows on their own: a tile's rows go straight from memory
+// into registers as fragments, all of the contraction at once, and each set of
+// FR 16-output fragments is finished -- bias, activation, residual, rounding --
+// before the next is begun.  No barrier after the start: the waves of a CU hide
+// each other's loads.
+// A pair of fragments deals its 32 outputs so that a lane has 8 consecutive ones
+// of one row: row i of fragment h is output (i / 4) * 8 + h * 4 + i % 4.  A set of
+// two pairs reads and writes whole 128-byte lines (16-bit outputs): with one pair
+// a set, half lines left L2 before their other halves came, and 1.35 times the
+// bytes were written and 1.45 times read (2^20 x 256 x 256).
 // Slices of W are workgroups next to each other on one XCD that walk the same
 // rows, so x comes from HBM once.
 // kCut: 0 the contraction is whole fragments; 1 its last fragment is cut; 2 it
 // is shorter than a piece.
-template <typename T, typename Y, int KU, int RF, int WAVES, int FR, int kCut>
-__global__ __launch_bounds__(WAVES * 64) void linear_stream_kernel(const FwdArgs a, int slices, int slice_n) {
+template <typename T, typename Y, int KU, int RF, int FR, int kCut>
+__global__ __launch_bounds__(1024) void linear_stream_kernel(const FwdArgs a, int slices, int slice_n) {
     extern __shared__ __attribute__((aligned(16))) char lds[];
+    constexpr int kWaves = 16, kHalves = sizeof(T) == 1 ? 2 : 1;
+    constexpr int kPairs = FR / 2, kOut = FR == 1 ? 4 : 8;  // pairs of a set; consecutive outputs of a lane
+    constexpr bool kWide = sizeof(T) == 1 && KU <= 8;       // 8-bit rows are widened as they come; longer ones at each use
     u32x4 *const wl = (u32x4 *)lds;
-    constexpr int kOut = 4 * FR;  // outputs of a lane in a set
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, row16 = lane & 15, group = lane >> 4;
     // workgroups b, b + 8, b + 16, ... share an XCD
     const int xcd = blockIdx.x & 7, in_xcd = blockIdx.x >> 3;
@@ -66,7 +72,7 @@ __global__ __launch_bounds__(WAVES * 64) void linear_stream_kernel(const FwdArgs
     const int walkers = (gridDim.x >> 3) / slices * 8, walker = in_xcd / slices * 8 + xcd;
     const int nn = a.n - n0 < slice_n ? a.n - n0 : slice_n;
     const int sets = (nn + 16 * FR - 1) / (16 * FR);
-    float *const bias = (float *)(lds + (size_t)(slice_n / 16) * KU * 1024), *const wsc = bias + slice_n;
+    float *const bias = (float *)(lds + (size_t)(slice_n / 16) * KU * kHalves * 1024), *const wsc = bias + slice_n;
 
     // The last fragment's piece of this lane.
     const Cut<T> last = cut_piece<T>((KU - 1) * kStretch<T> + group * kPiece<T>, a.k);
@@ -76,72 +82,111 @@ __global__ __launch_bounds__(WAVES * 64) void linear_stream_kernel(const FwdArgs
         return load_loose<u32x4>(row + group * kPiece<T> + u * kStretch<T>);
     };
 
-    for (int b = wave; b < sets * FR; b += WAVES) {
-        const int f = b % FR, s = b / FR;
-        const int n = s * 16 * FR + (row16 >> 2) * kOut + f * 4 + (row16 & 3);
+    for (int b = wave; b < sets * FR; b += kWaves) {
+        const int n = FR == 1 ? row16 : (b >> 1) * 32 + (row16 >> 2) * 8 + (b & 1) * 4 + (row16 & 3);
         const T *w = (const T *)a.w + (int64_t)(n0 + (n < nn ? n : nn - 1)) * a.ws;
 #pragma unroll
-        for (int u = 0; u < KU; ++u) wl[(b * KU + u) * 64 + lane] = piece(w, u);
+        for (int u = 0; u < KU; ++u) {
+            if constexpr (sizeof(T) == 1) {
+                const Widened v = widen(piece(w, u));
+                wl[((b * KU + u) * 2) * 64 + lane] = v.lo;
+                wl[((b * KU + u) * 2 + 1) * 64 + lane] = v.hi;
+            } else {
+                wl[(b * KU + u) * 64 + lane] = piece(w, u);
+            }
+        }
     }
-    for (int n = threadIdx.x; n < slice_n; n += WAVES * 64) {
+    for (int n = threadIdx.x; n < slice_n; n += kWaves * 64) {
         bias[n] = a.bias && n < nn ? a.bias[n0 + n] : 0.f;
         if constexpr (sizeof(T) == 1) wsc[n] = n < nn ? a.w_scale[n0 + n] : 0.f;
     }
     __syncthreads();
 
     const int64_t tiles = (a.m + RF * 16 - 1) / (RF * 16);
-    for (int64_t tile = (int64_t)wave * walkers + walker; tile < tiles; tile += (int64_t)WAVES * walkers) {
+    for (int64_t tile = (int64_t)wave * walkers + walker; tile < tiles; tile += (int64_t)kWaves * walkers) {
         const int64_t m0 = tile * (RF * 16) + row16;
-        Ready<T> x[RF][KU];
+        u32x4 x[RF][KU * (kWide ? 2 : 1)];
         float xsc[RF];
 #pragma unroll
         for (int r = 0; r < RF; ++r) {
             const int64_t m = m0 + r * 16 < a.m ? m0 + r * 16 : a.m - 1;
             const T *p = (const T *)a.x + m * a.xs;
 #pragma unroll
-            for (int u = 0; u < KU; ++u) x[r][u] = ready<T>(piece(p, u));
+            for (int u = 0; u < KU; ++u) x[r][u] = piece(p, u);
             if constexpr (sizeof(T) == 1) xsc[r] = a.x_scale[m];
         }
+        if constexpr (kWide)
+#pragma unroll
+            for (int r = 0; r < RF; ++r)
+#pragma unroll
+                for (int u = KU - 1; u >= 0; --u) {
+                    const Widened v = widen(x[r][u]);
+                    x[r][2 * u] = v.lo, x[r][2 * u + 1] = v.hi;
+                }
         for (int s = 0; s < sets; ++s) {
+            const int n = s * 16 * FR + group * kOut;  // this lane's outputs: kOut from n, and from n + 32
+            // The residual is asked for before the products.
+            Held<kOut, Y> res[RF][FR == 1 ? 1 : kPairs];
+            if (a.r)
+#pragma unroll
+                for (int r = 0; r < RF; ++r) {
+                    const int64_t m = m0 + r * 16 < a.m ? m0 + r * 16 : a.m - 1;
+#pragma unroll
+                    for (int q = 0; q < (FR == 1 ? 1 : kPairs); ++q)
+                        res[r][q] = hold<kOut>((const Y *)a.r + m * a.rs + n0 + n + q * 32, nn - n - q * 32);
+                }
             f32x4 acc[FR][RF];
 #pragma unroll
             for (int f = 0; f < FR; ++f)
 #pragma unroll
                 for (int r = 0; r < RF; ++r) acc[f][r] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int u = 0; u < KU; ++u)
+            for (int u = 0; u < KU; ++u) {
+                Widened xw[RF];
+                if constexpr (sizeof(T) == 1 && !kWide)
 #pragma unroll
-                for (int f = 0; f < FR; ++f) {
-                    const Ready<T> w = ready<T>(wl[((s * FR + f) * KU + u) * 64 + lane]);
+                    for (int r = 0; r < RF; ++r) xw[r] = widen(x[r][u]);
 #pragma unroll
-                    for (int r = 0; r < RF; ++r) acc[f][r] = mma<T>(w, x[r][u], acc[f][r]);
-                }
-            const int n = s * 16 * FR + group * kOut, left = nn - n;
-            float bs[kOut], ws[kOut];
+                for (int f = 0; f < FR; ++f)
 #pragma unroll
-            for (int j = 0; j < kOut; ++j) {
-                bs[j] = bias[n + j];
-                if constexpr (sizeof(T) == 1) ws[j] = wsc[n + j];
+                    for (int h = 0; h < kHalves; ++h) {
+                        const u32x4 w = wl[(((s * FR + f) * KU + u) * kHalves + h) * 64 + lane];
+#pragma unroll
+                        for (int r = 0; r < RF; ++r) {
+                            u32x4 v;
+                            if constexpr (sizeof(T) == 1 && !kWide) v = h ? xw[r].hi : xw[r].lo;
+                            else v = x[r][u * kHalves + h];
+                            acc[f][r] = mma16<T>(w, v, acc[f][r]);
+                        }
+                    }
             }
 #pragma unroll
-            for (int r = 0; r < RF; ++r) {
-                const int64_t m = m0 + r * 16;
-                if (m >= a.m) continue;
-                float z[kOut], res[kOut];
-                if (a.r) load_some<kOut>((const Y *)a.r + m * a.rs + n0 + n, left, res);
+            for (int q = 0; q < (FR == 1 ? 1 : kPairs); ++q) {
+                const int at = n + q * 32, left = nn - at;
+                float bs[kOut], ws[kOut];
 #pragma unroll
                 for (int j = 0; j < kOut; ++j) {
-                    z[j] = acc[j / 4][r][j % 4];
-                    if constexpr (sizeof(T) == 1) z[j] = z[j] * xsc[r] * ws[j];
-                    z[j] += bs[j];
+                    bs[j] = bias[at + j];
+                    if constexpr (sizeof(T) == 1) ws[j] = wsc[at + j];
                 }
-                if constexpr (sizeof(T) == 2)
-                    if (a.pre) store_some<kOut>((T *)a.pre + m * a.ps + n0 + n, left, z);
-                activate_all(z, a.act);
-                if (a.r)
 #pragma unroll
-                    for (int j = 0; j < kOut; ++j) z[j] += res[j];
-                store_some<kOut>((Y *)a.y + m * a.ys + n0 + n, left, z);
+                for (int r = 0; r < RF; ++r) {
+                    const int64_t m = m0 + r * 16;
+                    float z[kOut];
+#pragma unroll
+                    for (int j = 0; j < kOut; ++j) {
+                        z[j] = acc[q * 2 + j / 4][r][j % 4];
+                        if constexpr (sizeof(T) == 1) z[j] = z[j] * xsc[r] * ws[j];
+                        z[j] += bs[j];
+                    }
+                    if constexpr (sizeof(T) == 2)
+                        if (a.pre && m < a.m) store_some<kOut>((T *)a.pre + m * a.ps + n0 + at, left, z);
+                    activate_all(z, a.act);
+                    if (a.r)
+#pragma unroll
+                        for (int j = 0; j < kOut; ++j) z[j] += (float)res[r][q].v[j];
+                    if (m < a.m) store_some<kOut>((Y *)a.y + m * a.ys + n0 + at, left, z);
+                }
             }
         }
     }
@@ -149,57 +194,58 @@ __global__ __launch_bounds__(WAVES * 64) void linear_stream_kernel(const FwdArgs
 
 constexpr int kLdsBytes = 160 * 1024;
 
-template <typename T, typename Y, int KU, int RF, int WAVES, int FR, int kCut>
-hipError_t stream_launch(const FwdArgs &a, int slices, int slice_n, hipStream_t stream) {
-    const auto kernel = linear_stream_kernel<T, Y, KU, RF, WAVES, FR, kCut>;
-    const size_t bytes = (size_t)(slice_n / 16) * KU * 1024 + (size_t)slice_n * 8;
+template <typename T, typename Y, int KU, int RF, int FR, int kCut>
+hipError_t stream_launch(const FwdArgs &a, hipStream_t stream) {
+    const auto kernel = linear_stream_kernel<T, Y, KU, RF, FR, kCut>;
+    constexpr int per = KU * 64 * (sizeof(T) == 1 ? 2 : 1) + 8, set = 16 * FR;  // LDS bytes of an output; outputs of a set
+    const int fit = kLdsBytes / per / set * set;
+    int slices = (int)div_up(a.n, fit);
+    const int slice_n = (int)div_up(div_up(a.n, slices), set) * set;
+    slices = (int)div_up(a.n, slice_n);
+    const int bytes = slice_n * per;
     if (bytes > 65536) {
-        const hipError_t e = hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+        const hipError_t e = hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != hipSuccess) return e;
     }
     const int64_t tiles = div_up(a.m, RF * 16);
     int64_t walkers = kCus / slices;  // workgroups that share the rows
     if (walkers > tiles) walkers = tiles;
     walkers = div_up(walkers, 8) * 8;
-    kernel<<<dim3((unsigned)(walkers * slices)), WAVES * 64, bytes, stream>>>(a, slices, slice_n);
+    kernel<<<dim3((unsigned)(walkers * slices)), 1024, bytes, stream>>>(a, slices, slice_n);
     return hipGetLastError();
 }
 
-template <typename T, typename Y, int KU, int RF, int WAVES, int kCut>
-hipError_t stream_slices(const FwdArgs &a, hipStream_t stream) {
-    if (a.n <= 16) return stream_launch<T, Y, KU, RF, WAVES, 1, kCut>(a, 1, 16, stream);
-    const int fit = (kLdsBytes - 8192) / (KU * 64 + 8) / 32 * 32;  // outputs whose weights fit LDS
-    int slices = (int)div_up(a.n, fit);
-    const int slice_n = (int)div_up(div_up(a.n, slices), 32) * 32;
-    slices = (int)div_up(a.n, slice_n);
-    return stream_launch<T, Y, KU, RF, WAVES, 2, kCut>(a, slices, slice_n, stream);
+template <typename T, typename Y, int KU, int kCut>
+hipError_t stream_set(const FwdArgs &a, hipStream_t stream) {
+    if (a.n <= 16) return stream_launch<T, Y, KU, 1, 1, kCut>(a, stream);
+    if (a.n <= 32) return stream_launch<T, Y, KU, 1, 2, kCut>(a, stream);
+    return stream_launch<T, Y, KU, 1, 4, kCut>(a, stream);
 }
 
 // hipErrorNotSupported: not a case of this kernel.
 template <typename T, typename Y>
 hipError_t run_stream(const FwdArgs &a, hipStream_t stream) {
-    constexpr int W = sizeof(T) == 1 ? 8 : 16;
-    if (a.k < kPiece<T>) return stream_slices<T, Y, 1, 2, W, 2>(a, stream);
+    if (a.k < kPiece<T>) return stream_set<T, Y, 1, 2>(a, stream);
     const bool cut = a.k % kStretch<T> != 0;
     switch (div_up(a.k, kStretch<T>)) {
-#define HG_STREAM(KU, RF) \
-    case KU: return cut ? stream_slices<T, Y, KU, RF, W, 1>(a, stream) : stream_slices<T, Y, KU, RF, W, 0>(a, stream);
-        HG_STREAM(1, 2)
-        HG_STREAM(2, 2)
-        HG_STREAM(3, 2)
-        HG_STREAM(4, 2)
-        HG_STREAM(5, 2)
-        HG_STREAM(6, 2)
-        HG_STREAM(7, 2)
-        HG_STREAM(8, 2)
-        HG_STREAM(9, 1)
-        HG_STREAM(10, 1)
-        HG_STREAM(11, 1)
-        HG_STREAM(12, 1)
-        HG_STREAM(13, 1)
-        HG_STREAM(14, 1)
-        HG_STREAM(15, 1)
-        HG_STREAM(16, 1)
+#define HG_STREAM(KU) \
+    case KU: return cut ? stream_set<T, Y, KU, 1>(a, stream) : stream_set<T, Y, KU, 0>(a, stream);
+        HG_STREAM(1)
+        HG_STREAM(2)
+        HG_STREAM(3)
+        HG_STREAM(4)
+        HG_STREAM(5)
+        HG_STREAM(6)
+        HG_STREAM(7)
+        HG_STREAM(8)
+        HG_STREAM(9)
+        HG_STREAM(10)
+        HG_STREAM(11)
+        HG_STREAM(12)
+        HG_STREAM(13)
+        HG_STREAM(14)
+        HG_STREAM(15)
+        HG_STREAM(16)
 #undef HG_STREAM
     }
     return hipErrorNotSupported;
