@@ -107,14 +107,18 @@ __device__ __forceinline__ float logistic(float z) {
     return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504f * z));
 }
 
+// A product in which 0 times anything is 0 (v_mul_legacy_f32): an infinite z
+// meets a logistic of 0 in both activations and their slopes, and 0 is the limit.
+// A NaN z makes the other factor NaN too and stays.
+__device__ float fmul_legacy(float a, float b) __asm("llvm.amdgcn.fmul.legacy");
+__device__ __forceinline__ float mul0(float a, float b) { return fmul_legacy(a, b); }
+
 // act(z).  GELU is the tanh form: 0.5 z (1 + tanh u) = z logistic(2 u), with
-// u = sqrt(2 / pi) (z + 0.044715 z^3).  -inf gives 0 in both, as the limit has it.
+// u = sqrt(2 / pi) (z + 0.044715 z^3).
 __device__ __forceinline__ float activate(float z, int act) {
     if (act == HG_ACT_RELU) return z > 0.f ? z : z != z ? z : 0.f;
-    if (act == HG_ACT_SILU || act == HG_ACT_GELU_TANH) {
-        const float u = act == HG_ACT_SILU ? z : 1.59576912f * z * fmaf(0.044715f * z, z, 1.f);
-        return z == -__builtin_inff() ? 0.f : z * logistic(u);
-    }
+    if (act == HG_ACT_SILU) return mul0(z, logistic(z));
+    if (act == HG_ACT_GELU_TANH) return mul0(z, logistic(1.59576912f * z * fmaf(0.044715f * z, z, 1.f)));
     return z;
 }
 
@@ -137,12 +141,11 @@ __device__ __forceinline__ float slope(float z, int act) {
     if (act == HG_ACT_RELU) return z > 0.f ? 1.f : z != z ? z : 0.f;
     if (act == HG_ACT_SILU) {
         const float p = logistic(z);
-        return __builtin_isinf(z) ? p : p * fmaf(z, 1.f - p, 1.f);
+        return mul0(p, 1.f + mul0(z, 1.f - p));
     }
     if (act == HG_ACT_GELU_TANH) {
         const float p = logistic(1.59576912f * z * fmaf(0.044715f * z, z, 1.f));
-        const float q = 1.59576912f * z * fmaf(0.134145f * z, z, 1.f);
-        return p == 0.f || p == 1.f ? p : p * fmaf(q, 1.f - p, 1.f);
+        return mul0(p, 1.f + mul0(1.59576912f * z * fmaf(0.134145f * z, z, 1.f), 1.f - p));
     }
     return 1.f;
 }

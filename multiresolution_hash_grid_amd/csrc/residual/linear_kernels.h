@@ -61,10 +61,11 @@ __global__ __launch_bounds__(256) void linear_tile_kernel(const FwdArgs a) {
 template <typename T, typename Y, int KU, int RF, int FR, int kCut>
 __global__ __launch_bounds__(1024) void linear_stream_kernel(const FwdArgs a, int slices, int slice_n) {
     extern __shared__ __attribute__((aligned(16))) char lds[];
-    constexpr int kWaves = 16, kHalves = sizeof(T) == 1 ? 2 : 1;
+    constexpr int kHalves = sizeof(T) == 1 ? 2 : 1;
     constexpr int kPairs = FR / 2, kOut = FR == 1 ? 4 : 8;  // pairs of a set; consecutive outputs of a lane
-    constexpr bool kWide = sizeof(T) == 1 && KU <= 8;       // 8-bit rows are widened as they come; longer ones at each use
+    constexpr bool kWide = sizeof(T) == 1 && KU <= 4;       // 8-bit rows are widened as they come; longer ones at each use
     u32x4 *const wl = (u32x4 *)lds;
+    const int waves = blockDim.x >> 6;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, row16 = lane & 15, group = lane >> 4;
     // workgroups b, b + 8, b + 16, ... share an XCD
     const int xcd = blockIdx.x & 7, in_xcd = blockIdx.x >> 3;
@@ -82,7 +83,7 @@ __global__ __launch_bounds__(1024) void linear_stream_kernel(const FwdArgs a, in
         return load_loose<u32x4>(row + group * kPiece<T> + u * kStretch<T>);
     };
 
-    for (int b = wave; b < sets * FR; b += kWaves) {
+    for (int b = wave; b < sets * FR; b += waves) {
         const int n = FR == 1 ? row16 : (b >> 1) * 32 + (row16 >> 2) * 8 + (b & 1) * 4 + (row16 & 3);
         const T *w = (const T *)a.w + (int64_t)(n0 + (n < nn ? n : nn - 1)) * a.ws;
 #pragma unroll
@@ -96,14 +97,14 @@ __global__ __launch_bounds__(1024) void linear_stream_kernel(const FwdArgs a, in
             }
         }
     }
-    for (int n = threadIdx.x; n < slice_n; n += kWaves * 64) {
+    for (int n = threadIdx.x; n < slice_n; n += blockDim.x) {
         bias[n] = a.bias && n < nn ? a.bias[n0 + n] : 0.f;
         if constexpr (sizeof(T) == 1) wsc[n] = n < nn ? a.w_scale[n0 + n] : 0.f;
     }
     __syncthreads();
 
     const int64_t tiles = (a.m + RF * 16 - 1) / (RF * 16);
-    for (int64_t tile = (int64_t)wave * walkers + walker; tile < tiles; tile += (int64_t)kWaves * walkers) {
+    for (int64_t tile = (int64_t)wave * walkers + walker; tile < tiles; tile += (int64_t)waves * walkers) {
         const int64_t m0 = tile * (RF * 16) + row16;
         u32x4 x[RF][KU * (kWide ? 2 : 1)];
         float xsc[RF];
@@ -139,13 +140,20 @@ __global__ __launch_bounds__(1024) void linear_stream_kernel(const FwdArgs a, in
 #pragma unroll
             for (int f = 0; f < FR; ++f)
 #pragma unroll
-                for (int r = 0; r < RF; ++r) acc[f][r] = f32x4{0.f, 0.f, 0.f, 0.f};
+                for (int r = 0; r < RF; ++r) {
+                    // sums begin with the bias; 8-bit ones are scaled first
+                    if constexpr (sizeof(T) == 1) acc[f][r] = f32x4{0.f, 0.f, 0.f, 0.f};
+                    else acc[f][r] = *(const f32x4 *)(bias + n + (f >> 1) * 32 + (f & 1) * 4);
+                }
 #pragma unroll
             for (int u = 0; u < KU; ++u) {
                 Widened xw[RF];
                 if constexpr (sizeof(T) == 1 && !kWide)
 #pragma unroll
-                    for (int r = 0; r < RF; ++r) xw[r] = widen(x[r][u]);
+                    for (int r = 0; r < RF; ++r) {
+                        asm volatile("" : "+v"(x[r][u]));  // widen here, not once before all sets: the registers are not there
+                        xw[r] = widen(x[r][u]);
+                    }
 #pragma unroll
                 for (int f = 0; f < FR; ++f)
 #pragma unroll
@@ -164,11 +172,9 @@ __global__ __launch_bounds__(1024) void linear_stream_kernel(const FwdArgs a, in
             for (int q = 0; q < (FR == 1 ? 1 : kPairs); ++q) {
                 const int at = n + q * 32, left = nn - at;
                 float bs[kOut], ws[kOut];
+                if constexpr (sizeof(T) == 1)
 #pragma unroll
-                for (int j = 0; j < kOut; ++j) {
-                    bs[j] = bias[at + j];
-                    if constexpr (sizeof(T) == 1) ws[j] = wsc[at + j];
-                }
+                    for (int j = 0; j < kOut; ++j) bs[j] = bias[at + j], ws[j] = wsc[at + j];
 #pragma unroll
                 for (int r = 0; r < RF; ++r) {
                     const int64_t m = m0 + r * 16;
@@ -176,8 +182,7 @@ __global__ __launch_bounds__(1024) void linear_stream_kernel(const FwdArgs a, in
 #pragma unroll
                     for (int j = 0; j < kOut; ++j) {
                         z[j] = acc[q * 2 + j / 4][r][j % 4];
-                        if constexpr (sizeof(T) == 1) z[j] = z[j] * xsc[r] * ws[j];
-                        z[j] += bs[j];
+                        if constexpr (sizeof(T) == 1) z[j] = fmaf(z[j] * xsc[r], ws[j], bs[j]);
                     }
                     if constexpr (sizeof(T) == 2)
                         if (a.pre && m < a.m) store_some<kOut>((T *)a.pre + m * a.ps + n0 + at, left, z);
@@ -207,11 +212,15 @@ hipError_t stream_launch(const FwdArgs &a, hipStream_t stream) {
         const hipError_t e = hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != hipSuccess) return e;
     }
+    // 16 waves a CU in one workgroup, or in two of eight where two slices fit its
+    // LDS (three where the registers allow six waves a SIMD): they start and end
+    // apart, and the last tiles are dealt more evenly.
+    const int groups = bytes > kLdsBytes / 2 ? 1 : KU > 1 || bytes > kLdsBytes / 3 ? 2 : 3;
     const int64_t tiles = div_up(a.m, RF * 16);
-    int64_t walkers = kCus / slices;  // workgroups that share the rows
+    int64_t walkers = kCus * groups / slices;  // workgroups that share the rows
     if (walkers > tiles) walkers = tiles;
     walkers = div_up(walkers, 8) * 8;
-    kernel<<<dim3((unsigned)(walkers * slices)), 1024, bytes, stream>>>(a, slices, slice_n);
+    kernel<<<dim3((unsigned)(walkers * slices)), groups == 1 ? 1024 : 512, bytes, stream>>>(a, slices, slice_n);
     return hipGetLastError();
 }
 
