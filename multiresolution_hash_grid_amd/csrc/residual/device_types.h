@@ -101,43 +101,6 @@ __device__ __forceinline__ void store8(T *p, int left, const float (&v)[8]) {
     }
 }
 
-// The same for 8 or 4 values.
-template <int N, typename T>
-__device__ __forceinline__ void load_some(const T *p, int left, float (&v)[N]) {
-    if constexpr (N == 8) {
-        load8(p, left, v);
-    } else if (left >= 4) {
-        typedef T T4 __attribute__((ext_vector_type(4)));
-        const T4 a = load_loose<T4>(p);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = (float)a[j];
-    } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            v[j] = 0.f;
-            if (j < left) v[j] = (float)p[j];
-        }
-    }
-}
-template <int N, typename T>
-__device__ __forceinline__ void store_some(T *p, int left, const float (&v)[N]) {
-    if constexpr (N == 8) {
-        store8(p, left, v);
-    } else {
-        typedef T T4 __attribute__((ext_vector_type(4)));
-        T4 a;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) a[j] = (T)v[j];
-        if (left >= 4) {
-            store_loose<T4>(p, a);
-            return;
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (j < left) p[j] = a[j];
-    }
-}
-
 // N values as they lie in memory, to be held until they are used.
 template <int N, typename T>
 struct Held {
@@ -157,6 +120,24 @@ __device__ __forceinline__ Held<N, T> hold(const T *p, int left) {
         }
     }
     return h;
+}
+
+template <int N, typename T>
+__device__ __forceinline__ Held<N, T> rounded(const float (&v)[N]) {
+    Held<N, T> h;
+#pragma unroll
+    for (int j = 0; j < N; ++j) h.v[j] = (T)v[j];
+    return h;
+}
+template <int N, typename T>
+__device__ __forceinline__ void put(T *p, int left, Held<N, T> h) {
+    if (left >= N) {
+        store_loose(p, h.v);
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+        if (j < left) p[j] = h.v[j];
 }
 
 // Sum over aligned groups of G lanes, in every lane of the group.

@@ -44,7 +44,7 @@ __global__ __launch_bounds__(256) void linear_tile_kernel(const FwdArgs a) {
 // Many rows, a weight that fits LDS in a few slices.  A workgroup keeps its
 // slice of W in LDS for good, in fragment order (a wave reads 1 KB in a row,
 // without conflicts; 8-bit weights are widened once, here), and its waves walk
-// row tiles of RF * 16 rows on their own: a tile's rows go straight from memory
+// row tiles of 16 rows on their own: a tile's rows go straight from memory
 // into registers as fragments, all of the contraction at once, and each set of
 // FR 16-output fragments is finished -- bias, activation, residual, rounding --
 // before the next is begun.  No barrier after the start: the waves of a CU hide
@@ -53,16 +53,18 @@ __global__ __launch_bounds__(256) void linear_tile_kernel(const FwdArgs a) {
 // of one row: row i of fragment h is output (i / 4) * 8 + h * 4 + i % 4.  A set of
 // two pairs reads and writes whole 128-byte lines (16-bit outputs): with one pair
 // a set, half lines left L2 before their other halves came, and 1.35 times the
-// bytes were written and 1.45 times read (2^20 x 256 x 256).
+// bytes were written and 1.45 times read (2^20 x 256 x 256).  The outputs of GS
+// sets are held, rounded, and stored together: rows of 512 bytes written in runs
+// of 128, 256 and 512 bytes go to memory at 3.6, 4.7 and 5.5 TB/s.
 // Slices of W are workgroups next to each other on one XCD that walk the same
 // rows, so x comes from HBM once.
 // kCut: 0 the contraction is whole fragments; 1 its last fragment is cut; 2 it
 // is shorter than a piece.
-template <typename T, typename Y, int KU, int RF, int FR, int kCut>
+template <typename T, typename Y, int KU, int FR, int GS, int kCut>
 __global__ __launch_bounds__(1024) void linear_stream_kernel(const FwdArgs a, int slices, int slice_n) {
     extern __shared__ __attribute__((aligned(16))) char lds[];
     constexpr int kHalves = sizeof(T) == 1 ? 2 : 1;
-    constexpr int kPairs = FR / 2, kOut = FR == 1 ? 4 : 8;  // pairs of a set; consecutive outputs of a lane
+    constexpr int kPairs = FR == 1 ? 1 : FR / 2, kOut = FR == 1 ? 4 : 8;  // pairs of a set; consecutive outputs of a lane
     constexpr bool kWide = sizeof(T) == 1 && KU <= 4;       // 8-bit rows are widened as they come; longer ones at each use
     u32x4 *const wl = (u32x4 *)lds;
     const int waves = blockDim.x >> 6;
@@ -103,105 +105,96 @@ __global__ __launch_bounds__(1024) void linear_stream_kernel(const FwdArgs a, in
     }
     __syncthreads();
 
-    const int64_t tiles = (a.m + RF * 16 - 1) / (RF * 16);
+    const int64_t tiles = (a.m + 15) / 16;
     for (int64_t tile = (int64_t)wave * walkers + walker; tile < tiles; tile += (int64_t)waves * walkers) {
-        const int64_t m0 = tile * (RF * 16) + row16;
-        u32x4 x[RF][KU * (kWide ? 2 : 1)];
-        float xsc[RF];
+        const bool there = tile * 16 + row16 < a.m;
+        const int64_t m = there ? tile * 16 + row16 : a.m - 1;
+        u32x4 x[KU * (kWide ? 2 : 1)];
+        float xsc;
 #pragma unroll
-        for (int r = 0; r < RF; ++r) {
-            const int64_t m = m0 + r * 16 < a.m ? m0 + r * 16 : a.m - 1;
-            const T *p = (const T *)a.x + m * a.xs;
-#pragma unroll
-            for (int u = 0; u < KU; ++u) x[r][u] = piece(p, u);
-            if constexpr (sizeof(T) == 1) xsc[r] = a.x_scale[m];
-        }
+        for (int u = 0; u < KU; ++u) x[u] = piece((const T *)a.x + m * a.xs, u);
+        if constexpr (sizeof(T) == 1) xsc = a.x_scale[m];
         if constexpr (kWide)
 #pragma unroll
-            for (int r = 0; r < RF; ++r)
-#pragma unroll
-                for (int u = KU - 1; u >= 0; --u) {
-                    const Widened v = widen(x[r][u]);
-                    x[r][2 * u] = v.lo, x[r][2 * u + 1] = v.hi;
-                }
-        for (int s = 0; s < sets; ++s) {
-            const int n = s * 16 * FR + group * kOut;  // this lane's outputs: kOut from n, and from n + 32
-            // The residual is asked for before the products.
-            Held<kOut, Y> res[RF][FR == 1 ? 1 : kPairs];
-            if (a.r)
-#pragma unroll
-                for (int r = 0; r < RF; ++r) {
-                    const int64_t m = m0 + r * 16 < a.m ? m0 + r * 16 : a.m - 1;
-#pragma unroll
-                    for (int q = 0; q < (FR == 1 ? 1 : kPairs); ++q)
-                        res[r][q] = hold<kOut>((const Y *)a.r + m * a.rs + n0 + n + q * 32, nn - n - q * 32);
-                }
-            f32x4 acc[FR][RF];
-#pragma unroll
-            for (int f = 0; f < FR; ++f)
-#pragma unroll
-                for (int r = 0; r < RF; ++r) {
-                    // sums begin with the bias; 8-bit ones are scaled first
-                    if constexpr (sizeof(T) == 1) acc[f][r] = f32x4{0.f, 0.f, 0.f, 0.f};
-                    else acc[f][r] = *(const f32x4 *)(bias + n + (f >> 1) * 32 + (f & 1) * 4);
-                }
-#pragma unroll
-            for (int u = 0; u < KU; ++u) {
-                Widened xw[RF];
-                if constexpr (sizeof(T) == 1 && !kWide)
-#pragma unroll
-                    for (int r = 0; r < RF; ++r) {
-                        asm volatile("" : "+v"(x[r][u]));  // widen here, not once before all sets: the registers are not there
-                        xw[r] = widen(x[r][u]);
-                    }
-#pragma unroll
-                for (int f = 0; f < FR; ++f)
-#pragma unroll
-                    for (int h = 0; h < kHalves; ++h) {
-                        const u32x4 w = wl[(((s * FR + f) * KU + u) * kHalves + h) * 64 + lane];
-#pragma unroll
-                        for (int r = 0; r < RF; ++r) {
-                            u32x4 v;
-                            if constexpr (sizeof(T) == 1 && !kWide) v = h ? xw[r].hi : xw[r].lo;
-                            else v = x[r][u * kHalves + h];
-                            acc[f][r] = mma16<T>(w, v, acc[f][r]);
-                        }
-                    }
+            for (int u = KU - 1; u >= 0; --u) {
+                const Widened v = widen(x[u]);
+                x[2 * u] = v.lo, x[2 * u + 1] = v.hi;
             }
+        for (int s0 = 0; s0 < sets; s0 += GS) {
+            Held<kOut, Y> y[GS][kPairs];
+            typedef std::conditional_t<sizeof(T) == 1, f16, T> P;  // (8-bit operands keep no pre-activation)
+            Held<kOut, P> pre[GS][kPairs];
 #pragma unroll
-            for (int q = 0; q < (FR == 1 ? 1 : kPairs); ++q) {
-                const int at = n + q * 32, left = nn - at;
-                float bs[kOut], ws[kOut];
-                if constexpr (sizeof(T) == 1)
+            for (int i = 0; i < GS; ++i) {
+                const int s = s0 + i;
+                if (s >= sets) break;
+                const int n = s * 16 * FR + group * kOut;  // this lane's outputs: kOut from n, and from n + 32
+                // The residual is asked for before the products.
+                Held<kOut, Y> res[kPairs];
+                if (a.r)
 #pragma unroll
-                    for (int j = 0; j < kOut; ++j) bs[j] = bias[at + j], ws[j] = wsc[at + j];
+                    for (int q = 0; q < kPairs; ++q)
+                        res[q] = hold<kOut>((const Y *)a.r + m * a.rs + n0 + n + q * 32, nn - n - q * 32);
+                f32x4 acc[FR];
 #pragma unroll
-                for (int r = 0; r < RF; ++r) {
-                    const int64_t m = m0 + r * 16;
+                for (int f = 0; f < FR; ++f) {
+                    // sums begin with the bias; 8-bit ones are scaled first
+                    if constexpr (sizeof(T) == 1) acc[f] = f32x4{0.f, 0.f, 0.f, 0.f};
+                    else acc[f] = *(const f32x4 *)(bias + n + (f >> 1) * 32 + (f & 1) * 4);
+                }
+#pragma unroll
+                for (int u = 0; u < KU; ++u) {
+                    Widened xw;
+                    if constexpr (sizeof(T) == 1 && !kWide) {
+                        asm volatile("" : "+v"(x[u]));  // widen here, not once before all sets: the registers are not there
+                        xw = widen(x[u]);
+                    }
+#pragma unroll
+                    for (int f = 0; f < FR; ++f)
+#pragma unroll
+                        for (int h = 0; h < kHalves; ++h) {
+                            const u32x4 w = wl[(((s * FR + f) * KU + u) * kHalves + h) * 64 + lane];
+                            u32x4 v;
+                            if constexpr (sizeof(T) == 1 && !kWide) v = h ? xw.hi : xw.lo;
+                            else v = x[u * kHalves + h];
+                            acc[f] = mma16<T>(w, v, acc[f]);
+                        }
+                }
+#pragma unroll
+                for (int q = 0; q < kPairs; ++q) {
                     float z[kOut];
 #pragma unroll
                     for (int j = 0; j < kOut; ++j) {
-                        z[j] = acc[q * 2 + j / 4][r][j % 4];
-                        if constexpr (sizeof(T) == 1) z[j] = fmaf(z[j] * xsc[r], ws[j], bs[j]);
+                        z[j] = acc[q * 2 + j / 4][j % 4];
+                        if constexpr (sizeof(T) == 1) z[j] = fmaf(z[j] * xsc, wsc[n + q * 32 + j], bias[n + q * 32 + j]);
                     }
                     if constexpr (sizeof(T) == 2)
-                        if (a.pre && m < a.m) store_some<kOut>((T *)a.pre + m * a.ps + n0 + at, left, z);
+                        if (a.pre) pre[i][q] = rounded<kOut, T>(z);
                     activate_all(z, a.act);
                     if (a.r)
 #pragma unroll
-                        for (int j = 0; j < kOut; ++j) z[j] += (float)res[r][q].v[j];
-                    if (m < a.m) store_some<kOut>((Y *)a.y + m * a.ys + n0 + at, left, z);
+                        for (int j = 0; j < kOut; ++j) z[j] += (float)res[q].v[j];
+                    y[i][q] = rounded<kOut, Y>(z);
                 }
             }
+            if (!there) continue;
+            const int at = n0 + s0 * 16 * FR + group * kOut, left = n0 + nn - at;
+            if constexpr (sizeof(T) == 2)
+                if (a.pre)
+#pragma unroll
+                    for (int q = 0; q < GS * kPairs; ++q)
+                        put((T *)a.pre + m * a.ps + at + q * 32, left - q * 32, pre[q / kPairs][q % kPairs]);
+#pragma unroll
+            for (int q = 0; q < GS * kPairs; ++q) put((Y *)a.y + m * a.ys + at + q * 32, left - q * 32, y[q / kPairs][q % kPairs]);
         }
     }
 }
 
 constexpr int kLdsBytes = 160 * 1024;
 
-template <typename T, typename Y, int KU, int RF, int FR, int kCut>
+template <typename T, typename Y, int KU, int FR, int GS, int kCut>
 hipError_t stream_launch(const FwdArgs &a, hipStream_t stream) {
-    const auto kernel = linear_stream_kernel<T, Y, KU, RF, FR, kCut>;
+    const auto kernel = linear_stream_kernel<T, Y, KU, FR, GS, kCut>;
     constexpr int per = KU * 64 * (sizeof(T) == 1 ? 2 : 1) + 8, set = 16 * FR;  // LDS bytes of an output; outputs of a set
     const int fit = kLdsBytes / per / set * set;
     int slices = (int)div_up(a.n, fit);
@@ -216,7 +209,7 @@ hipError_t stream_launch(const FwdArgs &a, hipStream_t stream) {
     // LDS (three where the registers allow six waves a SIMD): they start and end
     // apart, and the last tiles are dealt more evenly.
     const int groups = bytes > kLdsBytes / 2 ? 1 : KU > 1 || bytes > kLdsBytes / 3 ? 2 : 3;
-    const int64_t tiles = div_up(a.m, RF * 16);
+    const int64_t tiles = div_up(a.m, 16);
     int64_t walkers = kCus * groups / slices;  // workgroups that share the rows
     if (walkers > tiles) walkers = tiles;
     walkers = div_up(walkers, 8) * 8;
@@ -227,8 +220,9 @@ hipError_t stream_launch(const FwdArgs &a, hipStream_t stream) {
 template <typename T, typename Y, int KU, int kCut>
 hipError_t stream_set(const FwdArgs &a, hipStream_t stream) {
     if (a.n <= 16) return stream_launch<T, Y, KU, 1, 1, kCut>(a, stream);
-    if (a.n <= 32) return stream_launch<T, Y, KU, 1, 2, kCut>(a, stream);
-    return stream_launch<T, Y, KU, 1, 4, kCut>(a, stream);
+    if (a.n <= 32) return stream_launch<T, Y, KU, 2, 1, kCut>(a, stream);
+    constexpr int GS = sizeof(Y) == 4 ? (KU <= 4 ? 2 : 1) : KU <= 12 ? 2 : 1;  // what the registers hold
+    return stream_launch<T, Y, KU, 4, GS, kCut>(a, stream);
 }
 
 // hipErrorNotSupported: not a case of this kernel.
