@@ -41,6 +41,38 @@ __global__ __launch_bounds__(256) void linear_tile_kernel(const FwdArgs a) {
     ((Y *)a.y)[m * a.ys + n] = (Y)y;
 }
 
+// A wave's buffer of 16 rows by 512 bytes: 8 values of 16 or 32 bits are one or
+// two pieces of 16 bytes, permuted in their row by the row's number.
+constexpr int kStageBytes = 16 * 512;
+template <typename V>
+__device__ __forceinline__ void stage_put(char *stage, int row, int eight, Held<8, V> h) {
+    if constexpr (sizeof(V) == 2) {
+        *(u32x4 *)(stage + row * 512 + ((eight ^ row) << 4)) = __builtin_bit_cast(u32x4, h.v);
+    } else {
+        f32x4 lo, hi;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) lo[j] = h.v[j], hi[j] = h.v[4 + j];
+        *(f32x4 *)(stage + row * 512 + (((2 * eight) ^ row) << 4)) = lo;
+        *(f32x4 *)(stage + row * 512 + (((2 * eight + 1) ^ row) << 4)) = hi;
+    }
+}
+// The first `pairs` * 32 values of each row to columns n .. of rows m1 ..; only
+// rows below `rows` and columns below `width` exist.  The wave's own writes are
+// in order before its reads.
+template <typename V>
+__device__ __forceinline__ void stage_store(V *y, int64_t stride, int64_t m1, int64_t rows, int n, int width, const char *stage,
+                                            int pairs, int lane) {
+    constexpr int per = 16 / (int)sizeof(V);  // values of a piece
+    const int pieces = pairs * 32 / per;      // of a row: a multiple of 4
+#pragma unroll 1
+    for (int at = lane; at < pieces * 16; at += 64) {
+        const int row = at / pieces, c = at - row * pieces;
+        typedef V VP __attribute__((ext_vector_type(16 / (int)sizeof(V))));
+        const Held<per, V> h = {__builtin_bit_cast(VP, *(const u32x4 *)(stage + row * 512 + ((c ^ row) << 4)))};
+        if (m1 + row < rows) put(y + (m1 + row) * stride + n + c * per, width - n - c * per, h);
+    }
+}
+
 // Many rows, a weight that fits LDS in a few slices.  A workgroup keeps its
 // slice of W in LDS for good, in fragment order (a wave reads 1 KB in a row,
 // without conflicts; 8-bit weights are widened once, here), and its waves walk
@@ -56,11 +88,14 @@ __global__ __launch_bounds__(256) void linear_tile_kernel(const FwdArgs a) {
 // bytes were written and 1.45 times read (2^20 x 256 x 256).  The outputs of GS
 // sets are held, rounded, and stored together: rows of 512 bytes written in runs
 // of 128, 256 and 512 bytes go to memory at 3.6, 4.7 and 5.5 TB/s.
+// kStage: where the weights leave LDS room, 512 bytes of each row are collected in
+// a buffer of the wave's own, pieces permuted against bank conflicts, and stored
+// 1 KB at a time in memory order (2^18 x 32 x 256 with z kept: 74 -> 62 us).
 // Slices of W are workgroups next to each other on one XCD that walk the same
 // rows, so x comes from HBM once.
 // kCut: 0 the contraction is whole fragments; 1 its last fragment is cut; 2 it
 // is shorter than a piece.
-template <typename T, typename Y, int KU, int FR, int GS, int kCut>
+template <typename T, typename Y, int KU, int FR, int GS, int kCut, bool kStage>
 __global__ __launch_bounds__(1024) void linear_stream_kernel(const FwdArgs a, int slices, int slice_n) {
     extern __shared__ __attribute__((aligned(16))) char lds[];
     constexpr int kHalves = sizeof(T) == 1 ? 2 : 1;
@@ -76,6 +111,7 @@ __global__ __launch_bounds__(1024) void linear_stream_kernel(const FwdArgs a, in
     const int nn = a.n - n0 < slice_n ? a.n - n0 : slice_n;
     const int sets = (nn + 16 * FR - 1) / (16 * FR);
     float *const bias = (float *)(lds + (size_t)(slice_n / 16) * KU * kHalves * 1024), *const wsc = bias + slice_n;
+    char *const stage = (char *)(wsc + slice_n) + wave * kStageBytes;
 
     // The last fragment's piece of this lane.
     const Cut<T> last = cut_piece<T>((KU - 1) * kStretch<T> + group * kPiece<T>, a.k);
@@ -121,7 +157,7 @@ __global__ __launch_bounds__(1024) void linear_stream_kernel(const FwdArgs a, in
                 x[2 * u] = v.lo, x[2 * u + 1] = v.hi;
             }
         for (int s0 = 0; s0 < sets; s0 += GS) {
-            Held<kOut, Y> y[GS][kPairs];
+            Held<kOut, Y> y[kStage ? 1 : GS][kPairs];
             typedef std::conditional_t<sizeof(T) == 1, f16, T> P;  // (8-bit operands keep no pre-activation)
             Held<kOut, P> pre[GS][kPairs];
 #pragma unroll
@@ -174,8 +210,22 @@ __global__ __launch_bounds__(1024) void linear_stream_kernel(const FwdArgs a, in
                     if (a.r)
 #pragma unroll
                         for (int j = 0; j < kOut; ++j) z[j] += (float)res[q].v[j];
-                    y[i][q] = rounded<kOut, Y>(z);
+                    if constexpr (kStage) stage_put(stage, row16, (i * kPairs + q) * 4 + group, rounded<kOut, Y>(z));
+                    else y[i][q] = rounded<kOut, Y>(z);
                 }
+            }
+            if constexpr (kStage) {
+                const int count = (sets - s0 < GS ? sets - s0 : GS) * kPairs;  // pairs of this round
+                const int64_t m1 = tile * 16;
+                stage_store((Y *)a.y, a.ys, m1, a.m, n0 + s0 * 16 * FR, n0 + nn, stage, count, lane);
+                if constexpr (sizeof(T) == 2)
+                    if (a.pre) {
+#pragma unroll
+                        for (int q = 0; q < GS * kPairs; ++q)
+                            if (q < count) stage_put(stage, row16, q * 4 + group, pre[q / kPairs][q % kPairs]);
+                        stage_store((T *)a.pre, a.ps, m1, a.m, n0 + s0 * 16 * FR, n0 + nn, stage, count, lane);
+                    }
+                continue;
             }
             if (!there) continue;
             const int at = n0 + s0 * 16 * FR + group * kOut, left = n0 + nn - at;
@@ -185,22 +235,26 @@ __global__ __launch_bounds__(1024) void linear_stream_kernel(const FwdArgs a, in
                     for (int q = 0; q < GS * kPairs; ++q)
                         put((T *)a.pre + m * a.ps + at + q * 32, left - q * 32, pre[q / kPairs][q % kPairs]);
 #pragma unroll
-            for (int q = 0; q < GS * kPairs; ++q) put((Y *)a.y + m * a.ys + at + q * 32, left - q * 32, y[q / kPairs][q % kPairs]);
+            for (int q = 0; q < (kStage ? 0 : GS * kPairs); ++q)
+                put((Y *)a.y + m * a.ys + at + q * 32, left - q * 32, y[kStage ? 0 : q / kPairs][q % kPairs]);
         }
     }
 }
 
 constexpr int kLdsBytes = 160 * 1024;
+// LDS of one output's weights, bias and scale.
+template <typename T, int KU>
+constexpr int kWeightBytes = KU * 64 * (sizeof(T) == 1 ? 2 : 1) + 8;
 
-template <typename T, typename Y, int KU, int FR, int GS, int kCut>
+template <typename T, typename Y, int KU, int FR, int GS, int kCut, bool kStage = false>
 hipError_t stream_launch(const FwdArgs &a, hipStream_t stream) {
-    const auto kernel = linear_stream_kernel<T, Y, KU, FR, GS, kCut>;
-    constexpr int per = KU * 64 * (sizeof(T) == 1 ? 2 : 1) + 8, set = 16 * FR;  // LDS bytes of an output; outputs of a set
+    const auto kernel = linear_stream_kernel<T, Y, KU, FR, GS, kCut, kStage>;
+    constexpr int per = kWeightBytes<T, KU>, set = 16 * FR;  // LDS bytes of an output; outputs of a set
     const int fit = kLdsBytes / per / set * set;
     int slices = (int)div_up(a.n, fit);
     const int slice_n = (int)div_up(div_up(a.n, slices), set) * set;
     slices = (int)div_up(a.n, slice_n);
-    const int bytes = slice_n * per;
+    const int bytes = slice_n * per + (kStage ? 16 * kStageBytes : 0);
     if (bytes > 65536) {
         const hipError_t e = hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != hipSuccess) return e;
@@ -221,6 +275,10 @@ template <typename T, typename Y, int KU, int kCut>
 hipError_t stream_set(const FwdArgs &a, hipStream_t stream) {
     if (a.n <= 16) return stream_launch<T, Y, KU, 1, 1, kCut>(a, stream);
     if (a.n <= 32) return stream_launch<T, Y, KU, 2, 1, kCut>(a, stream);
+    if (a.n <= 64) return stream_launch<T, Y, KU, 4, 1, kCut>(a, stream);
+    if constexpr (KU <= 4)  // rows of more than one set, weights beside 16 waves' buffers
+        if (div_up(a.n, 64) * 64 * kWeightBytes<T, KU> <= kLdsBytes - 16 * kStageBytes)
+            return stream_launch<T, Y, KU, 4, sizeof(Y) == 4 ? 2 : 4, kCut, true>(a, stream);
     constexpr int GS = sizeof(Y) == 4 ? (KU <= 4 ? 2 : 1) : KU <= 12 ? 2 : 1;  // what the registers hold
     return stream_launch<T, Y, KU, 4, GS, kCut>(a, stream);
 }
