@@ -8,13 +8,13 @@ in the HIP kernels of the library and there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import struct
 from dataclasses import dataclass
 from typing import NamedTuple
 
 import torch
 
-from .hashgrid import (HG_ADAM_ZERO_GRAD, HG_F16, HG_F32, _check, _dev, _keep_for_stream, _stream,
-                       _workspace, load_library)
+from .hashgrid import (HG_ADAM_ZERO_GRAD, HG_F16, HG_F32, _check, _dev, _keep_for_stream, _stream, load_library)
 
 HG_BF16, HG_F8 = 2, 3
 HG_ACT = {"none": 0, "relu": 1, "silu": 2, "gelu_tanh": 3}
@@ -61,6 +61,22 @@ class _AdamW(ctypes.Structure):
     _fields_ = [("beta1", _F), ("beta2", _F), ("eps", _F), ("step", _I32), ("seed", ctypes.c_uint32)]
 
 
+def _packer(structure):
+    """struct.Struct of a ctypes structure: packing the fields' values into bytes costs a quarter of building it."""
+    codes, at = "@", 0
+    for name, kind in structure._fields_:
+        field = getattr(structure, name)
+        codes += f"{field.offset - at}x" if field.offset > at else ""
+        codes += {_P: "Q", _I64: "q", _I32: "i", _F: "f", ctypes.c_uint32: "I"}[kind]
+        at = field.offset + field.size
+    codes += f"{ctypes.sizeof(structure) - at}x" if ctypes.sizeof(structure) > at else ""
+    packer = struct.Struct(codes)
+    assert packer.size == ctypes.sizeof(structure)
+    return packer.pack
+
+
+_linear, _linear_grad, _rms_norm, _rms_norm_grad = (_packer(t) for t in (_Linear, _LinearGrad, _RmsNorm, _RmsNormGrad))
+
 _bound = None
 
 
@@ -83,23 +99,37 @@ def _lib() -> ctypes.CDLL:
     return _bound
 
 
-def _rows(t, name, shape, dtype, like) -> int:
+def _rows(t, name, shape, dtype, device) -> int:
     """Row stride of a matrix argument, after its checks."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.device != like.device:
-        raise ValueError(f"{name} must be a tensor on {like.device}")
+    if not isinstance(t, torch.Tensor) or t.device != device:
+        raise ValueError(f"{name} must be a tensor on {device}")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape or (t.stride(1) != 1 and shape[1] > 1):
-        raise ValueError(f"{name} must be [{shape[0]}, {shape[1]}] with unit column stride")
-    return t.stride(0)
+    if t.shape != shape:
+        raise ValueError(f"{name} must be [{shape[0]}, {shape[1]}], got {list(t.shape)}")
+    row, column = t.stride()
+    if column != 1 and shape[1] > 1:
+        raise ValueError(f"{name} must have unit column stride")
+    return row
 
 
-def _vector(t, name, n, like) -> int:
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.device != like.device or t.dtype != torch.float32:
-        raise ValueError(f"{name} must be a float32 tensor on {like.device}")
-    if t.dim() != 1 or t.shape[0] != n or (t.stride(0) != 1 and n > 1):
+def _vector(t, name, n, device) -> int:
+    if not isinstance(t, torch.Tensor) or t.device != device or t.dtype != torch.float32:
+        raise ValueError(f"{name} must be a float32 tensor on {device}")
+    if t.shape != (n,) or (n > 1 and t.stride(0) != 1):
         raise ValueError(f"{name} must be a contiguous [{n}] tensor")
     return t.data_ptr()
+
+
+#: The current stream's handle by device index; building a Stream object for it costs 1.5 us a call more.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
+
+
+def _here(device, stream) -> int:
+    """The stream of a call as an integer handle."""
+    if stream is None:
+        return _raw_stream(device.index)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _act(act) -> int:
@@ -126,24 +156,26 @@ def hashgrid_linear_forward(x: torch.Tensor, weight: torch.Tensor, bias: torch.T
     _matrix(weight, "weight")
     m, k = x.shape
     n = weight.shape[0]
-    eight = x.dtype == F8
+    dtype, device, mn = x.dtype, x.device, (m, n)
     if out_dtype is None:
-        out_dtype = out.dtype if out is not None else torch.bfloat16 if eight else x.dtype
-    made = out is None
-    y = torch.empty((m, n), dtype=out_dtype, device=x.device) if made else out
-    pre = torch.empty((m, n), dtype=x.dtype, device=x.device) if save_pre else None
-    op = _Linear(m, k, n, x.data_ptr(), _rows(x, "x", (m, k), x.dtype, x),
-                 weight.data_ptr(), _rows(weight, "weight", (n, k), x.dtype, x),
-                 None if x_scale is None else _vector(x_scale, "x_scale", m, x),
-                 None if weight_scale is None else _vector(weight_scale, "weight_scale", n, x),
-                 None if bias is None else _vector(bias, "bias", n, x),
-                 None if residual is None else residual.data_ptr(),
-                 0 if residual is None else _rows(residual, "residual", (m, n), out_dtype, x),
-                 y.data_ptr(), y.stride(0) if made else _rows(y, "out", (m, n), out_dtype, x),
-                 None if pre is None else pre.data_ptr(), n, _CODES[x.dtype], _CODES.get(out_dtype, -1), _act(act))
-    _check(_lib().hashgrid_linear_forward(ctypes.byref(op), _stream(x, stream)))
+        out_dtype = out.dtype if out is not None else torch.bfloat16 if dtype == F8 else dtype
+    if out is None:
+        y, ys = torch.empty(mn, dtype=out_dtype, device=device), n
+    else:
+        y, ys = out, _rows(out, "out", mn, out_dtype, device)
+    pre = torch.empty(mn, dtype=dtype, device=device) if save_pre else None
+    op = _linear(m, k, n, x.data_ptr(), _rows(x, "x", (m, k), dtype, device),
+                 weight.data_ptr(), _rows(weight, "weight", (n, k), dtype, device),
+                 0 if x_scale is None else _vector(x_scale, "x_scale", m, device),
+                 0 if weight_scale is None else _vector(weight_scale, "weight_scale", n, device),
+                 0 if bias is None else _vector(bias, "bias", n, device),
+                 0 if residual is None else residual.data_ptr(),
+                 0 if residual is None else _rows(residual, "residual", mn, out_dtype, device),
+                 y.data_ptr(), ys, 0 if pre is None else pre.data_ptr(), n, _CODES[dtype], _CODES.get(out_dtype, -1), _act(act))
+    if (rc := _lib().hashgrid_linear_forward(op, _here(device, stream))):
+        _check(rc)
     if stream is not None:
-        _keep_for_stream(x, stream, y if made else None, pre)
+        _keep_for_stream(x, stream, y if out is None else None, pre)
     return (y, pre) if save_pre else y
 
 
@@ -161,44 +193,67 @@ def hashgrid_linear_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Te
     _matrix(weight, "weight")
     m, k = x.shape
     n = weight.shape[0]
+    dtype, device, mn = x.dtype, x.device, (m, n)
     if accumulate and ((need_dw and dw is None) or (need_db and db is None)):
         raise ValueError("accumulate adds to dw and db: pass them")
     made = []
-
-    def output(t, need, shape, dtype):
-        if not need:
-            return None
-        if t is None:
-            t = torch.empty(shape, dtype=dtype, device=x.device)
-            made.append(t)
-        return t
-
+    dxs = dws = 0
     dw_dtype = weight_dtype if dw is None else dw.dtype
-    dx = output(dx, need_dx, (m, k), x.dtype)
-    dw = output(dw, need_dw, (n, k), dw_dtype)
-    db = output(db, need_db, (n,), torch.float32)
-    op = _LinearGrad(m, k, n, dy.data_ptr(), _rows(dy, "dy", (m, n), dy.dtype, x),
-                     None if pre is None else pre.data_ptr(),
-                     0 if pre is None else _rows(pre, "pre", (m, n), x.dtype, x),
-                     x.data_ptr(), _rows(x, "x", (m, k), x.dtype, x),
-                     weight.data_ptr(), _rows(weight, "weight", (n, k), x.dtype, x),
-                     None if dx is None else dx.data_ptr(), 0 if dx is None else _rows(dx, "dx", (m, k), x.dtype, x),
-                     None if dw is None else dw.data_ptr(), 0 if dw is None else _rows(dw, "dw", (n, k), dw_dtype, x),
-                     None if db is None else _vector(db, "db", n, x),
-                     _CODES[x.dtype], _CODES[dy.dtype], _CODES.get(dw_dtype, -1), _act(act), int(accumulate))
+    if not need_dx:
+        dx = None
+    elif dx is None:
+        dx, dxs = torch.empty((m, k), dtype=dtype, device=device), k
+        made.append(dx)
+    else:
+        dxs = _rows(dx, "dx", (m, k), dtype, device)
+    if not need_dw:
+        dw = None
+    elif dw is None:
+        dw, dws = torch.empty((n, k), dtype=dw_dtype, device=device), k
+        made.append(dw)
+    else:
+        dws = _rows(dw, "dw", (n, k), dw_dtype, device)
+    if not need_db:
+        db = None
+    elif db is None:
+        db = torch.empty((n,), dtype=torch.float32, device=device)
+        made.append(db)
+    op = _linear_grad(m, k, n, dy.data_ptr(), _rows(dy, "dy", mn, dy.dtype, device),
+                      0 if pre is None else pre.data_ptr(), 0 if pre is None else _rows(pre, "pre", mn, dtype, device),
+                      x.data_ptr(), _rows(x, "x", (m, k), dtype, device),
+                      weight.data_ptr(), _rows(weight, "weight", (n, k), dtype, device),
+                      0 if dx is None else dx.data_ptr(), dxs, 0 if dw is None else dw.data_ptr(), dws,
+                      0 if db is None else _vector(db, "db", n, device),
+                      _CODES[dtype], _CODES[dy.dtype], _CODES.get(dw_dtype, -1), _act(act), accumulate)
     lib = _lib()
-    auto = isinstance(workspace, str)
-
-    def alloc():
-        size = ctypes.c_size_t(0)
-        _check(lib.hashgrid_linear_backward_workspace_size(ctypes.byref(op), ctypes.byref(size)))
-        return torch.empty(size.value, dtype=torch.uint8, device=x.device) if size.value else None
-
-    ws_ptr, ws_bytes, ws = _workspace(workspace, alloc, "workspace")
-    _check(lib.hashgrid_linear_backward(ctypes.byref(op), ws_ptr, ws_bytes, _stream(x, stream)))
+    rc, made_ws = _with_workspace(lib.hashgrid_linear_backward_workspace_size, lib.hashgrid_linear_backward, op, workspace,
+                                  device, stream)
+    if rc:
+        _check(rc)
     if stream is not None:
-        _keep_for_stream(x, stream, *made, ws if auto else None)
+        _keep_for_stream(x, stream, *made, made_ws)
     return dx, dw, db
+
+
+def _with_workspace(sizer, call, op, workspace, device, stream):
+    """(return code of ``call``, the workspace made here if any)."""
+    ptr = size = 0
+    made = None
+    if isinstance(workspace, str):
+        if workspace != "auto":
+            raise ValueError("workspace must be a tensor, 'auto' or None")
+        need = ctypes.c_size_t(0)
+        rc = sizer(op, ctypes.byref(need))
+        if rc:
+            return rc, None
+        size = need.value
+        if size:
+            made = torch.empty(size, dtype=torch.uint8, device=device)
+            ptr = made.data_ptr()
+    elif workspace is not None:
+        _dev(workspace, "workspace", torch.uint8)
+        ptr, size = workspace.data_ptr(), workspace.numel()
+    return call(op, ptr, size, _here(device, stream)), made
 
 
 class RmsNormOutput(NamedTuple):
@@ -217,35 +272,27 @@ def hashgrid_rms_norm_forward(x: torch.Tensor, weight: torch.Tensor, *, residual
     bfloat16 and weight [c] in float32.  ``out_dtype`` is x's, or float8_e4m3fn with one scale a row.  ``save_sum``
     (or ``sum_out``, which may be x or the residual) keeps s in x's type, ``save_rstd`` the 1 / rms of each row."""
     _matrix(x, "x")
-    m, c = x.shape
+    m, c = mc = x.shape
+    dtype, device = x.dtype, x.device
     if out_dtype is None:
-        out_dtype = x.dtype if out is None else out.dtype
-    made = []
-    y = out
-    if y is None:
-        y = torch.empty((m, c), dtype=out_dtype, device=x.device)
-        made.append(y)
-    scale = rstd = None
-    if out_dtype == F8:
-        scale = torch.empty(m, dtype=torch.float32, device=x.device)
-        made.append(scale)
+        out_dtype = dtype if out is None else out.dtype
+    y = torch.empty(mc, dtype=out_dtype, device=device) if out is None else out
+    scale = torch.empty(m, dtype=torch.float32, device=device) if out_dtype == F8 else None
     s = sum_out
     if s is None and save_sum:
-        s = torch.empty((m, c), dtype=x.dtype, device=x.device)
-        made.append(s)
-    if save_rstd:
-        rstd = torch.empty(m, dtype=torch.float32, device=x.device)
-        made.append(rstd)
-    op = _RmsNorm(m, c, x.data_ptr(), _rows(x, "x", (m, c), x.dtype, x),
-                  None if residual is None else residual.data_ptr(),
-                  0 if residual is None else _rows(residual, "residual", (m, c), x.dtype, x),
-                  _vector(weight, "weight", c, x), y.data_ptr(), _rows(y, "out", (m, c), out_dtype, x),
-                  None if scale is None else scale.data_ptr(),
-                  None if s is None else s.data_ptr(), 0 if s is None else _rows(s, "sum_out", (m, c), x.dtype, x),
-                  None if rstd is None else rstd.data_ptr(), eps, _CODES[x.dtype], _CODES.get(out_dtype, -1))
-    _check(_lib().hashgrid_rms_norm_forward(ctypes.byref(op), _stream(x, stream)))
+        s = torch.empty(mc, dtype=dtype, device=device)
+    rstd = torch.empty(m, dtype=torch.float32, device=device) if save_rstd else None
+    op = _rms_norm(m, c, x.data_ptr(), _rows(x, "x", mc, dtype, device),
+                   0 if residual is None else residual.data_ptr(),
+                   0 if residual is None else _rows(residual, "residual", mc, dtype, device),
+                   _vector(weight, "weight", c, device), y.data_ptr(), c if out is None else _rows(y, "out", mc, out_dtype, device),
+                   0 if scale is None else scale.data_ptr(),
+                   0 if s is None else s.data_ptr(), 0 if s is None else _rows(s, "sum_out", mc, dtype, device),
+                   0 if rstd is None else rstd.data_ptr(), eps, _CODES[dtype], _CODES.get(out_dtype, -1))
+    if (rc := _lib().hashgrid_rms_norm_forward(op, _here(device, stream))):
+        _check(rc)
     if stream is not None:
-        _keep_for_stream(x, stream, *made)
+        _keep_for_stream(x, stream, y if out is None else None, scale, s if sum_out is None else None, rstd)
     return RmsNormOutput(y, scale, s, rstd)
 
 
@@ -257,35 +304,32 @@ def hashgrid_rms_norm_backward(dy: torch.Tensor, s: torch.Tensor, weight: torch.
     the gradient that reaches s itself and is added.  dx is the gradient of x and of the residual; dweight is float32
     (with ``accumulate``, ``dw`` must be given and is added to)."""
     _matrix(s, "s")
-    m, c = s.shape
+    m, c = mc = s.shape
+    dtype, device = s.dtype, s.device
     if accumulate and need_dw and dw is None:
         raise ValueError("accumulate adds to dw: pass it")
     made = []
     if dx is None:
-        dx = torch.empty((m, c), dtype=s.dtype, device=s.device)
+        dx, dxs = torch.empty(mc, dtype=dtype, device=device), c
         made.append(dx)
-    if dw is None and need_dw:
-        dw = torch.empty(c, dtype=torch.float32, device=s.device)
-        made.append(dw)
+    else:
+        dxs = _rows(dx, "dx", mc, dtype, device)
     if not need_dw:
         dw = None
-    op = _RmsNormGrad(m, c, dy.data_ptr(), _rows(dy, "dy", (m, c), s.dtype, s), s.data_ptr(),
-                      _rows(s, "s", (m, c), s.dtype, s), _vector(weight, "weight", c, s), _vector(rstd, "rstd", m, s),
-                      None if ds is None else ds.data_ptr(), 0 if ds is None else _rows(ds, "ds", (m, c), s.dtype, s),
-                      dx.data_ptr(), _rows(dx, "dx", (m, c), s.dtype, s), None if dw is None else _vector(dw, "dw", c, s),
-                      _CODES[s.dtype], int(accumulate))
+    elif dw is None:
+        dw = torch.empty(c, dtype=torch.float32, device=device)
+        made.append(dw)
+    op = _rms_norm_grad(m, c, dy.data_ptr(), _rows(dy, "dy", mc, dtype, device), s.data_ptr(), _rows(s, "s", mc, dtype, device),
+                        _vector(weight, "weight", c, device), _vector(rstd, "rstd", m, device),
+                        0 if ds is None else ds.data_ptr(), 0 if ds is None else _rows(ds, "ds", mc, dtype, device),
+                        dx.data_ptr(), dxs, 0 if dw is None else _vector(dw, "dw", c, device), _CODES[dtype], accumulate)
     lib = _lib()
-    auto = isinstance(workspace, str)
-
-    def alloc():
-        size = ctypes.c_size_t(0)
-        _check(lib.hashgrid_rms_norm_backward_workspace_size(ctypes.byref(op), ctypes.byref(size)))
-        return torch.empty(size.value, dtype=torch.uint8, device=s.device) if size.value else None
-
-    ws_ptr, ws_bytes, ws = _workspace(workspace, alloc, "workspace")
-    _check(lib.hashgrid_rms_norm_backward(ctypes.byref(op), ws_ptr, ws_bytes, _stream(s, stream)))
+    rc, made_ws = _with_workspace(lib.hashgrid_rms_norm_backward_workspace_size, lib.hashgrid_rms_norm_backward, op, workspace,
+                                  device, stream)
+    if rc:
+        _check(rc)
     if stream is not None:
-        _keep_for_stream(s, stream, *made, ws if auto else None)
+        _keep_for_stream(s, stream, *made, made_ws)
     return dx, dw
 
 
