@@ -101,11 +101,13 @@ __device__ __forceinline__ Cut<T> cut_piece(int k, int length) {
     return c;
 }
 
-// Logistic function; exp2 overflows to infinity for very negative z, whose
+// 1 / (1 + 2^t).  The logistic function of z is that of t = -log2(e) z; 2^t overflows to infinity for very negative z, whose
 // reciprocal is the right 0.
-__device__ __forceinline__ float logistic(float z) {
-    return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504f * z));
-}
+__device__ __forceinline__ float half_of(float t) { return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(t)); }
+__device__ __forceinline__ float logistic(float z) { return half_of(-1.44269504f * z); }
+// The logistic of 2 u, u = sqrt(2 / pi) (z + 0.044715 z^3), constants folded:
+// t = -log2(e) 2 u = z (-2.3022082 - 0.10294324 z^2).
+__device__ __forceinline__ float gelu_logistic(float z) { return half_of(z * fmaf(z * z, -0.10294324f, -2.3022082f)); }
 
 // A product in which 0 times anything is 0 (v_mul_legacy_f32): an infinite z
 // meets a logistic of 0 in both activations and their slopes, and 0 is the limit.
@@ -118,7 +120,7 @@ __device__ __forceinline__ float mul0(float a, float b) { return fmul_legacy(a, 
 __device__ __forceinline__ float activate(float z, int act) {
     if (act == HG_ACT_RELU) return z > 0.f ? z : z != z ? z : 0.f;
     if (act == HG_ACT_SILU) return mul0(z, logistic(z));
-    if (act == HG_ACT_GELU_TANH) return mul0(z, logistic(1.59576912f * z * fmaf(0.044715f * z, z, 1.f)));
+    if (act == HG_ACT_GELU_TANH) return mul0(z, gelu_logistic(z));
     return z;
 }
 
@@ -144,8 +146,8 @@ __device__ __forceinline__ float slope(float z, int act) {
         return mul0(p, 1.f + mul0(z, 1.f - p));
     }
     if (act == HG_ACT_GELU_TANH) {
-        const float p = logistic(1.59576912f * z * fmaf(0.044715f * z, z, 1.f));
-        return mul0(p, 1.f + mul0(1.59576912f * z * fmaf(0.134145f * z, z, 1.f), 1.f - p));
+        const float p = gelu_logistic(z);
+        return mul0(p, 1.f + mul0(z * fmaf(z * z, 0.21406447f, 1.59576912f), 1.f - p));
     }
     return 1.f;
 }

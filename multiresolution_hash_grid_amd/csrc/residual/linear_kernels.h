@@ -95,8 +95,8 @@ __device__ __forceinline__ void stage_store(V *y, int64_t stride, int64_t m1, in
 // rows, so x comes from HBM once.
 // kCut: 0 the contraction is whole fragments; 1 its last fragment is cut; 2 it
 // is shorter than a piece.
-template <typename T, typename Y, int KU, int FR, int GS, int kCut, bool kStage>
-__global__ __launch_bounds__(1024) void linear_stream_kernel(const FwdArgs a, int slices, int slice_n) {
+template <typename T, typename Y, int KU, int RF, int FR, int GS, int kCut, bool kStage>
+__global__ __launch_bounds__(RF == 1 ? 1024 : 512) void linear_stream_kernel(const FwdArgs a, int slices, int slice_n) {
     extern __shared__ __attribute__((aligned(16))) char lds[];
     constexpr int kHalves = sizeof(T) == 1 ? 2 : 1;
     constexpr int kPairs = FR == 1 ? 1 : FR / 2, kOut = FR == 1 ? 4 : 8;  // pairs of a set; consecutive outputs of a lane
@@ -141,80 +141,99 @@ __global__ __launch_bounds__(1024) void linear_stream_kernel(const FwdArgs a, in
     }
     __syncthreads();
 
-    const int64_t tiles = (a.m + 15) / 16;
+    const int64_t tiles = (a.m + RF * 16 - 1) / (RF * 16);
     for (int64_t tile = (int64_t)wave * walkers + walker; tile < tiles; tile += (int64_t)waves * walkers) {
-        const bool there = tile * 16 + row16 < a.m;
-        const int64_t m = there ? tile * 16 + row16 : a.m - 1;
-        u32x4 x[KU * (kWide ? 2 : 1)];
-        float xsc;
+        const int64_t m0 = tile * (RF * 16) + row16;
+        u32x4 x[RF][KU * (kWide ? 2 : 1)];
+        float xsc[RF];
 #pragma unroll
-        for (int u = 0; u < KU; ++u) x[u] = piece((const T *)a.x + m * a.xs, u);
-        if constexpr (sizeof(T) == 1) xsc = a.x_scale[m];
+        for (int r = 0; r < RF; ++r) {
+            const int64_t m = m0 + r * 16 < a.m ? m0 + r * 16 : a.m - 1;
+#pragma unroll
+            for (int u = 0; u < KU; ++u) x[r][u] = piece((const T *)a.x + m * a.xs, u);
+            if constexpr (sizeof(T) == 1) xsc[r] = a.x_scale[m];
+        }
         if constexpr (kWide)
 #pragma unroll
-            for (int u = KU - 1; u >= 0; --u) {
-                const Widened v = widen(x[u]);
-                x[2 * u] = v.lo, x[2 * u + 1] = v.hi;
-            }
+            for (int r = 0; r < RF; ++r)
+#pragma unroll
+                for (int u = KU - 1; u >= 0; --u) {
+                    const Widened v = widen(x[r][u]);
+                    x[r][2 * u] = v.lo, x[r][2 * u + 1] = v.hi;
+                }
         for (int s0 = 0; s0 < sets; s0 += GS) {
-            Held<kOut, Y> y[kStage ? 1 : GS][kPairs];
+            Held<kOut, Y> y[RF][kStage ? 1 : GS][kPairs];
             typedef std::conditional_t<sizeof(T) == 1, f16, T> P;  // (8-bit operands keep no pre-activation)
-            Held<kOut, P> pre[GS][kPairs];
+            Held<kOut, P> pre[RF][GS][kPairs];
 #pragma unroll
             for (int i = 0; i < GS; ++i) {
                 const int s = s0 + i;
                 if (s >= sets) break;
                 const int n = s * 16 * FR + group * kOut;  // this lane's outputs: kOut from n, and from n + 32
                 // The residual is asked for before the products.
-                Held<kOut, Y> res[kPairs];
+                Held<kOut, Y> res[RF][kPairs];
                 if (a.r)
 #pragma unroll
-                    for (int q = 0; q < kPairs; ++q)
-                        res[q] = hold<kOut>((const Y *)a.r + m * a.rs + n0 + n + q * 32, nn - n - q * 32);
-                f32x4 acc[FR];
+                    for (int r = 0; r < RF; ++r) {
+                        const int64_t m = m0 + r * 16 < a.m ? m0 + r * 16 : a.m - 1;
+#pragma unroll
+                        for (int q = 0; q < kPairs; ++q)
+                            res[r][q] = hold<kOut>((const Y *)a.r + m * a.rs + n0 + n + q * 32, nn - n - q * 32);
+                    }
+                f32x4 acc[RF][FR];
 #pragma unroll
                 for (int f = 0; f < FR; ++f) {
                     // sums begin with the bias; 8-bit ones are scaled first
-                    if constexpr (sizeof(T) == 1) acc[f] = f32x4{0.f, 0.f, 0.f, 0.f};
-                    else acc[f] = *(const f32x4 *)(bias + n + (f >> 1) * 32 + (f & 1) * 4);
+                    if constexpr (sizeof(T) == 1) acc[0][f] = f32x4{0.f, 0.f, 0.f, 0.f};
+                    else acc[0][f] = *(const f32x4 *)(bias + n + (f >> 1) * 32 + (f & 1) * 4);
+#pragma unroll
+                    for (int r = 1; r < RF; ++r) acc[r][f] = acc[0][f];
                 }
 #pragma unroll
                 for (int u = 0; u < KU; ++u) {
-                    Widened xw;
-                    if constexpr (sizeof(T) == 1 && !kWide) {
-                        asm volatile("" : "+v"(x[u]));  // widen here, not once before all sets: the registers are not there
-                        xw = widen(x[u]);
-                    }
+                    Widened xw[RF];
+                    if constexpr (sizeof(T) == 1 && !kWide)
+#pragma unroll
+                        for (int r = 0; r < RF; ++r) {
+                            asm volatile("" : "+v"(x[r][u]));  // widen here, not once before all sets: the registers are not there
+                            xw[r] = widen(x[r][u]);
+                        }
 #pragma unroll
                     for (int f = 0; f < FR; ++f)
 #pragma unroll
                         for (int h = 0; h < kHalves; ++h) {
                             const u32x4 w = wl[(((s * FR + f) * KU + u) * kHalves + h) * 64 + lane];
-                            u32x4 v;
-                            if constexpr (sizeof(T) == 1 && !kWide) v = h ? xw.hi : xw.lo;
-                            else v = x[u * kHalves + h];
-                            acc[f] = mma16<T>(w, v, acc[f]);
+#pragma unroll
+                            for (int r = 0; r < RF; ++r) {
+                                u32x4 v;
+                                if constexpr (sizeof(T) == 1 && !kWide) v = h ? xw[r].hi : xw[r].lo;
+                                else v = x[r][u * kHalves + h];
+                                acc[r][f] = mma16<T>(w, v, acc[r][f]);
+                            }
                         }
                 }
 #pragma unroll
-                for (int q = 0; q < kPairs; ++q) {
-                    float z[kOut];
+                for (int r = 0; r < RF; ++r)
 #pragma unroll
-                    for (int j = 0; j < kOut; ++j) {
-                        z[j] = acc[q * 2 + j / 4][j % 4];
-                        if constexpr (sizeof(T) == 1) z[j] = fmaf(z[j] * xsc, wsc[n + q * 32 + j], bias[n + q * 32 + j]);
+                    for (int q = 0; q < kPairs; ++q) {
+                        float z[kOut];
+#pragma unroll
+                        for (int j = 0; j < kOut; ++j) {
+                            z[j] = acc[r][q * 2 + j / 4][j % 4];
+                            if constexpr (sizeof(T) == 1) z[j] = fmaf(z[j] * xsc[r], wsc[n + q * 32 + j], bias[n + q * 32 + j]);
+                        }
+                        if constexpr (sizeof(T) == 2)
+                            if (a.pre) pre[r][i][q] = rounded<kOut, T>(z);
+                        activate_all(z, a.act);
+                        if (a.r)
+#pragma unroll
+                            for (int j = 0; j < kOut; ++j) z[j] += (float)res[r][q].v[j];
+                        if constexpr (kStage) stage_put(stage, row16, (i * kPairs + q) * 4 + group, rounded<kOut, Y>(z));
+                        else y[r][i][q] = rounded<kOut, Y>(z);
                     }
-                    if constexpr (sizeof(T) == 2)
-                        if (a.pre) pre[i][q] = rounded<kOut, T>(z);
-                    activate_all(z, a.act);
-                    if (a.r)
-#pragma unroll
-                        for (int j = 0; j < kOut; ++j) z[j] += (float)res[q].v[j];
-                    if constexpr (kStage) stage_put(stage, row16, (i * kPairs + q) * 4 + group, rounded<kOut, Y>(z));
-                    else y[i][q] = rounded<kOut, Y>(z);
-                }
             }
             if constexpr (kStage) {
+                static_assert(RF == 1);
                 const int count = (sets - s0 < GS ? sets - s0 : GS) * kPairs;  // pairs of this round
                 const int64_t m1 = tile * 16;
                 stage_store((Y *)a.y, a.ys, m1, a.m, n0 + s0 * 16 * FR, n0 + nn, stage, count, lane);
@@ -222,21 +241,25 @@ __global__ __launch_bounds__(1024) void linear_stream_kernel(const FwdArgs a, in
                     if (a.pre) {
 #pragma unroll
                         for (int q = 0; q < GS * kPairs; ++q)
-                            if (q < count) stage_put(stage, row16, q * 4 + group, pre[q / kPairs][q % kPairs]);
+                            if (q < count) stage_put(stage, row16, q * 4 + group, pre[0][q / kPairs][q % kPairs]);
                         stage_store((T *)a.pre, a.ps, m1, a.m, n0 + s0 * 16 * FR, n0 + nn, stage, count, lane);
                     }
-                continue;
-            }
-            if (!there) continue;
-            const int at = n0 + s0 * 16 * FR + group * kOut, left = n0 + nn - at;
-            if constexpr (sizeof(T) == 2)
-                if (a.pre)
+            } else {
+                const int at = n0 + s0 * 16 * FR + group * kOut, left = n0 + nn - at;
+#pragma unroll
+                for (int r = 0; r < RF; ++r) {
+                    const int64_t m = m0 + r * 16;
+                    if (m >= a.m) break;
+                    if constexpr (sizeof(T) == 2)
+                        if (a.pre)
+#pragma unroll
+                            for (int q = 0; q < GS * kPairs; ++q)
+                                put((T *)a.pre + m * a.ps + at + q * 32, left - q * 32, pre[r][q / kPairs][q % kPairs]);
 #pragma unroll
                     for (int q = 0; q < GS * kPairs; ++q)
-                        put((T *)a.pre + m * a.ps + at + q * 32, left - q * 32, pre[q / kPairs][q % kPairs]);
-#pragma unroll
-            for (int q = 0; q < (kStage ? 0 : GS * kPairs); ++q)
-                put((Y *)a.y + m * a.ys + at + q * 32, left - q * 32, y[kStage ? 0 : q / kPairs][q % kPairs]);
+                        put((Y *)a.y + m * a.ys + at + q * 32, left - q * 32, y[r][q / kPairs][q % kPairs]);
+                }
+            }
         }
     }
 }
@@ -246,9 +269,9 @@ constexpr int kLdsBytes = 160 * 1024;
 template <typename T, int KU>
 constexpr int kWeightBytes = KU * 64 * (sizeof(T) == 1 ? 2 : 1) + 8;
 
-template <typename T, typename Y, int KU, int FR, int GS, int kCut, bool kStage = false>
+template <typename T, typename Y, int KU, int RF, int FR, int GS, int kCut, bool kStage = false>
 hipError_t stream_launch(const FwdArgs &a, hipStream_t stream) {
-    const auto kernel = linear_stream_kernel<T, Y, KU, FR, GS, kCut, kStage>;
+    const auto kernel = linear_stream_kernel<T, Y, KU, RF, FR, GS, kCut, kStage>;
     constexpr int per = kWeightBytes<T, KU>, set = 16 * FR;  // LDS bytes of an output; outputs of a set
     const int fit = kLdsBytes / per / set * set;
     int slices = (int)div_up(a.n, fit);
@@ -262,25 +285,26 @@ hipError_t stream_launch(const FwdArgs &a, hipStream_t stream) {
     // 16 waves a CU in one workgroup, or in two of eight where two slices fit its
     // LDS (three where the registers allow six waves a SIMD): they start and end
     // apart, and the last tiles are dealt more evenly.
-    const int groups = bytes > kLdsBytes / 2 ? 1 : KU > 1 || bytes > kLdsBytes / 3 ? 2 : 3;
-    const int64_t tiles = div_up(a.m, 16);
+    const int groups = RF == 2 || bytes > kLdsBytes / 2 ? 1 : KU > 1 || bytes > kLdsBytes / 3 ? 2 : 3;
+    const int64_t tiles = div_up(a.m, RF * 16);
     int64_t walkers = kCus * groups / slices;  // workgroups that share the rows
     if (walkers > tiles) walkers = tiles;
     walkers = div_up(walkers, 8) * 8;
-    kernel<<<dim3((unsigned)(walkers * slices)), groups == 1 ? 1024 : 512, bytes, stream>>>(a, slices, slice_n);
+    kernel<<<dim3((unsigned)(walkers * slices)), RF == 1 && groups == 1 ? 1024 : 512, bytes, stream>>>(a, slices, slice_n);
     return hipGetLastError();
 }
 
 template <typename T, typename Y, int KU, int kCut>
 hipError_t stream_set(const FwdArgs &a, hipStream_t stream) {
-    if (a.n <= 16) return stream_launch<T, Y, KU, 1, 1, kCut>(a, stream);
-    if (a.n <= 32) return stream_launch<T, Y, KU, 2, 1, kCut>(a, stream);
-    if (a.n <= 64) return stream_launch<T, Y, KU, 4, 1, kCut>(a, stream);
+    if (a.n <= 16) return stream_launch<T, Y, KU, 1, 1, 1, kCut>(a, stream);
+    if (a.n <= 32) return stream_launch<T, Y, KU, 1, 2, 1, kCut>(a, stream);
+    if (a.n <= 64) return stream_launch<T, Y, KU, 1, 4, 1, kCut>(a, stream);
     if constexpr (KU <= 4)  // rows of more than one set, weights beside 16 waves' buffers
         if (div_up(a.n, 64) * 64 * kWeightBytes<T, KU> <= kLdsBytes - 16 * kStageBytes)
-            return stream_launch<T, Y, KU, 4, sizeof(Y) == 4 ? 2 : 4, kCut, true>(a, stream);
+            return stream_launch<T, Y, KU, 1, 4, sizeof(Y) == 4 ? 2 : 4, kCut, true>(a, stream);
     constexpr int GS = sizeof(Y) == 4 ? (KU <= 4 ? 2 : 1) : KU <= 12 ? 2 : 1;  // what the registers hold
-    return stream_launch<T, Y, KU, 4, GS, kCut>(a, stream);
+    if constexpr (KU >= 5) return stream_launch<T, Y, KU, 2, 4, GS, kCut>(a, stream);
+    return stream_launch<T, Y, KU, 1, 4, GS, kCut>(a, stream);
 }
 
 // hipErrorNotSupported: not a case of this kernel.
