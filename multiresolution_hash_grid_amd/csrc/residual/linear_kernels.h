@@ -307,6 +307,152 @@ hipError_t stream_set(const FwdArgs &a, hipStream_t stream) {
     return stream_launch<T, Y, KU, 1, 4, GS, kCut>(a, stream);
 }
 
+// Many rows, a weight too large to stay in LDS.  A workgroup makes a block of 128
+// rows by 256 outputs, its eight waves 64 x 64 each, over steps of 128 bytes of
+// the contraction: the next step's pieces of x and W are on their way into
+// registers while this step's are read from LDS as fragments.  Two workgroups a
+// CU (128 registers a wave, 48 KB of LDS each) fill each other's barriers and
+// epilogues.  Row and output tiles are dealt to the XCDs in runs, the output
+// tiles of one row tile next to each other, so x and W come from an XCD's L2 after
+// their first reader.
+// In LDS a row's eight pieces are permuted by three bits of its number, those in
+// which the 16 rows of a fragment read differ, lines of 256 bytes apart: rows
+// follow each other in x, and in W go as the outputs are dealt to the lanes.
+template <bool kDealt>
+__device__ __forceinline__ int block_at(int row, int piece) {
+    const int turn = kDealt ? ((row >> 1) & 1) | ((row >> 2) & 6) : (row >> 1) & 7;
+    return row * 128 + ((piece ^ turn) << 4);
+}
+constexpr int kBlockM = 128, kBlockN = 256;
+template <typename T, typename Y>
+__global__ __launch_bounds__(512, 4) void linear_block_kernel(const FwdArgs a, int tiles_n, int per_xcd, int tiles) {
+    __shared__ __attribute__((aligned(16))) char xt[kBlockM * 128], wt[kBlockN * 128];
+    constexpr int kStep = 128 / (int)sizeof(T), kX = kBlockM * 8 / 512, kW = kBlockN * 8 / 512;
+    const int tile = (blockIdx.x & 7) * per_xcd + (blockIdx.x >> 3);
+    if (tile >= tiles) return;
+    const int64_t m0 = (int64_t)(tile / tiles_n) * kBlockM;
+    const int n0 = tile % tiles_n * kBlockN;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, row16 = lane & 15, group = lane >> 4;
+    const int wm = wave & 1, wn = wave >> 1;
+    const int p = threadIdx.x & 7, row = threadIdx.x >> 3;  // this thread's piece of its rows row, row + 64, ...
+
+    const T *xr[kX], *wr[kW];
+#pragma unroll
+    for (int i = 0; i < kX; ++i) {
+        const int64_t m = m0 + row + i * 64;
+        xr[i] = (const T *)a.x + (m < a.m ? m : a.m - 1) * a.xs;
+    }
+#pragma unroll
+    for (int i = 0; i < kW; ++i) {
+        const int n = n0 + row + i * 64;
+        wr[i] = (const T *)a.w + (int64_t)(n < a.n ? n : a.n - 1) * a.ws;
+    }
+    u32x4 nx[kX], nw[kW];
+    auto fetch = [&](int k0) {
+        const int k = k0 + p * kPiece<T>, at = k + kPiece<T> <= a.k ? k : a.k - kPiece<T>;
+#pragma unroll
+        for (int i = 0; i < kX; ++i) nx[i] = load_loose<u32x4>(xr[i] + at);
+#pragma unroll
+        for (int i = 0; i < kW; ++i) nw[i] = load_loose<u32x4>(wr[i] + at);
+    };
+
+    f32x4 acc[4][4] = {};
+    fetch(0);
+    for (int k0 = 0; k0 < a.k; k0 += kStep) {
+        if (k0 + kStep > a.k) {  // the step that the contraction's end cuts
+            const u32x4 mask = cut_piece<T>(k0 + p * kPiece<T>, a.k).mask;
+#pragma unroll
+            for (int i = 0; i < kX; ++i) nx[i] &= mask;
+#pragma unroll
+            for (int i = 0; i < kW; ++i) nw[i] &= mask;
+        }
+        __syncthreads();  // the last step's reads are done
+#pragma unroll
+        for (int i = 0; i < kX; ++i) *(u32x4 *)(xt + block_at<false>(row + i * 64, p)) = nx[i];
+#pragma unroll
+        for (int i = 0; i < kW; ++i) *(u32x4 *)(wt + block_at<true>(row + i * 64, p)) = nw[i];
+        __syncthreads();
+        if (k0 + kStep < a.k) fetch(k0 + kStep);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            u32x4 x[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) x[r] = *(const u32x4 *)(xt + block_at<false>(wm * 64 + r * 16 + row16, u * 4 + group));
+            if constexpr (sizeof(T) == 1) {
+                Widened xw[4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) xw[r] = widen(x[r]);
+#pragma unroll
+                for (int f = 0; f < 4; ++f) {
+                    const int n = wn * 64 + (f >> 1) * 32 + (row16 >> 2) * 8 + (f & 1) * 4 + (row16 & 3);
+                    const Widened w = widen(*(const u32x4 *)(wt + block_at<true>(n, u * 4 + group)));
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) acc[r][f] = mma16<f16>(w.hi, xw[r].hi, mma16<f16>(w.lo, xw[r].lo, acc[r][f]));
+                }
+            } else {
+#pragma unroll
+                for (int f = 0; f < 4; ++f) {
+                    const int n = wn * 64 + (f >> 1) * 32 + (row16 >> 2) * 8 + (f & 1) * 4 + (row16 & 3);
+                    const u32x4 w = *(const u32x4 *)(wt + block_at<true>(n, u * 4 + group));
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) acc[r][f] = mma16<T>(w, x[r], acc[r][f]);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const int n = n0 + wn * 64 + q * 32 + group * 8, left = a.n - n;
+        float bs[8], ws[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            bs[j] = a.bias && j < left ? a.bias[n + j] : 0.f;
+            if constexpr (sizeof(T) == 1) ws[j] = j < left ? a.w_scale[n + j] : 0.f;
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int64_t m = m0 + wm * 64 + r * 16 + row16;
+            if (m >= a.m || left <= 0) continue;
+            Held<8, Y> res;
+            if (a.r) res = hold<8>((const Y *)a.r + m * a.rs + n, left);
+            float z[8];
+            float xsc = 1.f;
+            if constexpr (sizeof(T) == 1) xsc = a.x_scale[m];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                z[j] = acc[r][q * 2 + j / 4][j % 4];
+                if constexpr (sizeof(T) == 1) z[j] = fmaf(z[j] * xsc, ws[j], bs[j]);
+                else z[j] += bs[j];
+            }
+            if constexpr (sizeof(T) == 2)
+                if (a.pre) put((T *)a.pre + m * a.ps + n, left, rounded<8, T>(z));
+            activate_all(z, a.act);
+            if (a.r)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) z[j] += (float)res.v[j];
+            put((Y *)a.y + m * a.ys + n, left, rounded<8, Y>(z));
+        }
+    }
+}
+
+template <typename T, typename Y>
+hipError_t run_block(const FwdArgs &a, hipStream_t stream) {
+    const int tiles_n = (int)div_up(a.n, kBlockN);
+    FwdArgs part = a;
+    const int64_t most = ((int64_t)1 << 30) / tiles_n / kBlockM * kBlockM;  // rows of a launch
+    for (int64_t m = 0; m < a.m; m += most) {
+        part.m = a.m - m < most ? a.m - m : most;
+        part.x = (const T *)a.x + m * a.xs;
+        part.r = a.r ? (const Y *)a.r + m * a.rs : nullptr;
+        part.y = (Y *)a.y + m * a.ys;
+        part.pre = a.pre ? (T *)a.pre + m * a.ps : nullptr;
+        part.x_scale = a.x_scale ? a.x_scale + m : nullptr;
+        const int tiles = (int)div_up(part.m, kBlockM) * tiles_n, per_xcd = (int)div_up(tiles, 8);
+        linear_block_kernel<T, Y><<<dim3((unsigned)per_xcd * 8), 512, 0, stream>>>(part, tiles_n, per_xcd, tiles);
+    }
+    return hipGetLastError();
+}
+
 // hipErrorNotSupported: not a case of this kernel.
 template <typename T, typename Y>
 hipError_t run_stream(const FwdArgs &a, hipStream_t stream) {
@@ -340,7 +486,7 @@ template <typename T, typename Y>
 hipError_t linear_run(const FwdArgs &a, hipStream_t stream) {
     if (a.m >= 2048) {
         const hipError_t e = run_stream<T, Y>(a, stream);
-        if (e != hipErrorNotSupported) return e;
+        return e != hipErrorNotSupported ? e : run_block<T, Y>(a, stream);
     }
     FwdArgs part = a;
     const int64_t most = 65535LL * 16;  // rows a grid's second dimension reaches
