@@ -68,10 +68,11 @@ __device__ __forceinline__ int column_of(int slot, int width) {
     return j < c.drop || c.at + j >= width ? -1 : c.at + j;
 }
 
-template <typename T>
-__device__ __forceinline__ u32x4 load_columns(const T *row, Columns c, int width) {
-    if (width >= 8) return load_loose<u32x4>(row + c.at);
-    return load_piece(row + c.at, c.drop ? 0 : width);
+// The piece at p; kShort: rows may be shorter than a piece (the narrowest tiles').
+template <bool kShort, typename T>
+__device__ __forceinline__ u32x4 load_columns(const T *p, Columns c, int width) {
+    if (!kShort || width >= 8) return load_loose<u32x4>(p);
+    return load_piece(p, c.drop ? 0 : width);
 }
 
 // One piece of dz: 8 values from dy and z.
@@ -79,22 +80,22 @@ template <typename T, typename D>
 struct RawDz {
     u32x4 dy[sizeof(D) == 4 ? 2 : 1], pre;
 };
-template <typename T, typename D>
-__device__ __forceinline__ RawDz<T, D> load_dz(const GradArgs &a, int64_t m, Columns c) {
+// dy and pre: this piece's row and column in each.
+template <bool kShort, typename T, typename D>
+__device__ __forceinline__ RawDz<T, D> load_dz(const GradArgs &a, const D *dy, const T *pre, Columns c) {
     RawDz<T, D> v;
-    const D *dy = (const D *)a.dy + m * a.dys;
     if constexpr (sizeof(D) == 4) {
-        if (a.n >= 8) {
-            v.dy[0] = load_loose<u32x4>(dy + c.at), v.dy[1] = load_loose<u32x4>(dy + c.at + 4);
+        if (!kShort || a.n >= 8) {
+            v.dy[0] = load_loose<u32x4>(dy), v.dy[1] = load_loose<u32x4>(dy + 4);
         } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j) v.dy[j / 4][j % 4] = c.drop == 0 && j < a.n ? __float_as_uint(dy[j]) : 0u;
         }
     } else {
-        v.dy[0] = load_columns(dy, c, a.n);
+        v.dy[0] = load_columns<kShort>(dy, c, a.n);
     }
     v.pre = u32x4{0, 0, 0, 0};
-    if (a.act != HG_ACT_NONE) v.pre = load_columns((const T *)a.pre + m * a.ps, c, a.n);
+    if (a.act != HG_ACT_NONE) v.pre = load_columns<kShort>(pre, c, a.n);
     return v;
 }
 template <typename T, typename D>
@@ -182,12 +183,14 @@ __global__ __launch_bounds__(kGradThreads) void grad_kernel(const GradArgs a, fl
 
     const int n0 = blockIdx.y * NT, k0 = blockIdx.z * KT;
     const bool store_dz = !kDx && dz_out && blockIdx.z == 0;
-    const Columns cn = columns_of(n0 + threadIdx.x % PN * 8, a.n), ck = columns_of(k0 + threadIdx.x % PK * 8, a.k);
-    u32x4 keep_k;
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-        keep_k[j] = 2 * j >= ck.drop ? ~0u : 2 * j + 1 >= ck.drop ? 0xFFFF0000u : 0u;
-
+    // Where this thread's pieces lie is worked out anew in every step: held, it
+    // would cost registers that the widest tile does not have, and a spill's
+    // reload waits for every store and load before it.
+    auto thread = [] {
+        int t = threadIdx.x;
+        asm volatile("" : "+v"(t));
+        return t;
+    };
     if constexpr (kDx) stage_wt<T, NT, KT>(a, 0, wt);
 
     f32x4 acc[FN][FK];
@@ -199,17 +202,28 @@ __global__ __launch_bounds__(kGradThreads) void grad_kernel(const GradArgs a, fl
 
     RawDz<T, D> nz[LN];
     u32x4 nx[LK];
+    // Addresses: a uniform base for the step and i, and this thread's 32-bit offset
+    // of its row and column in a step (row strides are below 2^22).
     auto fetch = [&](int64_t step) {
+        const int t = thread(), rn = t / PN, rk = t / PK;
+        const Columns cn = columns_of(n0 + t % PN * 8, a.n), ck = columns_of(k0 + t % PK * 8, a.k);
+        const int64_t m = step * R;
+        const int last = a.m - m < R ? (int)(a.m - m) - 1 : R - 1;  // rows past the end read the last one
 #pragma unroll
         for (int i = 0; i < LN; ++i) {
-            const int64_t m = step * R + threadIdx.x / PN + i * (kGradThreads / PN);
-            nz[i] = load_dz<T, D>(a, m < a.m ? m : a.m - 1, cn);
+            const int skip = i * (kGradThreads / PN), room = last - skip < 0 ? 0 : last - skip;  // (a base stays inside)
+            const int64_t base = m + (last - skip < 0 ? last : skip);
+            const int r = rn < room ? rn : room;
+            nz[i] = load_dz<NT == 64, T, D>(a, (const D *)a.dy + base * a.dys + (uint32_t)(r * (int)a.dys + cn.at),
+                                  (const T *)a.pre + base * a.ps + (uint32_t)(r * (int)a.ps + cn.at), cn);
         }
         if (a.dw)
 #pragma unroll
             for (int i = 0; i < LK; ++i) {
-                const int64_t m = step * R + threadIdx.x / PK + i * (kGradThreads / PK);
-                nx[i] = load_columns((const T *)a.x + (m < a.m ? m : a.m - 1) * a.xs, ck, a.k);
+                const int skip = i * (kGradThreads / PK), room = last - skip < 0 ? 0 : last - skip;
+                const int64_t base = m + (last - skip < 0 ? last : skip);
+                const int r = rk < room ? rk : room;
+                nx[i] = load_columns<KT == 64>((const T *)a.x + base * a.xs + (uint32_t)(r * (int)a.xs + ck.at), ck, a.k);
             }
     };
 
@@ -224,9 +238,9 @@ __global__ __launch_bounds__(kGradThreads) void grad_kernel(const GradArgs a, fl
             const int block = wave + b * 8, k = block % (KT / 32) * 32 + (lane >> 4) * 8, left = a.k - k;
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                const int64_t m = step * R + block / (KT / 32) * 32 + r * 16 + (lane & 15);
-                T *const p = (T *)a.dx + m * a.dxs + k;
-                if (m < a.m) {
+                const int row = block / (KT / 32) * 32 + r * 16 + (lane & 15);
+                T *const p = (T *)a.dx + step * R * a.dxs + (uint32_t)(row * (int)a.dxs + k);
+                if (step * R + row < a.m) {
                     if (left >= 8) store_loose<u32x4>(p, late[b][r]);
                     else
 #pragma unroll
@@ -241,15 +255,17 @@ __global__ __launch_bounds__(kGradThreads) void grad_kernel(const GradArgs a, fl
     if (blockIdx.x < steps) fetch(blockIdx.x);
     for (int64_t step = blockIdx.x; step < steps; step += gridDim.x) {
         const bool whole = (step + 1) * R <= a.m;
+        const int t = thread();
+        const Columns cn = columns_of(n0 + t % PN * 8, a.n), ck = columns_of(k0 + t % PK * 8, a.k);
         __syncthreads();  // the last step's reads of the tiles are done
 #pragma unroll
         for (int i = 0; i < LN; ++i) {
-            const int r = threadIdx.x / PN + i * (kGradThreads / PN);
+            const int r = t / PN + i * (kGradThreads / PN);
             float dz[8];
             dz_of<T, D>(nz[i], a.act, whole || step * R + r < a.m ? cn.drop : 8, dz);
 #pragma unroll
             for (int j = 0; j < 8; ++j) db[j] += dz[j];
-            *(u32x4 *)(dzt + tile_at<NT>(r, threadIdx.x % PN)) = pack8<T>(dz);
+            *(u32x4 *)(dzt + tile_at<NT>(r, t % PN)) = pack8<T>(dz);
             if (store_dz && step * R + r < a.m) {
                 T *const p = dz_out + (step * R + r) * a.n + cn.at;
                 if (cn.drop == 0) store8(p, a.n < 8 ? a.n : 8, dz);
@@ -262,11 +278,13 @@ __global__ __launch_bounds__(kGradThreads) void grad_kernel(const GradArgs a, fl
         if (a.dw)
 #pragma unroll
             for (int i = 0; i < LK; ++i) {
-                const int r = threadIdx.x / PK + i * (kGradThreads / PK);
+                const int r = t / PK + i * (kGradThreads / PK);
                 u32x4 v = nx[i];
-                if (ck.drop > 0) v &= keep_k;
+                if (ck.drop > 0)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) v[j] &= 2 * j >= ck.drop ? ~0u : 2 * j + 1 >= ck.drop ? 0xFFFF0000u : 0u;
                 if (!whole && step * R + r >= a.m) v = u32x4{0, 0, 0, 0};
-                *(u32x4 *)(xt + tile_at<KT>(r, threadIdx.x % PK)) = v;
+                *(u32x4 *)(xt + tile_at<KT>(r, t % PK)) = v;
             }
         if (kDx && step != blockIdx.x) store_late(step - gridDim.x);
         if (step + gridDim.x < steps) fetch(step + gridDim.x);
