@@ -423,7 +423,8 @@ int hashgrid_linear_forward(const hg_linear *op, void *stream);
  * rounded once.  Where act' is 0 (ReLU below zero) dz is 0 whatever dy holds.
  * dw and db are WRITTEN, or added to their old values with accumulate; with
  * m == 0 they are zero (or unchanged).  The order of every sum is fixed by the
- * sizes: results do not depend on scheduling. */
+ * sizes: results do not depend on scheduling.  Row strides of dy, pre, x and dx are
+ * at most 2^22. */
 typedef struct {
     int64_t m;
     int32_t k, n;

@@ -13,9 +13,10 @@ GradPlan plan(const hg_linear_grad &op) {
     p.nt = tile_of(op.n), p.kt = tile_of(op.k);
     p.ny = (int)div_up(op.n, p.nt), p.nz = (int)div_up(op.k, p.kt);
     p.fused = op.dx && p.ny == 1 && p.nz == 1;
-    // one workgroup a CU over all tiles, and no more than there are steps
+    // one workgroup a CU over all tiles (two of the smallest tile, whose registers
+    // and LDS leave room), and no more than there are steps
     const int64_t steps = div_up(op.m, grad_rows(p.nt, p.kt));
-    int64_t parts = kCus / (p.ny * p.nz);
+    int64_t parts = kCus * (p.nt * p.kt == 64 * 64 ? 2 : 1) / (p.ny * p.nz);
     if (parts < 1) parts = 1;
     if (parts > steps) parts = steps;
     p.parts = (int)(parts < 1 ? 1 : parts);

@@ -358,25 +358,34 @@ __global__ __launch_bounds__(kGradThreads) void grad_kernel(const GradArgs a, fl
     }
 }
 
-// dW = (dW +) the partials' sum, rounded once; db alike.  A workgroup takes 64
-// groups of four values; its eight waves share the partials and add up in order.
+// dW = (dW +) the partials' sum, rounded once; db alike.  A workgroup takes 16
+// groups of four values; 32 threads share the partials of each, and their sums
+// are added in order, eight and then four.
 template <typename G>
 __global__ __launch_bounds__(512) void grad_join_kernel(const float *part, int parts, int nt, int kt, int ny, int nz, GradArgs a) {
-    __shared__ f32x4 lds[8][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    __shared__ f32x4 lds[32][16];
+    const int slot = threadIdx.x & 15, share = threadIdx.x >> 4;
     const int64_t quads = a.dw ? (int64_t)ny * nz * nt * kt / 4 : 0, all = quads + (a.db ? ny * nt / 4 : 0);
-    const int64_t q = (int64_t)blockIdx.x * 64 + lane;
+    const int64_t q = (int64_t)blockIdx.x * 16 + slot;
     const int64_t per = q < quads ? nt * kt / 4 : nt / 4;      // quads of a partial
     const int64_t local = q < quads ? q : q - quads;
     const float *p = part + (q < quads ? 0 : quads * 4 * parts) + (local / per * per * parts + local % per) * 4;
     f32x4 t = {0.f, 0.f, 0.f, 0.f};
     if (q < all)
 #pragma unroll 8
-        for (int i = wave; i < parts; i += 8) t += *(const f32x4 *)(p + i * per * 4);
-    lds[wave][lane] = t;
+        for (int i = share; i < parts; i += 32) t += *(const f32x4 *)(p + i * per * 4);
+    lds[share][slot] = t;
     __syncthreads();
-    if (wave || q >= all) return;
-    for (int i = 1; i < 8; ++i) t += lds[i][lane];
+    if (share < 4) {
+        t = lds[share * 8][slot];
+#pragma unroll
+        for (int i = 1; i < 8; ++i) t += lds[share * 8 + i][slot];
+    }
+    __syncthreads();
+    if (share < 4) lds[share][slot] = t;
+    __syncthreads();
+    if (share || q >= all) return;
+    for (int i = 1; i < 4; ++i) t += lds[i][slot];
     if (q < quads) {
         const int tile = (int)(local / per), e = (int)(local % per), frag = e / 64, l = e % 64;
         const int n = column_of(tile / nz * nt + frag / (kt / 16) * 16 + (l & 15), a.n);
@@ -455,7 +464,7 @@ hipError_t grad_run(const GradArgs &a, bool dw_f32, const GradPlan &p, char *wor
         const int64_t quads = (a.dw ? (int64_t)p.ny * p.nz * p.nt * p.kt : 0) / 4 + (a.db ? p.ny * p.nt / 4 : 0);
         const int parts = a.m > 0 ? p.parts : 0;
         const auto join = dw_f32 ? grad_join_kernel<float> : grad_join_kernel<T>;
-        join<<<dim3((unsigned)div_up(quads, 64)), 512, 0, stream>>>(part, parts, p.nt, p.kt, p.ny, p.nz, a);
+        join<<<dim3((unsigned)div_up(quads, 16)), 512, 0, stream>>>(part, parts, p.nt, p.kt, p.ny, p.nz, a);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     if (a.dx && a.m > 0 && !p.fused) {

@@ -13,6 +13,7 @@ using hg::abi_ok;
 constexpr int64_t kMaxRows = (int64_t)1 << 40;
 constexpr int kMaxWidth = 65536;
 constexpr int kMaxColumns = 1 << 20;
+constexpr int64_t kMaxGradStride = (int64_t)1 << 22;  // of a backward's rows: a step's offsets are 32-bit
 
 int size_of(int dtype) {
     switch (dtype) {
@@ -101,6 +102,8 @@ int check_linear_grad(const hg_linear_grad *op) {
     if ((rc = check_rows("w", op->w, op->w_stride, op->n, op->k, op->dtype, rows && op->dx))) return rc;
     if ((rc = check_rows("dx", op->dx, op->dx_stride, op->m, op->k, op->dtype, false))) return rc;
     if ((rc = check_rows("dw", op->dw, op->dw_stride, op->n, op->k, op->dw_dtype, false))) return rc;
+    for (const int64_t stride : {op->dy_stride, op->pre_stride, op->x_stride, op->dx_stride})
+        if (stride > kMaxGradStride) return abi_fail(HG_EINVAL, "row stride %lld > 2^22", (long long)stride);
     return check_vector("db", op->db, false);
 }
 

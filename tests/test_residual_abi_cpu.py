@@ -60,7 +60,7 @@ GRAD = dict(m=4, k=8, n=8, dy=P, dy_stride=8, pre=P, pre_stride=8, x=P, x_stride
     (dict(dy_dtype=R.HG_BF16), B.HG_EUNSUPPORTED, "dy_dtype"), (dict(dw_dtype=R.HG_F8), B.HG_EUNSUPPORTED, "dw_dtype"),
     (dict(dy=None), B.HG_EINVAL, "dy is NULL"), (dict(pre=None), B.HG_EINVAL, "pre is NULL"), (dict(x=None), B.HG_EINVAL, "x is NULL"),
     (dict(w=None), B.HG_EINVAL, "w is NULL"), (dict(dw_stride=4), B.HG_EINVAL, "stride"), (dict(dx_stride=4), B.HG_EINVAL, "stride"),
-    (dict(db=P + 1), B.HG_EINVAL, "aligned"), (dict(dy=P + 1), B.HG_EINVAL, "aligned"),
+    (dict(db=P + 1), B.HG_EINVAL, "aligned"), (dict(dy=P + 1), B.HG_EINVAL, "aligned"), (dict(x_stride=(1 << 22) + 1), B.HG_EINVAL, "stride"),
 ])
 def test_linear_backward_refuses(lib, change, code, word):
     op = R._LinearGrad(**(GRAD | change))
