@@ -462,7 +462,7 @@ int hashgrid_linear_backward(const hg_linear_grad *op, void *workspace, size_t w
  * unrounded s).  With y_dtype HG_F8 each row has a scale, y_scale = max |s q w|
  * / 448, and y holds s q w / y_scale rounded to nearest even: the 8-bit operand
  * and x_scale of hashgrid_linear_forward.  A row of zeros has scale 0; a row
- * with a NaN has scale NaN.  y and sum may be x or r themselves (same stride
+ * with a y that is not finite has scale NaN.  y and sum may be x or r themselves (same stride
  * and type). */
 typedef struct {
     int64_t m;             /* rows, >= 0                                              */

@@ -34,74 +34,96 @@ __device__ __forceinline__ void store_loose(void *p, V v) {
     reinterpret_cast<Loose<V> *>(p)->v = v;
 }
 
-// 8 consecutive elements at p as floats; only the first `left` exist (the
-// others read as zero and are not touched).
-template <typename T>
-__device__ __forceinline__ void load8(const T *p, int left, float (&v)[8]) {
-    if constexpr (sizeof(T) == 2) {
-        typedef T T8 __attribute__((ext_vector_type(8)));
-        if (left >= 8) {
-            const T8 a = load_loose<T8>(p);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = (float)a[j];
-            return;
-        }
-    } else {
-        if (left >= 8) {
-            const f32x4 a = load_loose<f32x4>(p), b = load_loose<f32x4>(p + 4);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] = a[j], v[4 + j] = b[j];
-            return;
-        }
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        v[j] = 0.f;
-        if (j < left) v[j] = (float)p[j];
-    }
+// The columns of one piece of 8 of a row of `width` columns.  The piece that the
+// row's end cuts is read so that it ends with the row; its first `drop` slots
+// belong to the piece before it, and all 8 of a piece past the row do not count.
+// So every piece is one wide access, without branches, and the compiler can count
+// the loads in flight.  Slot j is column at + j.  Rows of less than 8 columns are
+// read value by value.
+struct Columns {
+    int at, drop;
+};
+__device__ __forceinline__ Columns columns_of(int nominal, int width) {
+    if (width < 8) return {0, nominal < width ? 0 : 8};
+    const int at = nominal < width - 8 ? nominal : width - 8;
+    return {at, nominal - at};
+}
+// The column of a slot, or -1 of one that does not count.
+__device__ __forceinline__ int column_of(int slot, int width) {
+    const Columns c = columns_of(slot / 8 * 8, width);
+    const int j = slot % 8;
+    return j < c.drop || c.at + j >= width ? -1 : c.at + j;
 }
 
-// Stores the first `left` of 8 values, each rounded to nearest even.
-template <typename T>
-__device__ __forceinline__ void store8(T *p, int left, const float (&v)[8]) {
+// A row's piece as floats.  kShort: rows may have less than 8 columns; their loads
+// do not wait for each other either, and what is past them is zero.
+template <bool kShort, typename T>
+__device__ __forceinline__ void load8(const T *row, Columns c, int width, float (&v)[8]) {
+    if (!kShort || width >= 8) {
+        if constexpr (sizeof(T) == 2) {
+            typedef T T8 __attribute__((ext_vector_type(8)));
+            const T8 a = load_loose<T8>(row + c.at);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = (float)a[j];
+        } else {
+            const f32x4 a = load_loose<f32x4>(row + c.at), b = load_loose<f32x4>(row + c.at + 4);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = a[j], v[4 + j] = b[j];
+        }
+        return;
+    }
+    T t[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) t[j] = row[j < width ? j : width - 1];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = j < width && c.drop == 0 ? (float)t[j] : 0.f;
+}
+
+// Stores a row's piece, each value rounded to nearest even.  The slots that the
+// piece before holds too are written twice, with the same values.
+template <bool kShort, typename T>
+__device__ __forceinline__ void store8(T *row, Columns c, int width, const float (&v)[8]) {
+    if (c.drop >= 8) return;
+    T *const p = row + c.at;
     if constexpr (sizeof(T) == 2) {
         typedef T T8 __attribute__((ext_vector_type(8)));
         T8 a;
 #pragma unroll
         for (int j = 0; j < 8; ++j) a[j] = (T)v[j];
-        if (left >= 8) {
+        if (!kShort || width >= 8) {
             store_loose<T8>(p, a);
             return;
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            if (j < left) p[j] = a[j];
+            if (j < width) p[j] = a[j];
     } else if constexpr (sizeof(T) == 4) {
-        if (left >= 8) {
+        if (!kShort || width >= 8) {
             store_loose<f32x4>(p, f32x4{v[0], v[1], v[2], v[3]});
             store_loose<f32x4>(p + 4, f32x4{v[4], v[5], v[6], v[7]});
             return;
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            if (j < left) p[j] = v[j];
+            if (j < width) p[j] = v[j];
     } else {
         int lo = 0, hi = 0;
         lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], lo, false);
         lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], lo, true);
         hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[4], v[5], hi, false);
         hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[6], v[7], hi, true);
-        if (left >= 8) {
+        if (!kShort || width >= 8) {
             store_loose<u32x2>(p, u32x2{(uint32_t)lo, (uint32_t)hi});
             return;
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            if (j < left) p[j].bits = (uint8_t)((j < 4 ? lo : hi) >> (8 * (j & 3)));
+            if (j < width) p[j].bits = (uint8_t)((j < 4 ? lo : hi) >> (8 * (j & 3)));
     }
 }
 
-// N values as they lie in memory, to be held until they are used.
+// N values as they lie in memory, to be held until they are used; of those past
+// `left` nothing is said.
 template <int N, typename T>
 struct Held {
     T v __attribute__((ext_vector_type(N)));
@@ -112,12 +134,9 @@ __device__ __forceinline__ Held<N, T> hold(const T *p, int left) {
     Held<N, T> h;
     if (left >= N) {
         h.v = load_loose<V>(p);
-    } else {
+    } else if (left > 0) {  // loads that do not wait for each other
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-            h.v[j] = (T)0.f;
-            if (j < left) h.v[j] = p[j];
-        }
+        for (int j = 0; j < N; ++j) h.v[j] = p[j < left ? j : left - 1];
     }
     return h;
 }

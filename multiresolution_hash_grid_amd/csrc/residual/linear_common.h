@@ -59,20 +59,21 @@ __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 acc) {
     }
 }
 
-// The 16-byte piece at p of a row that has `left` more elements; what lies
-// past them is zero and is not touched.
+// The first piece of a row of fewer values than a piece, zeros past it; the loads
+// do not wait for each other.
 template <typename T>
-__device__ __forceinline__ u32x4 load_piece(const T *p, int left) {
-    if (left >= kPiece<T>) return load_loose<u32x4>(p);
+__device__ __forceinline__ u32x4 load_short(const T *row, int length) {
+    T t[kPiece<T>];
+#pragma unroll
+    for (int j = 0; j < kPiece<T>; ++j) t[j] = row[j < length ? j : length - 1];
     u32x4 v = {0, 0, 0, 0};
-    if constexpr (sizeof(T) == 2) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (j < left) v[j / 2] |= (uint32_t)__builtin_bit_cast(uint16_t, p[j]) << (16 * (j & 1));
-    } else {
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-            if (j < left) v[j / 4] |= (uint32_t)p[j].bits << (8 * (j & 3));
+    for (int j = 0; j < kPiece<T>; ++j) {
+        uint32_t bits;
+        if constexpr (sizeof(T) == 2) bits = __builtin_bit_cast(uint16_t, t[j]);
+        else bits = t[j].bits;
+        constexpr int per = 4 / (int)sizeof(T);
+        if (j < length) v[j / per] |= bits << (8 * (int)sizeof(T) * (j % per));
     }
     return v;
 }

@@ -46,33 +46,13 @@ __device__ __forceinline__ u32x4 tile_columns(char *tile, int m, int q, int lane
     return r.v;
 }
 
-// The columns of one piece of a row of `width` columns.  Loads are the same for
-// every piece, without branches, so that the compiler can count them and a step
-// waits for its own loads alone: the piece that the row's end cuts is read so
-// that it ends with the row, and its first `drop` slots, which the piece before
-// holds, are zeroed where the piece is used (all 8 of a piece past the row).
-// Slots therefore stand for column at + slot; the join knows.  Rows of less
-// than a piece are read value by value.
-struct Columns {
-    int at, drop;
-};
-__device__ __forceinline__ Columns columns_of(int nominal, int width) {
-    if (width < 8) return {nominal, nominal < width ? 0 : 8};
-    const int at = nominal < width - 8 ? nominal : width - 8;
-    return {at, nominal - at};
-}
-// The column of a slot, or -1 of a zeroed one.
-__device__ __forceinline__ int column_of(int slot, int width) {
-    const Columns c = columns_of(slot / 8 * 8, width);
-    const int j = slot % 8;
-    return j < c.drop || c.at + j >= width ? -1 : c.at + j;
-}
-
+// Pieces of dz and x are cut as Columns has it, slots that do not count zeroed
+// where a piece is used; the join knows which column a slot stands for.
 // The piece at p; kShort: rows may be shorter than a piece (the narrowest tiles').
 template <bool kShort, typename T>
 __device__ __forceinline__ u32x4 load_columns(const T *p, Columns c, int width) {
     if (!kShort || width >= 8) return load_loose<u32x4>(p);
-    return load_piece(p, c.drop ? 0 : width);
+    return c.drop ? u32x4{0, 0, 0, 0} : load_short(p, width);
 }
 
 // One piece of dz: 8 values from dy and z.
@@ -88,8 +68,11 @@ __device__ __forceinline__ RawDz<T, D> load_dz(const GradArgs &a, const D *dy, c
         if (!kShort || a.n >= 8) {
             v.dy[0] = load_loose<u32x4>(dy), v.dy[1] = load_loose<u32x4>(dy + 4);
         } else {
+            uint32_t t[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v.dy[j / 4][j % 4] = c.drop == 0 && j < a.n ? __float_as_uint(dy[j]) : 0u;
+            for (int j = 0; j < 8; ++j) t[j] = __float_as_uint(dy[j < a.n ? j : a.n - 1]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v.dy[j / 4][j % 4] = c.drop == 0 && j < a.n ? t[j] : 0u;
         }
     } else {
         v.dy[0] = load_columns<kShort>(dy, c, a.n);
@@ -133,19 +116,30 @@ __device__ __forceinline__ u32x4 pack8(const float (&v)[8]) {
     return __builtin_bit_cast(u32x4, p);
 }
 
-// W^T of rows n < NT, columns k0 .. k0 + KT in LDS as fragments for dx: block
+// A cut piece moved so that its first slot that counts is slot 0.
+__device__ __forceinline__ u32x4 shifted(u32x4 v, int drop) {
+    if (drop & 4) v = u32x4{v[2], v[3], 0, 0};
+    if (drop & 2) v = u32x4{v[1], v[2], v[3], 0};
+    if (drop & 1) v = u32x4{v[0] >> 16 | v[1] << 16, v[1] >> 16 | v[2] << 16, v[2] >> 16 | v[3] << 16, v[3] >> 16};
+    return v;
+}
+
+// W^T of rows n < NT, columns k < KT in LDS as fragments for dx: block
 // (pair s of 16-column fragments, fragment f, step u of 32 rows n), lane (i, g):
 // column 32 s + (i / 4) 8 + 4 f + i % 4, rows 32 u + 8 g .. + 7.  A thread turns
 // 8 x 8 values: eight pieces of eight rows, two rows' halves merged at a time.
 template <typename T, int NT, int KT>
-__device__ __forceinline__ void stage_wt(const GradArgs &a, int k0, u32x4 *wt) {
+__device__ __forceinline__ void stage_wt(const GradArgs &a, u32x4 *wt) {
     for (int b = threadIdx.x; b < NT / 8 * (KT / 8); b += kGradThreads) {
         const int k8 = b % (KT / 8), n8 = b / (KT / 8);
         u32x4 row[8];
 #pragma unroll
         for (int r = 0; r < 8; ++r) {
             const int n = column_of(n8 * 8 + r, a.n);
-            row[r] = load_piece((const T *)a.w + (int64_t)n * a.ws + k0 + k8 * 8, n >= 0 ? a.k - k0 - k8 * 8 : 0);
+            const T *const w = (const T *)a.w + (int64_t)(n < 0 ? 0 : n) * a.ws;
+            const Columns c = columns_of(k8 * 8, a.k);
+            row[r] = a.k < 8 ? load_short(w, a.k) : shifted(load_loose<u32x4>(w + c.at), c.drop);
+            if (n < 0 || c.drop >= 8) row[r] = u32x4{0, 0, 0, 0};
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -191,7 +185,7 @@ __global__ __launch_bounds__(kGradThreads) void grad_kernel(const GradArgs a, fl
         asm volatile("" : "+v"(t));
         return t;
     };
-    if constexpr (kDx) stage_wt<T, NT, KT>(a, 0, wt);
+    if constexpr (kDx) stage_wt<T, NT, KT>(a, wt);
 
     f32x4 acc[FN][FK];
 #pragma unroll
@@ -268,7 +262,8 @@ __global__ __launch_bounds__(kGradThreads) void grad_kernel(const GradArgs a, fl
             *(u32x4 *)(dzt + tile_at<NT>(r, t % PN)) = pack8<T>(dz);
             if (store_dz && step * R + r < a.m) {
                 T *const p = dz_out + (step * R + r) * a.n + cn.at;
-                if (cn.drop == 0) store8(p, a.n < 8 ? a.n : 8, dz);
+                const int have = a.n < 8 ? a.n : 8;
+                if (cn.drop == 0) put(p, have, rounded<8, T>(dz));
                 else
 #pragma unroll
                     for (int j = 0; j < 8; ++j)

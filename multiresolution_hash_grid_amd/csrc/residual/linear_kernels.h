@@ -21,8 +21,18 @@ __global__ __launch_bounds__(256) void linear_tile_kernel(const FwdArgs a) {
     const int wn = n0 + (lane & 15) < a.n ? n0 + (lane & 15) : a.n - 1;
     const T *x = (const T *)a.x + xm * a.xs, *w = (const T *)a.w + (int64_t)wn * a.ws;
     f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-    for (int k = wave * kStretch<T> + (lane >> 4) * kPiece<T>; k - (lane >> 4) * kPiece<T> < a.k; k += 4 * kStretch<T>)
-        acc = mma<T>(load_piece(w + k, a.k - k), load_piece(x + k, a.k - k), acc);
+    const int group = lane >> 4;
+    if (a.k < kPiece<T>) {
+        if (wave == 0) {
+            const u32x4 none = {0, 0, 0, 0};
+            acc = mma<T>(group ? none : load_short(w, a.k), group ? none : load_short(x, a.k), acc);
+        }
+    } else {
+        for (int k0 = wave * kStretch<T>; k0 < a.k; k0 += 4 * kStretch<T>) {
+            const Cut<T> c = cut_piece<T>(k0 + group * kPiece<T>, a.k);
+            acc = mma<T>(load_loose<u32x4>(w + c.at) & c.mask, load_loose<u32x4>(x + c.at) & c.mask, acc);
+        }
+    }
     sums[wave][lane] = acc;
     __syncthreads();
     // thread t: row t / 16, output t % 16; it lies in lane (output / 4) * 16 + row, word output % 4
@@ -116,7 +126,7 @@ __global__ __launch_bounds__(RF == 1 ? 1024 : 512) void linear_stream_kernel(con
     // The last fragment's piece of this lane.
     const Cut<T> last = cut_piece<T>((KU - 1) * kStretch<T> + group * kPiece<T>, a.k);
     auto piece = [&](const T *row, int u) -> u32x4 {
-        if constexpr (kCut == 2) return load_piece(row + group * kPiece<T>, a.k - group * kPiece<T>);
+        if constexpr (kCut == 2) return group ? u32x4{0, 0, 0, 0} : load_short(row, a.k);
         if (kCut == 1 && u == KU - 1) return load_loose<u32x4>(row + last.at) & last.mask;
         return load_loose<u32x4>(row + group * kPiece<T> + u * kStretch<T>);
     };

@@ -15,7 +15,26 @@ namespace res {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kWide = 4096;  // columns a wave holds (64 lanes x 8 vectors of 8)
+constexpr int kWide = 4096;  // columns that a workgroup holds (256 threads x 2 vectors of 8)
+
+// Sum or maximum over the G lanes of a row, in each of them: lanes of a wave, or
+// (G = 256) the workgroup, through one of two LDS slots in turn, so that one
+// barrier is enough.
+template <int G, bool kMax>
+__device__ __forceinline__ float row_all(float v, float (*lds)[kThreads / 64], int &turn) {
+    auto join = [](float a, float b) { return kMax ? fmaxf(a, b) : a + b; };
+#pragma unroll
+    for (int o = 1; o < (G < 64 ? G : 64); o <<= 1) v = join(v, __shfl_xor(v, o, 64));
+    if constexpr (G == kThreads) {
+        if ((threadIdx.x & 63) == 0) lds[turn][threadIdx.x >> 6] = v;
+        __syncthreads();
+        v = lds[turn][0];
+#pragma unroll
+        for (int i = 1; i < kThreads / 64; ++i) v = join(v, lds[turn][i]);
+        turn ^= 1;
+    }
+    return v;
+}
 
 struct NormArgs {
     int64_t m, xs, rs, ys, ss;
@@ -30,42 +49,48 @@ struct NormArgs {
 // Rows of at most G * I * 8 columns, G lanes a row.
 template <typename T, typename Y, int G, int I>
 __global__ __launch_bounds__(kThreads) void norm_kernel(const NormArgs a) {
+    __shared__ float lds[2][kThreads / 64];
+    int turn = 0;
     const int lane = threadIdx.x % G;
     const int64_t rows = (int64_t)gridDim.x * (kThreads / G);
     float w[I][8];
-    int left[I];
+    Columns at[I];
 #pragma unroll
     for (int i = 0; i < I; ++i) {
-        left[i] = a.c - (i * G + lane) * 8;
-        load8(a.w + (i * G + lane) * 8, left[i], w[i]);
+        at[i] = columns_of((i * G + lane) * 8, a.c);
+        load8<G == 4>(a.w, at[i], a.c, w[i]);
     }
     for (int64_t row = (int64_t)blockIdx.x * (kThreads / G) + threadIdx.x / G; row < a.m; row += rows) {
         float v[I][8];
-        const T *x = (const T *)a.x + row * a.xs + lane * 8;
-        const T *r = (const T *)a.r + row * a.rs + lane * 8;
 #pragma unroll
-        for (int i = 0; i < I; ++i) load8(x + i * G * 8, left[i], v[i]);
+        for (int i = 0; i < I; ++i) load8<G == 4>((const T *)a.x + row * a.xs, at[i], a.c, v[i]);
         if (a.r) {
 #pragma unroll
             for (int i = 0; i < I; ++i) {
                 float t[8];
-                load8(r + i * G * 8, left[i], t);
+                load8<G == 4>((const T *)a.r + row * a.rs, at[i], a.c, t);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) v[i][j] += t[j];
             }
         }
         float sq = 0.f;
 #pragma unroll
-        for (int i = 0; i < I; ++i)
+        for (int i = 0; i < I; ++i) {
+            if (a.c % 8 == 0) {
+                float t = 0.f;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) sq = fmaf(v[i][j], v[i][j], sq);
-        sq = group_sum<G>(sq);
-        const float q = 1.f / sqrtf(sq * a.inv_c + a.eps);
-        if (a.s) {
-            T *s = (T *)a.s + row * a.ss + lane * 8;
+                for (int j = 0; j < 8; ++j) t = fmaf(v[i][j], v[i][j], t);
+                sq += at[i].drop ? 0.f : t;
+            } else {
 #pragma unroll
-            for (int i = 0; i < I; ++i) store8(s + i * G * 8, left[i], v[i]);
+                for (int j = 0; j < 8; ++j) sq += j < at[i].drop ? 0.f : v[i][j] * v[i][j];
+            }
         }
+        sq = row_all<G, false>(sq, lds, turn);
+        const float q = 1.f / sqrtf(sq * a.inv_c + a.eps);
+        if (a.s)
+#pragma unroll
+            for (int i = 0; i < I; ++i) store8<G == 4>((T *)a.s + row * a.ss, at[i], a.c, v[i]);
         if (a.rstd && lane == 0) a.rstd[row] = q;
 #pragma unroll
         for (int i = 0; i < I; ++i)
@@ -80,9 +105,9 @@ __global__ __launch_bounds__(kThreads) void norm_kernel(const NormArgs a) {
                     top = fmaxf(top, fabsf(v[i][j]));
                     bad = v[i][j] != v[i][j] ? 1.f : bad;
                 }
-            top = group_max<G>(top);
-            bad = group_max<G>(bad);
-            if (bad != 0.f) top = __builtin_nanf("");  // a row with a NaN has the scale NaN
+            if (bad != 0.f) top = __builtin_inff();  // a row with a NaN has the scale NaN: larger than any maximum on the way
+            top = row_all<G, true>(top, lds, turn);
+            if (top == __builtin_inff()) top = __builtin_nanf("");
             const float inv = top > 0.f ? 448.f / top : 0.f;
 #pragma unroll
             for (int i = 0; i < I; ++i)
@@ -90,75 +115,85 @@ __global__ __launch_bounds__(kThreads) void norm_kernel(const NormArgs a) {
                 for (int j = 0; j < 8; ++j) v[i][j] = fminf(fmaxf(v[i][j] * inv, -448.f), 448.f);
             if (lane == 0) a.scale[row] = top / 448.f;
         }
-        Y *y = (Y *)a.y + row * a.ys + lane * 8;
 #pragma unroll
-        for (int i = 0; i < I; ++i) store8(y + i * G * 8, left[i], v[i]);
+        for (int i = 0; i < I; ++i) store8<G == 4>((Y *)a.y + row * a.ys, at[i], a.c, v[i]);
     }
 }
 
-// Sum (or maximum) over the workgroup, in every thread.
-template <bool kMax>
-__device__ __forceinline__ float block_all(float v, float *lds) {
-    v = kMax ? group_max<64>(v) : group_sum<64>(v);
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
-    __syncthreads();
-    float t = lds[0];
-    for (int i = 1; i < kThreads / 64; ++i) t = kMax ? fmaxf(t, lds[i]) : t + lds[i];
-    return t;
+// store8 without the slots that the piece before holds too.
+template <typename T>
+__device__ __forceinline__ void store_own(T *row, Columns c, int width, const float (&v)[8]) {
+    if (c.drop == 0) {
+        store8<false>(row, c, width, v);
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        if (j >= c.drop) {
+            if constexpr (sizeof(T) == 1) row[c.at + j].bits = (uint8_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[j], v[j], 0, false);
+            else row[c.at + j] = (T)v[j];
+        }
 }
 
 // Rows of any length, a workgroup a row: the row is read again for its output
 // (it is in L2 by then).
 template <typename T, typename Y>
 __global__ __launch_bounds__(kThreads) void norm_long_kernel(const NormArgs a) {
-    __shared__ float lds[kThreads / 64];
+    __shared__ float lds[2][kThreads / 64];
+    int turn = 0;
     for (int64_t row = blockIdx.x; row < a.m; row += gridDim.x) {
         const T *x = (const T *)a.x + row * a.xs, *r = (const T *)a.r + row * a.rs;
-        auto sum8 = [&](int at, float (&v)[8]) {
-            load8(x + at, a.c - at, v);
+        auto sum8 = [&](Columns at, float (&v)[8]) {
+            load8<false>(x, at, a.c, v);
             if (a.r) {
                 float t[8];
-                load8(r + at, a.c - at, t);
+                load8<false>(r, at, a.c, t);
+#pragma unroll
                 for (int j = 0; j < 8; ++j) v[j] += t[j];
             }
         };
         float sq = 0.f, v[8], w[8];
-        for (int at = threadIdx.x * 8; at < a.c; at += kThreads * 8) {
+        for (int k = threadIdx.x * 8; k < a.c; k += kThreads * 8) {
+            const Columns at = columns_of(k, a.c);
             sum8(at, v);
-            for (int j = 0; j < 8; ++j) sq = fmaf(v[j], v[j], sq);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sq += j < at.drop ? 0.f : v[j] * v[j];
         }
-        sq = block_all<false>(sq, lds);
+        sq = row_all<kThreads, false>(sq, lds, turn);
         const float q = 1.f / sqrtf(sq * a.inv_c + a.eps);
         if (a.rstd && threadIdx.x == 0) a.rstd[row] = q;
         float inv = 1.f;
         if constexpr (sizeof(Y) == 1) {
             float top = 0.f, bad = 0.f;
-            for (int at = threadIdx.x * 8; at < a.c; at += kThreads * 8) {
+            for (int k = threadIdx.x * 8; k < a.c; k += kThreads * 8) {
+                const Columns at = columns_of(k, a.c);
                 sum8(at, v);
-                load8(a.w + at, a.c - at, w);
+                load8<false>(a.w, at, a.c, w);
+#pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const float y = v[j] * q * w[j];
                     top = fmaxf(top, fabsf(y));
                     bad = y != y ? 1.f : bad;
                 }
             }
-            top = block_all<true>(top, lds);
-            bad = block_all<true>(bad, lds);
-            if (bad != 0.f) top = __builtin_nanf("");
+            if (bad != 0.f) top = __builtin_inff();
+            top = row_all<kThreads, true>(top, lds, turn);
+            if (top == __builtin_inff()) top = __builtin_nanf("");
             inv = top > 0.f ? 448.f / top : 0.f;
             if (threadIdx.x == 0) a.scale[row] = top / 448.f;
         }
-        for (int at = threadIdx.x * 8; at < a.c; at += kThreads * 8) {
+        for (int k = threadIdx.x * 8; k < a.c; k += kThreads * 8) {
+            const Columns at = columns_of(k, a.c);
             sum8(at, v);
-            load8(a.w + at, a.c - at, w);
-            // s may be x or r itself: this thread has read what it overwrites
-            if (a.s) store8((T *)a.s + row * a.ss + at, a.c - at, v);
+            load8<false>(a.w, at, a.c, w);
+            // s and y may be x or r themselves: each thread writes columns of its own
+            if (a.s) store_own((T *)a.s + row * a.ss, at, a.c, v);
+#pragma unroll
             for (int j = 0; j < 8; ++j) {
                 v[j] = v[j] * q * w[j];
                 if constexpr (sizeof(Y) == 1) v[j] = fminf(fmaxf(v[j] * inv, -448.f), 448.f);
             }
-            store8((Y *)a.y + row * a.ys + at, a.c - at, v);
+            store_own((Y *)a.y + row * a.ys, at, a.c, v);
         }
     }
 }
@@ -179,8 +214,8 @@ void norm_pick(const NormArgs &a, hipStream_t stream) {
     else if (v <= 32) norm_run<T, Y, 32, 1>(a, stream);
     else if (v <= 64) norm_run<T, Y, 64, 1>(a, stream);
     else if (v <= 128) norm_run<T, Y, 64, 2>(a, stream);
-    else if (v <= 256) norm_run<T, Y, 64, 4>(a, stream);
-    else if (v <= 512) norm_run<T, Y, 64, 8>(a, stream);
+    else if (v <= 256) norm_run<T, Y, 256, 1>(a, stream);
+    else if (v <= 512) norm_run<T, Y, 256, 2>(a, stream);
     else {
         const int64_t most = kCus * 8;
         norm_long_kernel<T, Y><<<dim3((unsigned)(a.m < most ? a.m : most)), kThreads, 0, stream>>>(a);
@@ -202,55 +237,54 @@ struct GradArgs {
 // order and written as one partial row, so dw does not depend on scheduling.
 template <typename T, int G, int I>
 __global__ __launch_bounds__(kThreads) void norm_grad_kernel(const GradArgs a) {
-    __shared__ float lds[kThreads * 8];
+    __shared__ float lds[kThreads * 8], ends[2][kThreads / 64];
+    int turn = 0;
     const int lane = threadIdx.x % G;
     const int64_t rows = (int64_t)gridDim.x * (kThreads / G);
     float w[I][8], dw[I][8];
-    int left[I];
+    Columns at[I];
 #pragma unroll
     for (int i = 0; i < I; ++i) {
-        left[i] = a.c - (i * G + lane) * 8;
-        load8(a.w + (i * G + lane) * 8, left[i], w[i]);
+        at[i] = columns_of((i * G + lane) * 8, a.c);
+        load8<G == 4>(a.w, at[i], a.c, w[i]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) dw[i][j] = 0.f;
     }
     for (int64_t row = (int64_t)blockIdx.x * (kThreads / G) + threadIdx.x / G; row < a.m; row += rows) {
-        float dy[I][8], h[I][8];
-        const T *py = (const T *)a.dy + row * a.dys + lane * 8, *ps = (const T *)a.s + row * a.ss + lane * 8;
+        float dy[I][8], h[I][8], ds[I][8];
 #pragma unroll
         for (int i = 0; i < I; ++i) {
-            load8(py + i * G * 8, left[i], dy[i]);
-            load8(ps + i * G * 8, left[i], h[i]);
+            load8<G == 4>((const T *)a.dy + row * a.dys, at[i], a.c, dy[i]);
+            load8<G == 4>((const T *)a.s + row * a.ss, at[i], a.c, h[i]);
         }
+        if (a.ds)
+#pragma unroll
+            for (int i = 0; i < I; ++i) load8<G == 4>((const T *)a.ds + row * a.dss, at[i], a.c, ds[i]);
         const float q = a.rstd[row];
         float dot = 0.f;
 #pragma unroll
-        for (int i = 0; i < I; ++i)
+        for (int i = 0; i < I; ++i) {
+            float t = 0.f;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 h[i][j] *= q;
                 dw[i][j] = fmaf(dy[i][j], h[i][j], dw[i][j]);
                 dy[i][j] *= w[i][j];
-                dot = fmaf(dy[i][j], h[i][j], dot);
+                if (a.c % 8 == 0) t = fmaf(dy[i][j], h[i][j], t);
+                else t += j < at[i].drop ? 0.f : dy[i][j] * h[i][j];
             }
-        dot = group_sum<G>(dot) * a.inv_c;
-#pragma unroll
-        for (int i = 0; i < I; ++i)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) dy[i][j] = q * (dy[i][j] - h[i][j] * dot);
-        if (a.ds) {
-            const T *pd = (const T *)a.ds + row * a.dss + lane * 8;
-#pragma unroll
-            for (int i = 0; i < I; ++i) {
-                float t[8];
-                load8(pd + i * G * 8, left[i], t);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) dy[i][j] += t[j];
-            }
+            dot += at[i].drop >= 8 ? 0.f : t;
         }
-        T *px = (T *)a.dx + row * a.dxs + lane * 8;
+        dot = row_all<G, false>(dot, ends, turn) * a.inv_c;
 #pragma unroll
-        for (int i = 0; i < I; ++i) store8(px + i * G * 8, left[i], dy[i]);
+        for (int i = 0; i < I; ++i) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                dy[i][j] = q * (dy[i][j] - h[i][j] * dot);
+                if (a.ds) dy[i][j] += ds[i][j];
+            }
+            store8<G == 4>((T *)a.dx + row * a.dxs, at[i], a.c, dy[i]);
+        }
     }
     if (!a.part) return;
 #pragma unroll
@@ -262,8 +296,8 @@ __global__ __launch_bounds__(kThreads) void norm_grad_kernel(const GradArgs a) {
         for (int k = threadIdx.x; k < G * 8; k += kThreads) {
             float t = 0.f;
             for (int g = 0; g < kThreads / G; ++g) t += lds[g * G * 8 + k];
-            const int col = i * G * 8 + k;
-            if (col < a.c) a.part[(int64_t)blockIdx.x * a.c + col] = t;
+            const int col = column_of(i * G * 8 + k, a.c);
+            if (col >= 0) a.part[(int64_t)blockIdx.x * a.c + col] = t;
         }
     }
 }
@@ -271,28 +305,34 @@ __global__ __launch_bounds__(kThreads) void norm_grad_kernel(const GradArgs a) {
 // dx of rows of any length, and dw in a pass of its own (below).
 template <typename T>
 __global__ __launch_bounds__(kThreads) void norm_grad_long_kernel(const GradArgs a) {
-    __shared__ float lds[kThreads / 64];
+    __shared__ float lds[2][kThreads / 64];
+    int turn = 0;
     for (int64_t row = blockIdx.x; row < a.m; row += gridDim.x) {
         const T *py = (const T *)a.dy + row * a.dys, *ps = (const T *)a.s + row * a.ss;
         const float q = a.rstd[row];
         float dot = 0.f, dy[8], s[8], w[8], t[8];
-        for (int at = threadIdx.x * 8; at < a.c; at += kThreads * 8) {
-            load8(py + at, a.c - at, dy);
-            load8(ps + at, a.c - at, s);
-            load8(a.w + at, a.c - at, w);
-            for (int j = 0; j < 8; ++j) dot = fmaf(dy[j] * w[j], s[j] * q, dot);
+        for (int k = threadIdx.x * 8; k < a.c; k += kThreads * 8) {
+            const Columns at = columns_of(k, a.c);
+            load8<false>(py, at, a.c, dy);
+            load8<false>(ps, at, a.c, s);
+            load8<false>(a.w, at, a.c, w);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) dot += j < at.drop ? 0.f : dy[j] * w[j] * (s[j] * q);
         }
-        dot = block_all<false>(dot, lds) * a.inv_c;
-        for (int at = threadIdx.x * 8; at < a.c; at += kThreads * 8) {
-            load8(py + at, a.c - at, dy);
-            load8(ps + at, a.c - at, s);
-            load8(a.w + at, a.c - at, w);
+        dot = row_all<kThreads, false>(dot, lds, turn) * a.inv_c;
+        for (int k = threadIdx.x * 8; k < a.c; k += kThreads * 8) {
+            const Columns at = columns_of(k, a.c);
+            load8<false>(py, at, a.c, dy);
+            load8<false>(ps, at, a.c, s);
+            load8<false>(a.w, at, a.c, w);
+#pragma unroll
             for (int j = 0; j < 8; ++j) dy[j] = q * (dy[j] * w[j] - s[j] * q * dot);
             if (a.ds) {
-                load8((const T *)a.ds + row * a.dss + at, a.c - at, t);
+                load8<false>((const T *)a.ds + row * a.dss, at, a.c, t);
+#pragma unroll
                 for (int j = 0; j < 8; ++j) dy[j] += t[j];
             }
-            store8((T *)a.dx + row * a.dxs + at, a.c - at, dy);
+            store8<false>((T *)a.dx + row * a.dxs, at, a.c, dy);
         }
     }
 }
@@ -300,44 +340,53 @@ __global__ __launch_bounds__(kThreads) void norm_grad_long_kernel(const GradArgs
 // over its rows.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void norm_dw_long_kernel(const GradArgs a) {
-    const int at = (blockIdx.x * kThreads + threadIdx.x) * 8;
-    if (at >= a.c) return;
+    const Columns at = columns_of((blockIdx.x * kThreads + threadIdx.x) * 8, a.c);
+    if (at.drop >= 8) return;
     float dw[8] = {}, dy[8], s[8];
     for (int64_t row = blockIdx.y; row < a.m; row += gridDim.y) {
-        load8((const T *)a.dy + row * a.dys + at, a.c - at, dy);
-        load8((const T *)a.s + row * a.ss + at, a.c - at, s);
+        load8<false>((const T *)a.dy + row * a.dys, at, a.c, dy);
+        load8<false>((const T *)a.s + row * a.ss, at, a.c, s);
         const float q = a.rstd[row];
+#pragma unroll
         for (int j = 0; j < 8; ++j) dw[j] = fmaf(dy[j], s[j] * q, dw[j]);
     }
-    store8(a.part + (int64_t)blockIdx.y * a.c + at, a.c - at, dw);
+    store8<false>(a.part + (int64_t)blockIdx.y * a.c, at, a.c, dw);
 }
 
-// dw = (dw +) the partial rows' sum: 64 columns a workgroup, 16 waves share the rows.
+// dw = (dw +) the partial rows' sum: 16 columns a workgroup, 64 threads share the
+// rows of each, and their sums are added in order, 16 and then four.
 __global__ __launch_bounds__(1024) void dw_join_kernel(const float *part, int rows, int c, float *dw, int accumulate) {
-    __shared__ float lds[16][64];
-    const int col = blockIdx.x * 64 + (threadIdx.x & 63), wave = threadIdx.x >> 6;
+    __shared__ float lds[64][16];
+    const int slot = threadIdx.x & 15, share = threadIdx.x >> 4, col = blockIdx.x * 16 + slot;
     float t = 0.f;
     if (col < c)
 #pragma unroll 8
-        for (int r = wave; r < rows; r += 16) t += part[(int64_t)r * c + col];
-    lds[wave][threadIdx.x & 63] = t;
+        for (int r = share; r < rows; r += 64) t += part[(int64_t)r * c + col];
+    lds[share][slot] = t;
     __syncthreads();
-    if (wave == 0 && col < c) {
-        for (int i = 1; i < 16; ++i) t += lds[i][threadIdx.x];
+    if (share < 4) {
+        t = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) t += lds[share * 16 + i][slot];
+    }
+    __syncthreads();
+    if (share < 4) lds[share][slot] = t;
+    __syncthreads();
+    if (share == 0 && col < c) {
+        t = lds[0][slot] + lds[1][slot] + lds[2][slot] + lds[3][slot];
         dw[col] = accumulate ? dw[col] + t : t;
     }
 }
 
 int grad_group(int c) {
     const int v = (c + 7) / 8;
-    return v <= 4 ? 4 : v <= 8 ? 8 : v <= 16 ? 16 : v <= 32 ? 32 : 64;
+    return v <= 4 ? 4 : v <= 8 ? 8 : v <= 16 ? 16 : v <= 32 ? 32 : v <= 128 ? 64 : 256;
 }
-// Workgroups (and partial rows) of a backward: enough to fill the chip twice
-// over, few enough that the partial rows stay small.
+// Workgroups (and partial rows) of a backward: as many as are resident.
 int64_t grad_groups(int64_t m, int c) {
     if (c > kWide) return m < 256 ? m : 256;
     if (m == 0) return 0;
-    const int64_t need = div_up(m, kThreads / grad_group(c)), most = kCus * 4;
+    const int64_t need = div_up(m, kThreads / grad_group(c)), most = kCus * 8;
     return need < most ? need : most;
 }
 
@@ -355,8 +404,8 @@ void grad_pick(const GradArgs &a, hipStream_t stream) {
     else if (v <= 32) grad_run<T, 32, 1>(a, stream);
     else if (v <= 64) grad_run<T, 64, 1>(a, stream);
     else if (v <= 128) grad_run<T, 64, 2>(a, stream);
-    else if (v <= 256) grad_run<T, 64, 4>(a, stream);
-    else if (v <= 512) grad_run<T, 64, 8>(a, stream);
+    else if (v <= 256) grad_run<T, 256, 1>(a, stream);
+    else if (v <= 512) grad_run<T, 256, 2>(a, stream);
     else {
         const int64_t most = kCus * 8;
         norm_grad_long_kernel<T><<<dim3((unsigned)(a.m < most ? a.m : most)), kThreads, 0, stream>>>(a);
@@ -391,7 +440,7 @@ hipError_t launch_rms_norm_backward(const hg_rms_norm_grad &op, void *workspace,
     else grad_pick<float>(a, stream);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || !op.dw) return e;
-    dw_join_kernel<<<dim3((unsigned)div_up(op.c, 64)), 1024, 0, stream>>>((const float *)workspace,
+    dw_join_kernel<<<dim3((unsigned)div_up(op.c, 16)), 1024, 0, stream>>>((const float *)workspace,
                                                                          (int)grad_groups(op.m, op.c), op.c, op.dw,
                                                                          op.accumulate);
     return hipGetLastError();

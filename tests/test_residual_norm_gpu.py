@@ -73,7 +73,7 @@ def test_backward(c, dtype, pad):
 
 def test_in_place():
     g = gen(3)
-    for c in (96, 5000):
+    for c in (3, 96, 101, 5000, 5003):
         x, r = wide(g, 50, c, BF16, 0), wide(g, 50, c, BF16, 0)
         w = torch.randn(c, generator=g).to(DEV)
         want = hg.hashgrid_rms_norm_forward(x, w, residual=r, save_sum=True)
