@@ -1,7 +1,8 @@
 """MI355X-native multiresolution hash-grid encoder.
 
 The encoder runs in ``libhashgrid.so`` (HIP kernels for gfx950 behind the C
-ABI of ``include/hashgrid.h``); ``hashgrid`` is its Python binding and
+ABI of ``include/hashgrid.h``); ``hashgrid`` is its Python binding,
+``residual`` that of the operators of a residual head on the encoding, and
 ``inputs`` the seeded synthetic workload generator.
 """
 from .hashgrid import (  # noqa: F401
@@ -34,11 +35,17 @@ from .hashgrid import (  # noqa: F401
 )
 from .residual import (  # noqa: F401
     AdamWTensor,
+    HashGridAdamW,
     HashGridAdamWPlan,
+    HashGridLinearFunction,
+    HashGridResidualHead,
+    HashGridResidualHead8,
+    HashGridRmsNormFunction,
     RmsNormOutput,
     hashgrid_adamw_step,
     hashgrid_linear_backward,
     hashgrid_linear_forward,
     hashgrid_rms_norm_backward,
     hashgrid_rms_norm_forward,
+    quantize_rows,
 )

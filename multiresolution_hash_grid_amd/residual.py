@@ -432,3 +432,175 @@ class HashGridAdamWPlan:
 def hashgrid_adamw_step(tensors, **kw) -> None:
     """One AdamW update of a list of ``AdamWTensor``: ``HashGridAdamWPlan(tensors).step(**kw)``."""
     HashGridAdamWPlan(tensors).step(**kw)
+
+
+class HashGridLinearFunction(torch.autograd.Function):
+    """Autograd of hashgrid_linear_forward: x in a 16-bit type, the weight an fp32 master that the products read
+    rounded to it, bias fp32, residual in the output's type.  Gradients of the masters are fp32."""
+
+    @staticmethod
+    def forward(ctx, x, weight, bias, act="none", residual=None, out_dtype=None):
+        w = weight.to(x.dtype)
+        train = any(ctx.needs_input_grad)
+        # ReLU's slope can be read from y itself where no residual was added
+        keep = train and act != "none" and not (act == "relu" and residual is None and out_dtype in (None, x.dtype))
+        out = hashgrid_linear_forward(x, w, bias, act=act, residual=residual, out_dtype=out_dtype, save_pre=keep)
+        y, pre = out if keep else (out, out if train and act == "relu" else None)
+        ctx.act = act
+        ctx.save_for_backward(x, w, pre)
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, w, pre = ctx.saved_tensors
+        need = ctx.needs_input_grad + (False,) * (6 - len(ctx.needs_input_grad))  # arguments may have been left out
+        dy = dy.contiguous()
+        dx, dw, db = hashgrid_linear_backward(dy, x, w, act=ctx.act, pre=pre, need_dx=need[0], need_dw=need[1],
+                                              need_db=need[2])
+        return dx, dw, db, None, dy if need[4] else None, None
+
+
+class HashGridRmsNormFunction(torch.autograd.Function):
+    """Autograd of hashgrid_rms_norm_forward: returns y, or (y, s) with a residual, s = x + residual in x's type."""
+
+    @staticmethod
+    def forward(ctx, x, weight, residual=None, eps=1e-6):
+        out = hashgrid_rms_norm_forward(x, weight, residual=residual, eps=eps, save_sum=residual is not None, save_rstd=True)
+        s = x if residual is None else out.sum
+        ctx.save_for_backward(s, weight, out.rstd)
+        return out.y if residual is None else (out.y, out.sum)
+
+    @staticmethod
+    def backward(ctx, dy, ds=None):
+        s, weight, rstd = ctx.saved_tensors
+        need = ctx.needs_input_grad + (False,) * (4 - len(ctx.needs_input_grad))
+        dx, dw = hashgrid_rms_norm_backward(dy.contiguous(), s, weight, rstd, ds=None if ds is None else ds.contiguous(),
+                                            need_dw=need[1])
+        return dx, dw, dx if need[2] else None, None
+
+
+class HashGridResidualHead(torch.nn.Module):
+    """A residual head of any width on the encoding: ``forward(features [n, in_features]) -> [n, out_features]`` fp32.
+
+        h = stem(features)
+        per block: h = h + W2 act(W1 norm(h) + b1) + b2
+        y = W norm(h + stem's h) + b
+
+    Weights, biases and norm weights are fp32 masters; activations and the weights' copies that the matrix cores read
+    are ``dtype`` (bfloat16 or float16).  ``quantized()`` is the same head for inference with 8-bit operands behind
+    the blocks' norms."""
+
+    def __init__(self, in_features=32, width=256, blocks=2, out_features=4, act="silu", dtype=torch.bfloat16,
+                 eps=1e-6, device="cuda"):
+        super().__init__()
+        if dtype not in _HALF:
+            raise ValueError("dtype must be torch.float16 or torch.bfloat16")
+        _act(act)
+        self.act, self.dtype, self.eps, self.blocks = act, dtype, eps, blocks
+
+        def layer(name, fan_in, fan_out):
+            w = torch.empty((fan_out, fan_in), device=device)
+            torch.nn.init.xavier_uniform_(w)
+            b = torch.empty(fan_out, device=device).uniform_(-fan_in ** -0.5, fan_in ** -0.5)
+            self.register_parameter(f"{name}_w", torch.nn.Parameter(w))
+            self.register_parameter(f"{name}_b", torch.nn.Parameter(b))
+
+        layer("stem", in_features, width)
+        for i in range(blocks):
+            self.register_parameter(f"norm{i}", torch.nn.Parameter(torch.ones(width, device=device)))
+            layer(f"up{i}", width, width)
+            layer(f"down{i}", width, width)
+        self.register_parameter("norm_out", torch.nn.Parameter(torch.ones(width, device=device)))
+        layer("out", width, out_features)
+
+    def _layer(self, name):
+        return getattr(self, f"{name}_w"), getattr(self, f"{name}_b")
+
+    def forward(self, features: torch.Tensor) -> torch.Tensor:
+        linear, norm = HashGridLinearFunction.apply, HashGridRmsNormFunction.apply
+        h = stem = linear(features.to(self.dtype), *self._layer("stem"))
+        for i in range(self.blocks):
+            u = linear(norm(h, getattr(self, f"norm{i}"), None, self.eps), *self._layer(f"up{i}"), self.act)
+            h = linear(u, *self._layer(f"down{i}"), "none", h)
+        y, _ = norm(h, self.norm_out, stem, self.eps)
+        return linear(y, *self._layer("out"), "none", None, torch.float32)
+
+    def quantized(self) -> "HashGridResidualHead8":
+        return HashGridResidualHead8(self)
+
+
+def quantize_rows(w: torch.Tensor) -> tuple:
+    """(e4m3 values, scales) of a matrix, one scale a row: the largest magnitude of a row at 448."""
+    scale = w.detach().float().abs().amax(1) / 448.0
+    inv = torch.where(scale > 0, 1.0 / scale, torch.zeros_like(scale))
+    return (w.detach().float() * inv[:, None]).clamp(-448.0, 448.0).to(F8), scale
+
+
+class HashGridResidualHead8:
+    """A HashGridResidualHead for inference: the blocks' first products read 8-bit rows with scales, which the norm
+    writes, and 8-bit weights; the residual stream, the other products and the outputs stay in the head's 16-bit type."""
+
+    def __init__(self, head: HashGridResidualHead):
+        self.act, self.dtype, self.eps, self.blocks = head.act, head.dtype, head.eps, head.blocks
+        grab = lambda t: t.detach().clone()  # noqa: E731
+        self.stem = head.stem_w.detach().to(self.dtype), grab(head.stem_b)
+        self.layers = [(grab(getattr(head, f"norm{i}")), *quantize_rows(getattr(head, f"up{i}_w")), grab(getattr(head, f"up{i}_b")),
+                        getattr(head, f"down{i}_w").detach().to(self.dtype), grab(getattr(head, f"down{i}_b")))
+                       for i in range(self.blocks)]
+        self.out = grab(head.norm_out), head.out_w.detach().to(self.dtype), grab(head.out_b)
+
+    def __call__(self, features: torch.Tensor) -> torch.Tensor:
+        h = stem = hashgrid_linear_forward(features.to(self.dtype), *self.stem)
+        for norm, w8, ws, b1, w2, b2 in self.layers:
+            n8, scale, _, _ = hashgrid_rms_norm_forward(h, norm, eps=self.eps, out_dtype=F8)
+            u = hashgrid_linear_forward(n8, w8, b1, act=self.act, x_scale=scale, weight_scale=ws, out_dtype=self.dtype)
+            h = hashgrid_linear_forward(u, w2, b2, residual=h)
+        norm, w, b = self.out
+        return hashgrid_linear_forward(hashgrid_rms_norm_forward(h, norm, residual=stem, eps=self.eps).y, w, b,
+                                       out_dtype=torch.float32)
+
+
+class HashGridAdamW(torch.optim.Optimizer):
+    """AdamW over the tables and a head's weights, all tensors in one call (hashgrid_adamw_step).  Groups have their own
+    ``lr`` and ``weight_decay`` (the pages: no decay on the tables, a rate 5 to 10 times the head's); ``state_bits`` 8
+    keeps the moments in 8 bits.  ``grad_scale`` of ``step`` is the float32 GPU scalar gradients are multiplied by."""
+
+    def __init__(self, params, lr=1e-3, betas=(0.9, 0.99), eps=1e-15, weight_decay=0.0, state_bits=32, seed=0,
+                 zero_grad_in_step=False):
+        if state_bits not in (8, 32):
+            raise ValueError("state_bits must be 8 or 32")
+        super().__init__(params, dict(lr=lr, betas=betas, eps=eps, weight_decay=weight_decay, state_bits=state_bits))
+        self.seed, self.zero_grad_in_step = seed, zero_grad_in_step
+
+    @torch.no_grad()
+    def step(self, closure=None, grad_scale: torch.Tensor | None = None):
+        loss = None
+        if closure is not None:
+            with torch.enable_grad():
+                loss = closure()
+        calls: dict = {}
+        for group in self.param_groups:
+            for p in group["params"]:
+                if p.grad is None:
+                    continue
+                st = self.state[p]
+                if not st:
+                    st["step"] = 0
+                    st.update(AdamWTensor.states(p, group["state_bits"]))
+                st["step"] += 1
+                calls.setdefault((tuple(group["betas"]), group["eps"], st["step"]), []).append(
+                    AdamWTensor(p, p.grad, st["m"], st["v"], st.get("m_exp"), st.get("v_exp"), None, group["lr"],
+                                group["weight_decay"]))
+        for ((b1, b2), eps, t), tensors in calls.items():
+            HashGridAdamWPlan(tensors).step(step=t, beta1=b1, beta2=b2, eps=eps, seed=self.seed + t, grad_scale=grad_scale,
+                                            zero_grad=self.zero_grad_in_step)
+        return loss
+
+    def load_state_dict(self, state_dict):
+        """Restores 8-bit moments in their own types, which Optimizer.load_state_dict turns into the parameter's."""
+        super().load_state_dict(state_dict)
+        for st in self.state.values():
+            if "m_exp" in st:
+                st["m"] = st["m"].to(F8)
+                for k in ("v", "m_exp", "v_exp"):
+                    st[k] = st[k].to(torch.uint8)
