@@ -2,6 +2,8 @@
 // include this instantiate one operand type each, so that they build at once.
 #pragma once
 
+#include <math.h>
+
 #include "linear_common.h"
 
 namespace hg {
@@ -279,12 +281,21 @@ constexpr int kLdsBytes = 160 * 1024;
 template <typename T, int KU>
 constexpr int kWeightBytes = KU * 64 * (sizeof(T) == 1 ? 2 : 1) + 8;
 
+// With few rows a workgroup mostly reads weights: a CU fetches some 14 KB/us that
+// its own L1 misses, so 128 KB of weights take 9 us.  Slices of W cost their rows'
+// x again: bytes W / s + s x / CUs are least at s = sqrt(n CUs / m).
+inline int few_rows_slices(const FwdArgs &a) {
+    const int most = (int)div_up(a.n, 64), want = (int)sqrt((double)a.n * kCus / (double)a.m);
+    return want < most ? want : most;
+}
+
 template <typename T, typename Y, int KU, int RF, int FR, int GS, int kCut, bool kStage = false>
 hipError_t stream_launch(const FwdArgs &a, hipStream_t stream) {
     const auto kernel = linear_stream_kernel<T, Y, KU, RF, FR, GS, kCut, kStage>;
     constexpr int per = kWeightBytes<T, KU>, set = 16 * FR;  // LDS bytes of an output; outputs of a set
     const int fit = kLdsBytes / per / set * set;
     int slices = (int)div_up(a.n, fit);
+    if (FR == 4 && few_rows_slices(a) > slices) slices = few_rows_slices(a);
     const int slice_n = (int)div_up(div_up(a.n, slices), set) * set;
     slices = (int)div_up(a.n, slice_n);
     const int bytes = slice_n * per + (kStage ? 16 * kStageBytes : 0);
@@ -463,7 +474,6 @@ hipError_t run_block(const FwdArgs &a, hipStream_t stream) {
     return hipGetLastError();
 }
 
-// hipErrorNotSupported: not a case of this kernel.
 template <typename T, typename Y>
 hipError_t run_stream(const FwdArgs &a, hipStream_t stream) {
     if (a.k < kPiece<T>) return stream_set<T, Y, 1, 2>(a, stream);
@@ -489,15 +499,21 @@ hipError_t run_stream(const FwdArgs &a, hipStream_t stream) {
         HG_STREAM(16)
 #undef HG_STREAM
     }
-    return hipErrorNotSupported;
+    return hipErrorInvalidValue;
 }
 
 template <typename T, typename Y>
 hipError_t linear_run(const FwdArgs &a, hipStream_t stream) {
-    if (a.m >= 2048) {
-        const hipError_t e = run_stream<T, Y>(a, stream);
-        return e != hipErrorNotSupported ? e : run_block<T, Y>(a, stream);
-    }
+    // The tile kernel reads W for every 16 rows (30 us per 10^9 multiply-adds, at
+    // 64 x 64 to 1024 x 1024 alike); the others first bring W in: the stream kernel a
+    // slice of it (14 KB/us and CU, and x again for every further slice), the block kernel a step
+    // of 128 bytes of the contraction in 2.2 us.  At 256 x 256 they meet near 2^11
+    // rows (6 us), at 64 x 64 near 2^13 (3.4 us), at 1024 x 1024 near 1200 (36 us).
+    const double tile_us = 3e-8 * (double)a.m * a.n * a.k, row = (double)a.k * sizeof(T);
+    const bool stream_fits = div_up(a.k, kStretch<T>) <= 16;
+    const double slices = few_rows_slices(a) > 1 ? few_rows_slices(a) : 1;
+    const double other_us = stream_fits ? 0.5 + (a.n * row / slices + a.m * row * (slices - 1) / kCus) / 14500. : 2.2 * div_up((int64_t)row, 128);
+    if (tile_us > other_us) return stream_fits ? run_stream<T, Y>(a, stream) : run_block<T, Y>(a, stream);
     FwdArgs part = a;
     const int64_t most = 65535LL * 16;  // rows a grid's second dimension reaches
     for (int64_t m = 0; m < a.m; m += most) {
