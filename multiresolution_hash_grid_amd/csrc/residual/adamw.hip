@@ -54,8 +54,9 @@ static_assert(sizeof(Args) <= 4096, "kernel arguments");
 
 constexpr int kThreads = 256;
 constexpr int kPer = 4;                        // consecutive values of a thread: a wave has one 256-value block
-constexpr int kRounds = 2;                     // blocks a wave takes
-constexpr int kChunk = kThreads * kPer * kRounds;
+// One block a wave: 2^24 values of fp32 state and 2^25 of 8-bit state take 106 and 127 us;
+// with 2, 4, 8 blocks 112, 117, 123 and 135, 144, 154 (a wave's stores hold back its next loads).
+constexpr int kChunk = kThreads * kPer;
 
 // A 32-bit finalizer of multiplications and shifts (MurmurHash3's, public domain).
 __host__ __device__ __forceinline__ uint32_t mix(uint32_t h) {
@@ -217,17 +218,13 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(const Args a) {
         else hi = mid - 1;
     }
     const Tensor &t = a.t[lo];
-    const int64_t base = (int64_t)((int)blockIdx.x - t.first) * kChunk + threadIdx.x * kPer;
-#pragma unroll
-    for (int r = 0; r < kRounds; ++r) {
-        const int64_t i = base + (int64_t)r * kThreads * kPer;
-        const int64_t left = t.count - i;
-        // Whole waves decide together: a block is a wave's 256 values.
-        const int64_t wave_left = t.count - (i - (threadIdx.x & 63) * kPer);
-        if (wave_left <= 0) return;
-        if (wave_left >= 256 && t.vec) update4<kBits, true>(t, a, i, 4, scale);
-        else update4<kBits, false>(t, a, i, left > 4 ? 4 : left < 0 ? 0 : (int)left, scale);
-    }
+    const int64_t i = (int64_t)((int)blockIdx.x - t.first) * kChunk + threadIdx.x * kPer;
+    const int64_t left = t.count - i;
+    // Whole waves decide together: a block is a wave's 256 values.
+    const int64_t wave_left = t.count - (i - (threadIdx.x & 63) * kPer);
+    if (wave_left <= 0) return;
+    if (wave_left >= 256 && t.vec) update4<kBits, true>(t, a, i, 4, scale);
+    else update4<kBits, false>(t, a, i, left > 4 ? 4 : left < 0 ? 0 : (int)left, scale);
 }
 
 }  // namespace

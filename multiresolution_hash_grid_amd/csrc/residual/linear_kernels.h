@@ -505,14 +505,15 @@ hipError_t run_stream(const FwdArgs &a, hipStream_t stream) {
 template <typename T, typename Y>
 hipError_t linear_run(const FwdArgs &a, hipStream_t stream) {
     // The tile kernel reads W for every 16 rows (30 us per 10^9 multiply-adds, at
-    // 64 x 64 to 1024 x 1024 alike); the others first bring W in: the stream kernel a
+    // 64 x 64 to 1024 x 1024 alike, whole 16 x 32 tiles of W); the others first bring W in: the stream kernel a
     // slice of it (14 KB/us and CU, and x again for every further slice), the block kernel a step
     // of 128 bytes of the contraction in 2.2 us.  At 256 x 256 they meet near 2^11
     // rows (6 us), at 64 x 64 near 2^13 (3.4 us), at 1024 x 1024 near 1200 (36 us).
-    const double tile_us = 3e-8 * (double)a.m * a.n * a.k, row = (double)a.k * sizeof(T);
+    const double tile_us = 3e-8 * (double)a.m * (16 * div_up(a.n, 16)) * (32 * div_up(a.k, 32)), row = (double)a.k * sizeof(T);
     const bool stream_fits = div_up(a.k, kStretch<T>) <= 16;
     const double slices = few_rows_slices(a) > 1 ? few_rows_slices(a) : 1;
-    const double other_us = stream_fits ? 0.5 + (a.n * row / slices + a.m * row * (slices - 1) / kCus) / 14500. : 2.2 * div_up((int64_t)row, 128);
+    const double other_us = stream_fits ? 0.5 + (a.n * row / slices + a.m * row * (slices - 1) / kCus) / 14500.
+                                        : 2.2 * div_up((int64_t)row, 128);
     if (tile_us > other_us) return stream_fits ? run_stream<T, Y>(a, stream) : run_block<T, Y>(a, stream);
     FwdArgs part = a;
     const int64_t most = 65535LL * 16;  // rows a grid's second dimension reaches
