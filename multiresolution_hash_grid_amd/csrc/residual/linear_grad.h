@@ -8,7 +8,7 @@ namespace res {
 
 struct GradArgs {
     int64_t m, dys, ps, xs, ws, dxs, dws;
-    int k, n, act, accumulate;
+    int k, n, act, accumulate, dw_f32;
     const void *dy, *pre, *x, *w;
     void *dx, *dw;
     float *db;
@@ -27,8 +27,8 @@ struct GradPlan {
     size_t dz_at, wt_at, bytes;
 };
 
-hipError_t linear_grad_f16(const GradArgs &a, bool dy_f32, bool dw_f32, const GradPlan &p, char *workspace, hipStream_t stream);
-hipError_t linear_grad_bf16(const GradArgs &a, bool dy_f32, bool dw_f32, const GradPlan &p, char *workspace, hipStream_t stream);
+hipError_t linear_grad_f16(const GradArgs &a, bool dy_f32, const GradPlan &p, char *workspace, hipStream_t stream);
+hipError_t linear_grad_bf16(const GradArgs &a, bool dy_f32, const GradPlan &p, char *workspace, hipStream_t stream);
 
 }  // namespace res
 }  // namespace hg

@@ -155,6 +155,26 @@ __device__ __forceinline__ void stage_wt(const GradArgs &a, u32x4 *wt) {
     }
 }
 
+// Four values of dW, slots k .. k + 3 of slot n, rounded once.
+template <typename T>
+__device__ __forceinline__ void put_dw(const GradArgs &a, int n, int k, f32x4 t) {
+    const int row = column_of(n, a.n);
+    if (row < 0) return;
+    auto into = [&](auto *w) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int c = column_of(k + j, a.k);
+            if (c >= 0) w[c] = (std::remove_reference_t<decltype(*w)>)(a.accumulate ? (float)w[c] + t[j] : t[j]);
+        }
+    };
+    if (a.dw_f32) into((float *)a.dw + (int64_t)row * a.dws);
+    else into((T *)a.dw + (int64_t)row * a.dws);
+}
+__device__ __forceinline__ void put_db(const GradArgs &a, int n, float t) {
+    const int c = column_of(n, a.n);
+    if (c >= 0) a.db[c] = a.accumulate ? a.db[c] + t : t;
+}
+
 // The whole backward of up to NT outputs by KT inputs in one pass over the rows:
 // dy, z and x are read once, dz lives in LDS only.  A workgroup a CU walks steps
 // of R rows.  In a step each thread turns the pieces it loaded a step ahead into
@@ -162,7 +182,8 @@ __device__ __forceinline__ void stage_wt(const GradArgs &a, u32x4 *wt) {
 // adds the step's product to its part of dW, which stays in registers to the
 // end (4 x 2 waves over NT x KT), and makes one 32 x 32 block of dx from dz and
 // the W^T fragments held in LDS.  dW and db leave as one partial per workgroup,
-// joined in a fixed order by grad_join_kernel.
+// joined in a fixed order by grad_join_kernel; a workgroup alone with its tile
+// (few rows) writes them itself.
 // Wider layers: tiles of NT x KT (blockIdx.y over outputs, .z over inputs)
 // make dW and db alone, and the first column of tiles writes dz for dx's sake.
 template <typename T, typename D, int NT, int KT, bool kDx>
@@ -329,13 +350,17 @@ __global__ __launch_bounds__(kGradThreads) void grad_kernel(const GradArgs a, fl
 
     // Partials: dW as fragments, [tile][workgroup][NT x KT], then db, [output tile][workgroup][NT].
     const int tile = blockIdx.y * gridDim.z + blockIdx.z;
+    const bool alone = gridDim.x == 1;
     if (a.dw) {
         float *p = part + ((int64_t)tile * gridDim.x + blockIdx.x) * (NT * KT);
 #pragma unroll
         for (int i = 0; i < FN; ++i)
 #pragma unroll
-            for (int j = 0; j < FK; ++j)
-                *(f32x4 *)(p + ((wn * FN + i) * (KT / 16) + wk * FK + j) * 256 + lane * 4) = acc[i][j];
+            for (int j = 0; j < FK; ++j) {
+                const int fn = wn * FN + i, fk = wk * FK + j;
+                if (alone) put_dw<T>(a, n0 + fn * 16 + (lane & 15), k0 + fk * 16 + (lane >> 4) * 4, acc[i][j]);
+                else *(f32x4 *)(p + (fn * (KT / 16) + fk) * 256 + lane * 4) = acc[i][j];
+            }
     }
     if (a.db && blockIdx.z == 0) {
         float *const sums = (float *)lds;  // [512 / PN][NT]
@@ -348,7 +373,8 @@ __global__ __launch_bounds__(kGradThreads) void grad_kernel(const GradArgs a, fl
         for (int n = threadIdx.x; n < NT; n += kGradThreads) {
             float t = 0.f;
             for (int r = 0; r < kGradThreads / PN; ++r) t += sums[r * NT + n];
-            p[n] = t;
+            if (alone) put_db(a, n0 + n, t);
+            else p[n] = t;
         }
     }
 }
@@ -356,7 +382,7 @@ __global__ __launch_bounds__(kGradThreads) void grad_kernel(const GradArgs a, fl
 // dW = (dW +) the partials' sum, rounded once; db alike.  A workgroup takes 16
 // groups of four values; 32 threads share the partials of each, and their sums
 // are added in order, eight and then four.
-template <typename G>
+template <typename T>
 __global__ __launch_bounds__(512) void grad_join_kernel(const float *part, int parts, int nt, int kt, int ny, int nz, GradArgs a) {
     __shared__ f32x4 lds[32][16];
     const int slot = threadIdx.x & 15, share = threadIdx.x >> 4;
@@ -383,19 +409,9 @@ __global__ __launch_bounds__(512) void grad_join_kernel(const float *part, int p
     for (int i = 1; i < 4; ++i) t += lds[i][slot];
     if (q < quads) {
         const int tile = (int)(local / per), e = (int)(local % per), frag = e / 64, l = e % 64;
-        const int n = column_of(tile / nz * nt + frag / (kt / 16) * 16 + (l & 15), a.n);
-        const int k0 = tile % nz * kt + frag % (kt / 16) * 16 + (l >> 4) * 4;
-        if (n < 0) return;
-        G *w = (G *)a.dw + (int64_t)n * a.dws;
-        for (int j = 0; j < 4; ++j) {
-            const int k = column_of(k0 + j, a.k);
-            if (k >= 0) w[k] = (G)(a.accumulate ? (float)w[k] + t[j] : t[j]);
-        }
+        put_dw<T>(a, tile / nz * nt + frag / (kt / 16) * 16 + (l & 15), tile % nz * kt + frag % (kt / 16) * 16 + (l >> 4) * 4, t);
     } else {
-        for (int j = 0; j < 4; ++j) {
-            const int n = column_of((int)local * 4 + j, a.n);
-            if (n >= 0) a.db[n] = a.accumulate ? a.db[n] + t[j] : t[j];
-        }
+        for (int j = 0; j < 4; ++j) put_db(a, (int)local * 4 + j, t[j]);
     }
 }
 
@@ -445,7 +461,7 @@ hipError_t grad_pick(const GradArgs &a, const GradPlan &p, float *part, T *dz, h
 }
 
 template <typename T, typename D>
-hipError_t grad_run(const GradArgs &a, bool dw_f32, const GradPlan &p, char *workspace, hipStream_t stream,
+hipError_t grad_run(const GradArgs &a, const GradPlan &p, char *workspace, hipStream_t stream,
                     hipError_t (*forward)(const FwdArgs &, int, hipStream_t), int dtype) {
     float *const part = (float *)workspace;
     T *const dz = (T *)(workspace + p.dz_at), *const wt = (T *)(workspace + p.wt_at);
@@ -455,11 +471,10 @@ hipError_t grad_run(const GradArgs &a, bool dw_f32, const GradPlan &p, char *wor
                     : grad_pick<T, D, false>(a, p, part, a.dx ? dz : nullptr, stream);
         if (e != hipSuccess) return e;
     }
-    if (a.dw || a.db) {
+    if ((a.dw || a.db) && !(a.m > 0 && p.parts == 1)) {
         const int64_t quads = (a.dw ? (int64_t)p.ny * p.nz * p.nt * p.kt : 0) / 4 + (a.db ? p.ny * p.nt / 4 : 0);
         const int parts = a.m > 0 ? p.parts : 0;
-        const auto join = dw_f32 ? grad_join_kernel<float> : grad_join_kernel<T>;
-        join<<<dim3((unsigned)div_up(quads, 16)), 512, 0, stream>>>(part, parts, p.nt, p.kt, p.ny, p.nz, a);
+        grad_join_kernel<T><<<dim3((unsigned)div_up(quads, 16)), 512, 0, stream>>>(part, parts, p.nt, p.kt, p.ny, p.nz, a);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     if (a.dx && a.m > 0 && !p.fused) {
