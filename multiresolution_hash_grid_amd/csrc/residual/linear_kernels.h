@@ -333,6 +333,163 @@ hipError_t stream_set(const FwdArgs &a, hipStream_t stream) {
     return stream_launch<T, Y, KU, 1, 4, GS, kCut>(a, stream);
 }
 
+// Many rows, a contraction longer than a wave's registers hold, few outputs: W in
+// LDS and a wave's own row tiles as above, and the rows come in chunks of KC
+// fragments, the next chunk on its way while one is multiplied.  W's fragments are
+// padded with zeros to whole chunks, and the rows' with zeros too (what is past a
+// row need not be finite).
+constexpr int kChunkFragments = 4;
+constexpr int kLongSlices = 2;
+template <typename T, typename Y, int FR>
+__global__ __launch_bounds__(1024) void linear_long_kernel(const FwdArgs a, int slices, int units) {
+    extern __shared__ __attribute__((aligned(16))) char lds[];
+    constexpr int KC = kChunkFragments, kHalves = sizeof(T) == 1 ? 2 : 1;
+    constexpr int kPairs = FR == 1 ? 1 : FR / 2, kOut = FR == 1 ? 4 : 8;  // as in the stream kernel
+    u32x4 *const wl = (u32x4 *)lds;
+    const int chunks = (units + KC - 1) / KC, whole = chunks * KC;
+    float *const bias = (float *)(lds + (size_t)FR * whole * kHalves * 1024), *const wsc = bias + 16 * FR;
+    const int waves = blockDim.x >> 6;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, row16 = lane & 15, group = lane >> 4;
+    const int xcd = blockIdx.x & 7, in_xcd = blockIdx.x >> 3;
+    const int n0 = (in_xcd % slices) * 16 * FR;
+    const int walkers = (gridDim.x >> 3) / slices * 8, walker = in_xcd / slices * 8 + xcd;
+    const int nn = a.n - n0 < 16 * FR ? a.n - n0 : 16 * FR;
+
+    const Cut<T> last = cut_piece<T>((units - 1) * kStretch<T> + group * kPiece<T>, a.k);
+    auto piece = [&](const T *row, int u) {  // fragments past the row read the last one
+        return load_loose<u32x4>(row + (u < units - 1 ? u * kStretch<T> + group * kPiece<T> : last.at));
+    };
+    auto masked = [&](u32x4 v, int u) {
+        return u < units - 1 ? v : u == units - 1 ? v & last.mask : u32x4{0, 0, 0, 0};
+    };
+    for (int b = wave; b < FR * whole; b += waves) {
+        const int f = b / whole, u = b % whole;
+        const int n = FR == 1 ? row16 : (f >> 1) * 32 + (row16 >> 2) * 8 + (f & 1) * 4 + (row16 & 3);
+        const u32x4 v = masked(piece((const T *)a.w + (int64_t)(n0 + (n < nn ? n : nn - 1)) * a.ws, u), u);
+        if constexpr (sizeof(T) == 1) {
+            const Widened w = widen(v);
+            wl[(b * 2) * 64 + lane] = w.lo;
+            wl[(b * 2 + 1) * 64 + lane] = w.hi;
+        } else {
+            wl[b * 64 + lane] = v;
+        }
+    }
+    for (int n = threadIdx.x; n < 16 * FR; n += blockDim.x) {
+        bias[n] = a.bias && n < nn ? a.bias[n0 + n] : 0.f;
+        if constexpr (sizeof(T) == 1) wsc[n] = n < nn ? a.w_scale[n0 + n] : 0.f;
+    }
+    __syncthreads();
+
+    const int64_t tiles = (a.m + 15) / 16;
+    for (int64_t tile = (int64_t)wave * walkers + walker; tile < tiles; tile += (int64_t)waves * walkers) {
+        const int64_t m = tile * 16 + row16, mr = m < a.m ? m : a.m - 1;
+        const T *const row = (const T *)a.x + mr * a.xs;
+        const int n = group * kOut;  // this lane's outputs: kOut from n, and from n + 32
+        f32x4 acc[FR];
+#pragma unroll
+        for (int f = 0; f < FR; ++f) {
+            if constexpr (sizeof(T) == 1) acc[f] = f32x4{0.f, 0.f, 0.f, 0.f};
+            else acc[f] = *(const f32x4 *)(bias + n + (f >> 1) * 32 + (f & 1) * 4);
+        }
+        u32x4 even[KC], odd[KC];
+        auto load = [&](u32x4(&x)[KC], int c) {
+            if (c < chunks - 1) {
+                const T *const p = row + group * kPiece<T> + c * KC * kStretch<T>;
+#pragma unroll
+                for (int j = 0; j < KC; ++j) x[j] = load_loose<u32x4>(p + j * kStretch<T>);
+            } else {
+#pragma unroll
+                for (int j = 0; j < KC; ++j) x[j] = piece(row, c * KC + j);
+            }
+        };
+        auto multiply = [&](u32x4(&x)[KC], int c) {
+            if (c == chunks - 1)
+#pragma unroll
+                for (int j = 0; j < KC; ++j) x[j] = masked(x[j], c * KC + j);
+#pragma unroll
+            for (int j = 0; j < KC; ++j) {
+                Widened xw;
+                if constexpr (sizeof(T) == 1) xw = widen(x[j]);
+#pragma unroll
+                for (int f = 0; f < FR; ++f)
+#pragma unroll
+                    for (int h = 0; h < kHalves; ++h) {
+                        u32x4 v;
+                        if constexpr (sizeof(T) == 1) v = h ? xw.hi : xw.lo;
+                        else v = x[j];
+                        acc[f] = mma16<T>(wl[((f * whole + c * KC + j) * kHalves + h) * 64 + lane], v, acc[f]);
+                    }
+            }
+        };
+        load(even, 0);
+        for (int c = 0; c < chunks; c += 2) {
+            if (c + 1 < chunks) load(odd, c + 1);
+            multiply(even, c);
+            if (c + 1 >= chunks) break;
+            if (c + 2 < chunks) load(even, c + 2);
+            multiply(odd, c + 1);
+        }
+        float xsc = 1.f;
+        if constexpr (sizeof(T) == 1) xsc = a.x_scale[mr];
+#pragma unroll
+        for (int q = 0; q < kPairs; ++q) {
+            const int at = n + q * 32, left = nn - at;
+            float z[kOut];
+#pragma unroll
+            for (int j = 0; j < kOut; ++j) {
+                z[j] = acc[q * 2 + j / 4][j % 4];
+                if constexpr (sizeof(T) == 1) z[j] = fmaf(z[j] * xsc, wsc[at + j], bias[at + j]);
+            }
+            if constexpr (sizeof(T) == 2)
+                if (a.pre && m < a.m) put((T *)a.pre + m * a.ps + n0 + at, left, rounded<kOut, T>(z));
+            activate_all(z, a.act);
+            if (a.r) {
+                const Held<kOut, Y> res = hold<kOut>((const Y *)a.r + mr * a.rs + n0 + at, left);
+#pragma unroll
+                for (int j = 0; j < kOut; ++j) z[j] += (float)res.v[j];
+            }
+            if (m < a.m) put((Y *)a.y + m * a.ys + n0 + at, left, rounded<kOut, Y>(z));
+        }
+    }
+}
+
+// LDS of linear_long_kernel with fr fragments of outputs.
+template <typename T>
+int long_bytes(const FwdArgs &a, int fr) {
+    const int64_t chunks = div_up(div_up(a.k, kStretch<T>), kChunkFragments);
+    const int64_t bytes = chunks * kChunkFragments * fr * (sizeof(T) == 1 ? 2048 : 1024) + 16 * fr * 8;
+    return bytes > kLdsBytes ? 0 : (int)bytes;
+}
+template <typename T, typename Y, int FR>
+hipError_t long_launch(const FwdArgs &a, hipStream_t stream) {
+    const auto kernel = linear_long_kernel<T, Y, FR>;
+    const int bytes = long_bytes<T>(a, FR), slices = (int)div_up(a.n, 16 * FR);
+    if (bytes > 65536) {
+        const hipError_t e = hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e != hipSuccess) return e;
+    }
+    const int64_t tiles = div_up(a.m, 16);
+    int64_t walkers = kCus / slices;
+    if (walkers > tiles) walkers = tiles;
+    walkers = div_up(walkers, 8) * 8;
+    kernel<<<dim3((unsigned)(walkers * slices)), 1024, bytes, stream>>>(a, slices, (int)div_up(a.k, kStretch<T>));
+    return hipGetLastError();
+}
+// The fragments of outputs a workgroup of linear_long_kernel takes; 0: not its case.
+template <typename T>
+int long_fragments(const FwdArgs &a) {
+    const int fr = a.n <= 16 ? 1 : a.n <= 32 ? 2 : 4;
+    return div_up(a.n, 16 * fr) <= kLongSlices && long_bytes<T>(a, fr) ? fr : 0;
+}
+template <typename T, typename Y>
+hipError_t run_long(const FwdArgs &a, hipStream_t stream) {
+    switch (long_fragments<T>(a)) {
+        case 1: return long_launch<T, Y, 1>(a, stream);
+        case 2: return long_launch<T, Y, 2>(a, stream);
+        default: return long_launch<T, Y, 4>(a, stream);
+    }
+}
+
 // Many rows, a weight too large to stay in LDS.  A workgroup makes a block of 128
 // rows by 256 outputs, its eight waves 64 x 64 each, over steps of 128 bytes of
 // the contraction: the next step's pieces of x and W are on their way into
@@ -521,9 +678,12 @@ hipError_t linear_run(const FwdArgs &a, hipStream_t stream) {
     const double row = (double)a.k * sizeof(T);
     const bool stream_fits = div_up(a.k, kStretch<T>) <= 16;
     const double slices = few_rows_slices(a) > 1 ? few_rows_slices(a) : 1;
+    const bool long_fits = !stream_fits && long_fragments<T>(a);
     const double other_us = stream_fits ? 0.5 + (a.n * row / slices + a.m * row * (slices - 1) / kCus) / 14500.
+                            : long_fits ? 0.5 + (a.n < 64 ? a.n : 64) * row / 14500.
                                         : 2.2 * div_up((int64_t)row, 128);
-    if (tile_us > other_us) return stream_fits ? run_stream<T, Y>(a, stream) : run_block<T, Y>(a, stream);
+    if (tile_us > other_us)
+        return stream_fits ? run_stream<T, Y>(a, stream) : long_fits ? run_long<T, Y>(a, stream) : run_block<T, Y>(a, stream);
     FwdArgs part = a;
     const int64_t most = 65535LL * 16;  // rows a grid's second dimension reaches
     for (int64_t m = 0; m < a.m; m += most) {

@@ -109,6 +109,32 @@ def test_no_rows():
     assert (kept == 1).all()
 
 
+@pytest.mark.parametrize("m,k,n", [(4000, 513, 3), (5001, 640, 16), (3000, 1027, 32), (2500, 1000, 61), (2049, 900, 128), (1500, 5100, 9),
+                                   (1037, 1300, 64), (2000, 2040, 25)])
+@pytest.mark.parametrize("dtype", [F16, BF16, F8])
+def test_long_rows_to_few_outputs(m, k, n, dtype):
+    # Contractions longer than a wave's registers hold, whole fragments and cut ones, between columns of NaN.
+    g = gen(m, k, n, 9)
+    out = F32 if n % 2 else (BF16 if dtype == F8 else dtype)
+
+    def between(rows, scale):
+        buf = torch.full((rows, k + 3), float("nan")).to(dtype)
+        buf[:, 2:-1] = (torch.randn(rows, k, generator=g) * scale).to(dtype)
+        return buf.to(DEV)[:, 2:-1]
+
+    x, w = between(m, 1.0), between(n, 20.0 if dtype == F8 else k ** -0.5)
+    xs, ws = ((torch.rand(m, generator=g) * 0.1).to(DEV), (torch.rand(n, generator=g) * k ** -0.5).to(DEV)) if dtype == F8 else (None, None)
+    b, r = torch.randn(n, generator=g).to(DEV), wide(g, m, n, out, 3)
+    for kind, res in (("silu", r), ("none", None)):
+        got = hg.hashgrid_linear_forward(x, w, b, act=kind, residual=res, x_scale=xs, weight_scale=ws, out_dtype=out,
+                                         save_pre=dtype != F8)
+        y, z = got if dtype != F8 else (got, None)
+        wy, wz, ey, ez = R.linear(x, w, b, kind, res, xs, ws, out)
+        R.within(y, wy, ey)
+        if z is not None:
+            R.within(z, wz, R.rounded(wz, ez, dtype))
+
+
 @pytest.mark.parametrize("dtype", [F16, BF16, F8])
 @pytest.mark.parametrize("m,k,n", [(40, 35, 20), (700, 64, 40), (6000, 96, 64)])
 def test_bytes_around_the_rows_are_not_touched_or_used(dtype, m, k, n):
