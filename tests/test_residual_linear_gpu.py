@@ -98,6 +98,23 @@ def test_backward_accumulates():
         assert torch.equal(dw, (old.float() + dw0).to(wd)) and torch.equal(db, ob + db0)
 
 
+@pytest.mark.parametrize("m", [1, 20, 32])
+@pytest.mark.parametrize("k,n", [(40, 24), (5, 300), (300, 3), (256, 200)])
+def test_backward_of_few_rows_accumulates(m, k, n):
+    # One workgroup a tile: dW and db are added to where they lie, in a matrix with a stride of its own.
+    g = gen(m, k, n, 12)
+    for dtype, wd in ((F16, F32), (BF16, BF16)):
+        x, w, dy = wide(g, m, k, dtype, 3), wide(g, n, k, dtype, 0), wide(g, m, n, dtype, 3)
+        buf = torch.randn(n, k + 5, generator=g).to(wd).to(DEV)
+        old, ob = buf.clone(), torch.randn(n, generator=g).to(DEV)
+        dx0, dw0, db0 = hg.hashgrid_linear_backward(dy, x, w, weight_dtype=F32)
+        dw, db = buf[:, 2:2 + k], ob.clone()
+        dx, _, _ = hg.hashgrid_linear_backward(dy, x, w, dw=dw, db=db, accumulate=True)
+        assert torch.equal(dx, dx0)
+        assert torch.equal(dw, (old[:, 2:2 + k].float() + dw0).to(wd)) and torch.equal(db, ob + db0)
+        assert torch.equal(buf[:, :2], old[:, :2]) and torch.equal(buf[:, 2 + k:], old[:, 2 + k:])
+
+
 def test_no_rows():
     x, w = torch.empty(0, 32, dtype=F16, device=DEV), torch.ones(8, 32, dtype=F16, device=DEV)
     assert hg.hashgrid_linear_forward(x, w).shape == (0, 8)
