@@ -105,7 +105,9 @@ __device__ __forceinline__ void stage_store(V *y, int64_t stride, int64_t m1, in
 // a buffer of the wave's own, pieces permuted against bank conflicts, and stored
 // 1 KB at a time in memory order (2^18 x 32 x 256 with z kept: 74 -> 60 us).
 // Slices of W are workgroups next to each other on one XCD that walk the same
-// rows, so x comes from HBM once.
+// rows, so x comes from HBM once.  A weight of more slices than an XCD's share of
+// the workgroups has fewer than 8 walkers a slice (1, 2 or 4): each keeps to its
+// XCDs, and the slices go around all of them.
 // Bound by memory, and at 8 bits by what a wave does per output (widening, GELU,
 // residual) between its loads.  2^20 x 256 x 256 bf16 with SiLU and residual: 300 us,
 // 5.4 TB/s; 2^18 x 32 x 256 f16 with z kept: 60 us, 4.8 TB/s; 10^5 x 256 x 4: 10.5 us;
@@ -122,9 +124,9 @@ __global__ __launch_bounds__(RF == 1 ? 1024 : 512) void linear_stream_kernel(con
     const int waves = blockDim.x >> 6;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, row16 = lane & 15, group = lane >> 4;
     // workgroups b, b + 8, b + 16, ... share an XCD
-    const int xcd = blockIdx.x & 7, in_xcd = blockIdx.x >> 3;
-    const int n0 = (in_xcd % slices) * slice_n;
-    const int walkers = (gridDim.x >> 3) / slices * 8, walker = in_xcd / slices * 8 + xcd;
+    const int xcd = blockIdx.x & 7, in_xcd = blockIdx.x >> 3, walkers = gridDim.x / slices;
+    const int n0 = (walkers < 8 ? blockIdx.x / walkers : in_xcd % slices) * slice_n;
+    const int walker = walkers < 8 ? xcd & (walkers - 1) : in_xcd / slices * 8 + xcd;
     const int nn = a.n - n0 < slice_n ? a.n - n0 : slice_n;
     const int sets = (nn + 16 * FR - 1) / (16 * FR);
     float *const bias = (float *)(lds + (size_t)(slice_n / 16) * KU * kHalves * 1024), *const wsc = bias + slice_n;
@@ -315,7 +317,10 @@ hipError_t stream_launch(const FwdArgs &a, hipStream_t stream) {
     const int64_t tiles = div_up(a.m, RF * 16);
     int64_t walkers = kCus * groups / slices;  // workgroups that share the rows
     if (walkers > tiles) walkers = tiles;
-    walkers = div_up(walkers, 8) * 8;
+    // Whole rounds over the XCDs; below 8 a power of two, and at least one (more slices
+    // than workgroups are resident).  Always 8, each slice of W is brought in 8 times:
+    // 512 x 512 x 32768 f16 104 us, 37 so; 4096 x 512 x 50304 410 and 343.
+    walkers = walkers >= 8 ? div_up(walkers, 8) * 8 : walkers >= 4 ? 4 : walkers >= 2 ? 2 : 1;
     kernel<<<dim3((unsigned)(walkers * slices)), RF == 1 && groups == 1 ? 1024 : 512, bytes, stream>>>(a, slices, slice_n);
     return hipGetLastError();
 }
