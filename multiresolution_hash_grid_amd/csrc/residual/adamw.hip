@@ -59,6 +59,7 @@ constexpr int kPer = 4;                        // consecutive values of a thread
 // One block a wave: 2^24 values of fp32 state and 2^25 of 8-bit state take 106 and 127 us;
 // with 2, 4, 8 blocks 112, 117, 123 and 135, 144, 154 (a wave's stores hold back its next loads).
 constexpr int kChunk = kThreads * kPer;
+constexpr int64_t kMaxGroups = 1023 * kGridX;  // of a launch, in whole rows of the grid: their numbers are 32-bit
 
 // A 32-bit finalizer of multiplications and shifts (MurmurHash3's, public domain).
 __host__ __device__ __forceinline__ uint32_t mix(uint32_t h) {
@@ -212,15 +213,16 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(const Args a) {
         scale = *a.grad_scale;
         if (!(fabsf(scale) <= 3.402823466e38f)) return;  // not finite: the step does nothing
     }
+    const int block = (int)(blockIdx.y * kGridX + blockIdx.x);
     // The tensor of this workgroup: first[] is ascending.
     int lo = 0, hi = a.n - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (a.t[mid].first <= (int)blockIdx.x) lo = mid;
+        if (a.t[mid].first <= block) lo = mid;
         else hi = mid - 1;
     }
     const Tensor &t = a.t[lo];
-    const int64_t i = (int64_t)((int)blockIdx.x - t.first) * kChunk + threadIdx.x * kPer;
+    const int64_t i = (int64_t)(block - t.first) * kChunk + threadIdx.x * kPer;
     const int64_t left = t.count - i;
     // Whole waves decide together: a block is a wave's 256 values.
     const int64_t wave_left = t.count - (i - (threadIdx.x & 63) * kPer);
@@ -251,7 +253,7 @@ hipError_t launch_adamw(const hg_adamw &opt, const hg_adamw_tensor *tensors, int
                 const hg_adamw_tensor &s = tensors[at];
                 if (s.count == 0 || s.state_bits != bits) continue;
                 const int64_t more = div_up(s.count, kChunk);
-                if (groups + more > 0x7FFFFFFF) break;
+                if (groups + more > kMaxGroups) break;
                 Tensor &t = a.t[a.n++];
                 t.p = s.param, t.g = s.grad, t.m = s.m, t.v = s.v, t.copy = s.copy;
                 t.me = s.m_exp, t.ve = s.v_exp;
@@ -267,8 +269,8 @@ hipError_t launch_adamw(const hg_adamw &opt, const hg_adamw_tensor *tensors, int
                 groups += more;
             }
             if (a.n == 0) continue;
-            if (bits == 32) adamw_kernel<32><<<dim3((unsigned)groups), kThreads, 0, stream>>>(a);
-            else adamw_kernel<8><<<dim3((unsigned)groups), kThreads, 0, stream>>>(a);
+            if (bits == 32) adamw_kernel<32><<<grid_of(groups), kThreads, 0, stream>>>(a);
+            else adamw_kernel<8><<<grid_of(groups), kThreads, 0, stream>>>(a);
             const hipError_t e = hipGetLastError();
             if (e != hipSuccess) return e;
         }

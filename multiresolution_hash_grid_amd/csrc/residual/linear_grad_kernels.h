@@ -391,7 +391,7 @@ __global__ __launch_bounds__(512) void grad_join_kernel(const float *part, int p
     __shared__ f32x4 lds[32][16];
     const int slot = threadIdx.x & 15, share = threadIdx.x >> 4;
     const int64_t quads = a.dw ? (int64_t)ny * nz * nt * kt / 4 : 0, all = quads + (a.db ? ny * nt / 4 : 0);
-    const int64_t q = (int64_t)blockIdx.x * 16 + slot;
+    const int64_t q = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 16 + slot;
     const int64_t per = q < quads ? nt * kt / 4 : nt / 4;      // quads of a partial
     const int64_t local = q < quads ? q : q - quads;
     const float *p = part + (q < quads ? 0 : quads * 4 * parts) + (local / per * per * parts + local % per) * 4;
@@ -478,7 +478,7 @@ hipError_t grad_run(const GradArgs &a, const GradPlan &p, char *workspace, hipSt
     if ((a.dw || a.db) && !(a.m > 0 && p.parts == 1)) {
         const int64_t quads = (a.dw ? (int64_t)p.ny * p.nz * p.nt * p.kt : 0) / 4 + (a.db ? p.ny * p.nt / 4 : 0);
         const int parts = a.m > 0 ? p.parts : 0;
-        grad_join_kernel<T><<<dim3((unsigned)div_up(quads, 16)), 512, 0, stream>>>(part, parts, p.nt, p.kt, p.ny, p.nz, a);
+        grad_join_kernel<T><<<grid_of(div_up(quads, 16)), 512, 0, stream>>>(part, parts, p.nt, p.kt, p.ny, p.nz, a);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     if (a.dx && a.m > 0 && !p.fused) {

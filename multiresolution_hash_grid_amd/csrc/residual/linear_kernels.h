@@ -629,7 +629,7 @@ template <typename T, typename Y>
 hipError_t run_block(const FwdArgs &a, hipStream_t stream) {
     const int tiles_n = (int)div_up(a.n, kBlockN);
     FwdArgs part = a;
-    const int64_t most = ((int64_t)1 << 30) / tiles_n / kBlockM * kBlockM;  // rows of a launch
+    const int64_t most = ((int64_t)1 << 29) / tiles_n / kBlockM * kBlockM;  // rows of a launch: 2^31 threads at most
     for (int64_t m = 0; m < a.m; m += most) {
         part.m = a.m - m < most ? a.m - m : most;
         part.x = (const T *)a.x + m * a.xs;

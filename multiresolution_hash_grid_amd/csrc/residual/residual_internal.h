@@ -21,6 +21,15 @@ constexpr int kCus = 256;  // MI355X: 8 XCDs of 32 CUs
 
 inline int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// A grid of `groups` workgroups in two dimensions.  One dimension holds less than
+// 2^32 threads: a launch of more runs the remainder only, without an error.  The
+// kernel's index is blockIdx.y * gridDim.x + blockIdx.x, and some past the end exist.
+constexpr int64_t kGridX = (int64_t)1 << 21;  // times 1024 threads at most
+inline dim3 grid_of(int64_t groups) {
+    if (groups <= kGridX) return dim3((unsigned)groups);
+    return dim3((unsigned)kGridX, (unsigned)div_up(groups, kGridX));
+}
+
 hipError_t launch_linear_forward(const hg_linear &op, hipStream_t stream);
 size_t linear_backward_bytes(const hg_linear_grad &op);
 hipError_t launch_linear_backward(const hg_linear_grad &op, void *workspace, hipStream_t stream);
