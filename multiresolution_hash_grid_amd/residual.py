@@ -13,6 +13,7 @@ from dataclasses import dataclass
 from typing import NamedTuple
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from .hashgrid import (HG_ADAM_ZERO_GRAD, HG_F16, HG_F32, _check, _dev, _keep_for_stream, _stream, load_library)
 
@@ -436,7 +437,8 @@ def hashgrid_adamw_step(tensors, **kw) -> None:
 
 class HashGridLinearFunction(torch.autograd.Function):
     """Autograd of hashgrid_linear_forward: x in a 16-bit type, the weight an fp32 master that the products read
-    rounded to it, bias fp32, residual in the output's type.  Gradients of the masters are fp32."""
+    rounded to it, bias fp32, residual in the output's type.  Gradients of the masters are fp32.  The gradients cannot
+    be differentiated again: autograd raises."""
 
     @staticmethod
     def forward(ctx, x, weight, bias, act="none", residual=None, out_dtype=None):
@@ -451,6 +453,7 @@ class HashGridLinearFunction(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         x, w, pre = ctx.saved_tensors
         need = ctx.needs_input_grad + (False,) * (6 - len(ctx.needs_input_grad))  # arguments may have been left out
@@ -461,7 +464,8 @@ class HashGridLinearFunction(torch.autograd.Function):
 
 
 class HashGridRmsNormFunction(torch.autograd.Function):
-    """Autograd of hashgrid_rms_norm_forward: returns y, or (y, s) with a residual, s = x + residual in x's type."""
+    """Autograd of hashgrid_rms_norm_forward: returns y, or (y, s) with a residual, s = x + residual in x's type.
+    The gradients cannot be differentiated again: autograd raises."""
 
     @staticmethod
     def forward(ctx, x, weight, residual=None, eps=1e-6):
@@ -471,6 +475,7 @@ class HashGridRmsNormFunction(torch.autograd.Function):
         return out.y if residual is None else (out.y, out.sum)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, ds=None):
         s, weight, rstd = ctx.saved_tensors
         need = ctx.needs_input_grad + (False,) * (4 - len(ctx.needs_input_grad))
