@@ -554,8 +554,11 @@ typedef struct {
  *   grad_scale : NULL, or a DEVICE fp32 that every gradient is multiplied by
  *                first (loss unscaling, norm clipping); when it is not finite
  *                the step changes nothing.
- *   flags      : HG_ADAM_ZERO_GRAD clears the gradients.
+ *   flags      : HG_ADAM_ZERO_GRAD clears the gradients; with
+ *                HG_ADAM_ZERO_SKIPPED beside it also those of a step that
+ *                grad_scale skips (for callers that add to them otherwise).
  * One launch takes 36 tensors of one state_bits.  Errors: HG_EINVAL, HG_EHIP. */
+#define HG_ADAM_ZERO_SKIPPED 4
 int hashgrid_adamw_step(const hg_adamw *opt, const hg_adamw_tensor *tensors, int32_t n, const float *grad_scale,
                         int32_t flags, void *stream);
 

@@ -48,7 +48,7 @@ struct Tensor {
 struct Args {
     Tensor t[kAdamwTensors];
     int32_t n;
-    int32_t zero_grad;
+    int32_t flags;
     float beta1, beta2, omb1, omb2, root, eps;  // root = 1 / sqrt(1 - b2^t)
     const float *grad_scale;
 };
@@ -141,6 +141,12 @@ __device__ __forceinline__ uint32_t block_exponent(uint32_t bits, int top) {
     return bits == 0 || k < 1 ? 1 : (uint32_t)k;
 }
 
+template <bool kVec>
+__device__ __forceinline__ void clear4(const Tensor &t, int64_t i, int left) {
+    const float z[4] = {0.f, 0.f, 0.f, 0.f};
+    store4<kVec>(t.g, t.grad_type, i, left, z);
+}
+
 template <int kBits, bool kVec>
 __device__ __forceinline__ void update4(const Tensor &t, const Args &a, int64_t i, int left, float scale) {
 #pragma clang fp contract(off)
@@ -200,18 +206,17 @@ __device__ __forceinline__ void update4(const Tensor &t, const Args &a, int64_t 
     }
     store4<kVec>(t.p, HG_F32, i, left, pn);
     if (t.copy) store4<kVec>(t.copy, t.copy_type, i, left, pn);
-    if (a.zero_grad) {
-        const float z[4] = {0.f, 0.f, 0.f, 0.f};
-        store4<kVec>(t.g, t.grad_type, i, left, z);
-    }
+    if (a.flags & HG_ADAM_ZERO_GRAD) clear4<kVec>(t, i, left);
 }
 
 template <int kBits>
 __global__ __launch_bounds__(kThreads) void adamw_kernel(const Args a) {
     float scale = 1.f;
+    bool skip = false;
     if (a.grad_scale) {
         scale = *a.grad_scale;
-        if (!(fabsf(scale) <= 3.402823466e38f)) return;  // not finite: the step does nothing
+        skip = !(fabsf(scale) <= 3.402823466e38f);  // not finite: the step does nothing, or clears the gradients
+        if (skip && !(a.flags & HG_ADAM_ZERO_SKIPPED)) return;
     }
     const int block = (int)(blockIdx.y * kGridX + blockIdx.x);
     // The tensor of this workgroup: first[] is ascending.
@@ -227,14 +232,16 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(const Args a) {
     // Whole waves decide together: a block is a wave's 256 values.
     const int64_t wave_left = t.count - (i - (threadIdx.x & 63) * kPer);
     if (wave_left <= 0) return;
-    if (wave_left >= 256 && t.vec) update4<kBits, true>(t, a, i, 4, scale);
-    else update4<kBits, false>(t, a, i, left > 4 ? 4 : left < 0 ? 0 : (int)left, scale);
+    const int mine = left > 4 ? 4 : left < 0 ? 0 : (int)left;
+    if (skip) clear4<false>(t, i, mine);
+    else if (wave_left >= 256 && t.vec) update4<kBits, true>(t, a, i, 4, scale);
+    else update4<kBits, false>(t, a, i, mine, scale);
 }
 
 }  // namespace
 
 hipError_t launch_adamw(const hg_adamw &opt, const hg_adamw_tensor *tensors, int32_t n, const float *grad_scale,
-                        bool zero_grad, hipStream_t stream) {
+                        int32_t flags, hipStream_t stream) {
     const double bc1 = 1.0 - pow((double)opt.beta1, (double)opt.step), bc2 = 1.0 - pow((double)opt.beta2, (double)opt.step);
     auto al = [](const void *p, uintptr_t k) { return ((uintptr_t)p % k) == 0; };
     for (const int bits : {32, 8}) {
@@ -242,7 +249,7 @@ hipError_t launch_adamw(const hg_adamw &opt, const hg_adamw_tensor *tensors, int
         while (at < n) {
             Args a;
             a.n = 0;
-            a.zero_grad = zero_grad;
+            a.flags = flags;
             a.beta1 = opt.beta1, a.beta2 = opt.beta2;
             a.omb1 = (float)(1.0 - (double)opt.beta1), a.omb2 = (float)(1.0 - (double)opt.beta2);
             a.root = (float)(1.0 / sqrt(bc2));

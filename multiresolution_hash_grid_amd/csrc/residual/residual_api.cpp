@@ -195,7 +195,8 @@ int hashgrid_adamw_step(const hg_adamw *opt, const hg_adamw_tensor *tensors, int
     if (!(opt->beta1 >= 0.f && opt->beta1 < 1.f) || !(opt->beta2 >= 0.f && opt->beta2 < 1.f))
         return abi_fail(HG_EINVAL, "betas must lie in [0, 1)");
     if (!std::isfinite(opt->eps) || opt->eps < 0.f) return abi_fail(HG_EINVAL, "eps must be finite and >= 0");
-    if (flags & ~HG_ADAM_ZERO_GRAD) return abi_fail(HG_EINVAL, "unknown flags 0x%x", flags);
+    if (flags & ~(HG_ADAM_ZERO_GRAD | HG_ADAM_ZERO_SKIPPED)) return abi_fail(HG_EINVAL, "unknown flags 0x%x", flags);
+    if (flags == HG_ADAM_ZERO_SKIPPED) return abi_fail(HG_EINVAL, "HG_ADAM_ZERO_SKIPPED belongs to HG_ADAM_ZERO_GRAD");
     if (n < 0 || (n > 0 && !tensors)) return abi_fail(HG_EINVAL, "n = %d tensors at %p", n, (const void *)tensors);
     int rc = check_vector("grad_scale", grad_scale, false);
     if (rc) return rc;
@@ -218,7 +219,7 @@ int hashgrid_adamw_step(const hg_adamw *opt, const hg_adamw_tensor *tensors, int
             (uintptr_t)t.v % state || (t.copy && (uintptr_t)t.copy % 2))
             return abi_fail(HG_EINVAL, "tensor %d: misaligned buffer", i);
     }
-    return launched(hg::res::launch_adamw(*opt, tensors, n, grad_scale, (flags & HG_ADAM_ZERO_GRAD) != 0, (hipStream_t)stream),
+    return launched(hg::res::launch_adamw(*opt, tensors, n, grad_scale, flags, (hipStream_t)stream),
                     "adamw");
 }
 

@@ -41,7 +41,7 @@ hipError_t launch_rms_norm_backward(const hg_rms_norm_grad &op, void *workspace,
 // Tensors per launch: their descriptions travel in the kernel's arguments.
 constexpr int kAdamwTensors = 36;
 hipError_t launch_adamw(const hg_adamw &opt, const hg_adamw_tensor *tensors, int32_t n, const float *grad_scale,
-                        bool zero_grad, hipStream_t stream);
+                        int32_t flags, hipStream_t stream);
 
 }  // namespace res
 }  // namespace hg

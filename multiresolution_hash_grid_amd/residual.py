@@ -18,6 +18,7 @@ from torch.autograd.function import once_differentiable
 from .hashgrid import (HG_ADAM_ZERO_GRAD, HG_F16, HG_F32, _check, _dev, _keep_for_stream, _stream, load_library)
 
 HG_BF16, HG_F8 = 2, 3
+HG_ADAM_ZERO_SKIPPED = 4
 HG_ACT = {"none": 0, "relu": 1, "silu": 2, "gelu_tanh": 3}
 F8 = torch.float8_e4m3fn
 _CODES = {torch.float32: HG_F32, torch.float16: HG_F16, torch.bfloat16: HG_BF16, F8: HG_F8}
@@ -412,10 +413,12 @@ class HashGridAdamWPlan:
         self._c[i].lr, self._c[i].weight_decay = lr, weight_decay
 
     def step(self, *, step: int, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8, seed: int = 0,
-             grad_scale: torch.Tensor | None = None, zero_grad: bool = False, stream=None) -> None:
+             grad_scale: torch.Tensor | None = None, zero_grad: bool = False, zero_skipped: bool = False,
+             stream=None) -> None:
         """Update every tensor; ``step`` is the 1-based index of this update, ``seed`` that of the 8-bit moments'
         rounding noise (another one each step).  ``grad_scale``: a float32 GPU scalar the gradients are multiplied
-        by; when it is not finite the step changes nothing.  ``zero_grad`` clears the gradients."""
+        by; when it is not finite the step changes nothing.  ``zero_grad`` clears the gradients, with ``zero_skipped``
+        also those of a step that grad_scale skips."""
         if not self.tensors:
             return
         p = self.tensors[0].param
@@ -427,7 +430,8 @@ class HashGridAdamWPlan:
             scale = grad_scale.data_ptr()
         opt = _AdamW(beta1, beta2, eps, step, seed & 0xFFFFFFFF)
         _check(_lib().hashgrid_adamw_step(ctypes.byref(opt), self._c, len(self.tensors), scale,
-                                          HG_ADAM_ZERO_GRAD if zero_grad else 0, _stream(p, stream)))
+                                          (HG_ADAM_ZERO_GRAD if zero_grad else 0) | (HG_ADAM_ZERO_SKIPPED if zero_skipped else 0),
+                                          _stream(p, stream)))
 
 
 def hashgrid_adamw_step(tensors, **kw) -> None:
@@ -568,7 +572,9 @@ class HashGridResidualHead8:
 class HashGridAdamW(torch.optim.Optimizer):
     """AdamW over the tables and a head's weights, all tensors in one call (hashgrid_adamw_step).  Groups have their own
     ``lr`` and ``weight_decay`` (the pages: no decay on the tables, a rate 5 to 10 times the head's); ``state_bits`` 8
-    keeps the moments in 8 bits.  ``grad_scale`` of ``step`` is the float32 GPU scalar gradients are multiplied by."""
+    keeps the moments in 8 bits.  ``grad_scale`` of ``step`` is the float32 GPU scalar gradients are multiplied by; when
+    it is not finite the step leaves parameters and moments as they are.  ``zero_grad_in_step`` clears the gradients
+    inside the step, a skipped one too, so that the next backward can add to them."""
 
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.99), eps=1e-15, weight_decay=0.0, state_bits=32, seed=0,
                  zero_grad_in_step=False):
@@ -598,7 +604,7 @@ class HashGridAdamW(torch.optim.Optimizer):
                                 group["weight_decay"]))
         for ((b1, b2), eps, t), tensors in calls.items():
             HashGridAdamWPlan(tensors).step(step=t, beta1=b1, beta2=b2, eps=eps, seed=self.seed + t, grad_scale=grad_scale,
-                                            zero_grad=self.zero_grad_in_step)
+                                            zero_grad=self.zero_grad_in_step, zero_skipped=self.zero_grad_in_step)
         return loss
 
     def load_state_dict(self, state_dict):
