@@ -543,11 +543,19 @@ typedef struct {
     int32_t state_bits;    /* 32 or 8                                                 */
     int32_t reserved;      /* 0                                                       */
 } hg_adamw_tensor;
+/* The count of a tensor's steps, on the device, where it is known whether a
+ * step was skipped: zero before the first.  The other words are the call's. */
+typedef struct {
+    int32_t step;
+    float step_size, root;
+    uint32_t key;
+} hg_adamw_clock;
 typedef struct {
     float beta1, beta2;    /* in [0, 1)                                               */
     float eps;             /* >= 0                                                    */
-    int32_t step;          /* t >= 1                                                  */
+    int32_t step;          /* t >= 1 (not looked at with HG_ADAM_CLOCK)               */
     uint32_t seed;         /* of the rounding noise: another one each step            */
+    hg_adamw_clock *clocks;/* with HG_ADAM_CLOCK (else not looked at): DEVICE [n]     */
 } hg_adamw;
 /*   tensors    : HOST array of n descriptions, read before the call returns;
  *                the tensors must not overlap.
@@ -557,8 +565,13 @@ typedef struct {
  *   flags      : HG_ADAM_ZERO_GRAD clears the gradients; with
  *                HG_ADAM_ZERO_SKIPPED beside it also those of a step that
  *                grad_scale skips (for callers that add to them otherwise).
+ *                HG_ADAM_CLOCK: a step that is not skipped adds one to each
+ *                tensor's clock (but those of no values), t is that count, and
+ *                the noise's seed is seed + t, so a skipped step leaves no trace;
+ *                one launch of a workgroup more for 36 tensors.
  * One launch takes 36 tensors of one state_bits.  Errors: HG_EINVAL, HG_EHIP. */
 #define HG_ADAM_ZERO_SKIPPED 4
+#define HG_ADAM_CLOCK 8
 int hashgrid_adamw_step(const hg_adamw *opt, const hg_adamw_tensor *tensors, int32_t n, const float *grad_scale,
                         int32_t flags, void *stream);
 

@@ -39,10 +39,11 @@ struct Tensor {
     void *g, *m, *v, *copy;
     uint8_t *me, *ve;
     int64_t count;
-    float step_size;   // lr / (1 - b1^t)
+    float step_size;   // lr / (1 - b1^t); with clocks lr
     float keep;        // 1 - lr wd
     uint32_t key;      // of the rounding noise
     int32_t first;     // first workgroup
+    int32_t place;     // in the caller's list
     int8_t grad_type, copy_type, vec, pad;
 };
 struct Args {
@@ -50,7 +51,9 @@ struct Args {
     int32_t n;
     int32_t flags;
     float beta1, beta2, omb1, omb2, root, eps;  // root = 1 / sqrt(1 - b2^t)
+    uint32_t seed;
     const float *grad_scale;
+    hg_adamw_clock *clocks;
 };
 static_assert(sizeof(Args) <= 4096, "kernel arguments");
 
@@ -68,6 +71,33 @@ __host__ __device__ __forceinline__ uint32_t mix(uint32_t h) {
     h ^= h >> 13;
     h *= 0xC2B2AE35u;
     return h ^ (h >> 16);
+}
+
+__host__ __device__ __forceinline__ uint32_t noise_key(uint32_t seed, int place) {
+    return mix(seed + 0x9E3779B9u * (uint32_t)(place + 1));
+}
+
+// What depends on t, of one tensor.
+struct Rates {
+    float step_size, root;
+    uint32_t key;
+};
+
+__device__ __forceinline__ bool skipped(const Args &a) {
+    return a.grad_scale && !(fabsf(*a.grad_scale) <= 3.402823466e38f);
+}
+
+// Counts the step for each tensor of the launch that follows, unless it is
+// skipped, and leaves there what the host works out where it knows t.
+__global__ __launch_bounds__(64) void adamw_clock_kernel(const Args a) {
+    const int i = threadIdx.x;
+    if (i >= a.n || skipped(a)) return;
+    hg_adamw_clock *const c = a.clocks + a.t[i].place;
+    const int32_t t = c->step + 1;
+    c->step = t;
+    c->step_size = (float)((double)a.t[i].step_size / (1.0 - pow((double)a.beta1, (double)t)));
+    c->root = (float)(1.0 / sqrt(1.0 - pow((double)a.beta2, (double)t)));
+    c->key = noise_key(a.seed + (uint32_t)t, a.t[i].place);
 }
 
 template <bool kVec>
@@ -148,7 +178,7 @@ __device__ __forceinline__ void clear4(const Tensor &t, int64_t i, int left) {
 }
 
 template <int kBits, bool kVec>
-__device__ __forceinline__ void update4(const Tensor &t, const Args &a, int64_t i, int left, float scale) {
+__device__ __forceinline__ void update4(const Tensor &t, const Args &a, const Rates &rates, int64_t i, int left, float scale) {
 #pragma clang fp contract(off)
     float p[4], g[4], m[4], v[4];
     load4<kVec>(t.p, HG_F32, i, left, p);
@@ -173,7 +203,7 @@ __device__ __forceinline__ void update4(const Tensor &t, const Args &a, int64_t 
         const float gj = a.grad_scale ? g[j] * scale : g[j];
         m[j] = m[j] * a.beta1 + gj * a.omb1;
         v[j] = v[j] * a.beta2 + (gj * gj) * a.omb2;
-        pn[j] = p[j] * t.keep - t.step_size * m[j] / (sqrtf(v[j]) * a.root + a.eps);
+        pn[j] = p[j] * t.keep - rates.step_size * m[j] / (sqrtf(v[j]) * rates.root + a.eps);
     }
     if (kBits == 32) {
         store4<kVec>(t.m, HG_F32, i, left, m);
@@ -188,7 +218,7 @@ __device__ __forceinline__ void update4(const Tensor &t, const Args &a, int64_t 
         const uint32_t me = block_exponent(wave_max_u32(mb), 7), ve = block_exponent(wave_max_u32(vb), 15);
         uint32_t mc = 0, vc = 0;
         for (int j = 0; j < 4; ++j) {
-            const uint32_t h = mix((uint32_t)(i + j) ^ t.key);
+            const uint32_t h = mix((uint32_t)(i + j) ^ rates.key);
             const uint32_t mt = __float_as_uint(ldexpf(fabsf(m[j]), 7 - (int)me));
             const uint32_t vt = __float_as_uint(ldexpf(v[j], 15 - (int)ve));
             uint32_t c = ((mt + ((h & 0xFFFFu) << 4)) >> 20) & 127u;
@@ -211,13 +241,9 @@ __device__ __forceinline__ void update4(const Tensor &t, const Args &a, int64_t 
 
 template <int kBits>
 __global__ __launch_bounds__(kThreads) void adamw_kernel(const Args a) {
-    float scale = 1.f;
-    bool skip = false;
-    if (a.grad_scale) {
-        scale = *a.grad_scale;
-        skip = !(fabsf(scale) <= 3.402823466e38f);  // not finite: the step does nothing, or clears the gradients
-        if (skip && !(a.flags & HG_ADAM_ZERO_SKIPPED)) return;
-    }
+    const bool skip = skipped(a);  // the step does nothing, or clears the gradients
+    if (skip && !(a.flags & HG_ADAM_ZERO_SKIPPED)) return;
+    const float scale = a.grad_scale ? *a.grad_scale : 1.f;
     const int block = (int)(blockIdx.y * kGridX + blockIdx.x);
     // The tensor of this workgroup: first[] is ascending.
     int lo = 0, hi = a.n - 1;
@@ -227,6 +253,11 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(const Args a) {
         else hi = mid - 1;
     }
     const Tensor &t = a.t[lo];
+    Rates rates{t.step_size, a.root, t.key};
+    if (a.clocks) {
+        const hg_adamw_clock &c = a.clocks[t.place];
+        rates = {c.step_size, c.root, c.key};
+    }
     const int64_t i = (int64_t)(block - t.first) * kChunk + threadIdx.x * kPer;
     const int64_t left = t.count - i;
     // Whole waves decide together: a block is a wave's 256 values.
@@ -234,15 +265,17 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(const Args a) {
     if (wave_left <= 0) return;
     const int mine = left > 4 ? 4 : left < 0 ? 0 : (int)left;
     if (skip) clear4<false>(t, i, mine);
-    else if (wave_left >= 256 && t.vec) update4<kBits, true>(t, a, i, 4, scale);
-    else update4<kBits, false>(t, a, i, mine, scale);
+    else if (wave_left >= 256 && t.vec) update4<kBits, true>(t, a, rates, i, 4, scale);
+    else update4<kBits, false>(t, a, rates, i, mine, scale);
 }
 
 }  // namespace
 
 hipError_t launch_adamw(const hg_adamw &opt, const hg_adamw_tensor *tensors, int32_t n, const float *grad_scale,
                         int32_t flags, hipStream_t stream) {
-    const double bc1 = 1.0 - pow((double)opt.beta1, (double)opt.step), bc2 = 1.0 - pow((double)opt.beta2, (double)opt.step);
+    const bool clock = (flags & HG_ADAM_CLOCK) != 0;
+    const double t0 = clock ? 1.0 : (double)opt.step;
+    const double bc1 = clock ? 1.0 : 1.0 - pow((double)opt.beta1, t0), bc2 = 1.0 - pow((double)opt.beta2, t0);
     auto al = [](const void *p, uintptr_t k) { return ((uintptr_t)p % k) == 0; };
     for (const int bits : {32, 8}) {
         int32_t at = 0;
@@ -254,7 +287,9 @@ hipError_t launch_adamw(const hg_adamw &opt, const hg_adamw_tensor *tensors, int
             a.omb1 = (float)(1.0 - (double)opt.beta1), a.omb2 = (float)(1.0 - (double)opt.beta2);
             a.root = (float)(1.0 / sqrt(bc2));
             a.eps = opt.eps;
+            a.seed = opt.seed;
             a.grad_scale = grad_scale;
+            a.clocks = clock ? opt.clocks : nullptr;
             int64_t groups = 0;
             for (; at < n && a.n < kAdamwTensors; ++at) {
                 const hg_adamw_tensor &s = tensors[at];
@@ -267,7 +302,8 @@ hipError_t launch_adamw(const hg_adamw &opt, const hg_adamw_tensor *tensors, int
                 t.count = s.count;
                 t.step_size = (float)((double)s.lr / bc1);
                 t.keep = (float)(1.0 - (double)s.lr * (double)s.weight_decay);
-                t.key = mix(opt.seed + 0x9E3779B9u * (uint32_t)(at + 1));
+                t.key = noise_key(opt.seed, at);
+                t.place = at;
                 t.first = (int32_t)groups;
                 t.grad_type = (int8_t)s.grad_dtype, t.copy_type = (int8_t)s.copy_dtype;
                 const uintptr_t sa = bits == 8 ? 4 : 16;
@@ -276,6 +312,7 @@ hipError_t launch_adamw(const hg_adamw &opt, const hg_adamw_tensor *tensors, int
                 groups += more;
             }
             if (a.n == 0) continue;
+            if (clock) adamw_clock_kernel<<<1, 64, 0, stream>>>(a);
             if (bits == 32) adamw_kernel<32><<<grid_of(groups), kThreads, 0, stream>>>(a);
             else adamw_kernel<8><<<grid_of(groups), kThreads, 0, stream>>>(a);
             const hipError_t e = hipGetLastError();

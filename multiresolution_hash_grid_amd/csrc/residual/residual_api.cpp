@@ -191,15 +191,20 @@ int hashgrid_rms_norm_backward(const hg_rms_norm_grad *op, void *workspace, size
 int hashgrid_adamw_step(const hg_adamw *opt, const hg_adamw_tensor *tensors, int32_t n, const float *grad_scale,
                         int32_t flags, void *stream) {
     if (!opt) return abi_fail(HG_EINVAL, "opt is NULL");
-    if (opt->step < 1) return abi_fail(HG_EINVAL, "step %d < 1", opt->step);
+    const bool clock = (flags & HG_ADAM_CLOCK) != 0;
+    if (!clock && opt->step < 1) return abi_fail(HG_EINVAL, "step %d < 1", opt->step);
     if (!(opt->beta1 >= 0.f && opt->beta1 < 1.f) || !(opt->beta2 >= 0.f && opt->beta2 < 1.f))
         return abi_fail(HG_EINVAL, "betas must lie in [0, 1)");
     if (!std::isfinite(opt->eps) || opt->eps < 0.f) return abi_fail(HG_EINVAL, "eps must be finite and >= 0");
-    if (flags & ~(HG_ADAM_ZERO_GRAD | HG_ADAM_ZERO_SKIPPED)) return abi_fail(HG_EINVAL, "unknown flags 0x%x", flags);
-    if (flags == HG_ADAM_ZERO_SKIPPED) return abi_fail(HG_EINVAL, "HG_ADAM_ZERO_SKIPPED belongs to HG_ADAM_ZERO_GRAD");
+    if (flags & ~(HG_ADAM_ZERO_GRAD | HG_ADAM_ZERO_SKIPPED | HG_ADAM_CLOCK))
+        return abi_fail(HG_EINVAL, "unknown flags 0x%x", flags);
+    if ((flags & (HG_ADAM_ZERO_GRAD | HG_ADAM_ZERO_SKIPPED)) == HG_ADAM_ZERO_SKIPPED)
+        return abi_fail(HG_EINVAL, "HG_ADAM_ZERO_SKIPPED belongs to HG_ADAM_ZERO_GRAD");
     if (n < 0 || (n > 0 && !tensors)) return abi_fail(HG_EINVAL, "n = %d tensors at %p", n, (const void *)tensors);
     int rc = check_vector("grad_scale", grad_scale, false);
     if (rc) return rc;
+    if (clock && n > 0 && (!opt->clocks || (uintptr_t)opt->clocks % 4))
+        return abi_fail(HG_EINVAL, "clocks must be an aligned device pointer with HG_ADAM_CLOCK");
     for (int i = 0; i < n; ++i) {
         const hg_adamw_tensor &t = tensors[i];
         if (t.count < 0 || t.count > kMaxRows) return abi_fail(HG_EINVAL, "tensor %d: count %lld outside 0..2^40", i, (long long)t.count);

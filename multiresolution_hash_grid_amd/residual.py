@@ -18,7 +18,7 @@ from torch.autograd.function import once_differentiable
 from .hashgrid import (HG_ADAM_ZERO_GRAD, HG_F16, HG_F32, _check, _dev, _keep_for_stream, _stream, load_library)
 
 HG_BF16, HG_F8 = 2, 3
-HG_ADAM_ZERO_SKIPPED = 4
+HG_ADAM_ZERO_SKIPPED, HG_ADAM_CLOCK = 4, 8
 HG_ACT = {"none": 0, "relu": 1, "silu": 2, "gelu_tanh": 3}
 F8 = torch.float8_e4m3fn
 _CODES = {torch.float32: HG_F32, torch.float16: HG_F16, torch.bfloat16: HG_BF16, F8: HG_F8}
@@ -60,7 +60,7 @@ class _AdamWTensor(ctypes.Structure):
 
 
 class _AdamW(ctypes.Structure):
-    _fields_ = [("beta1", _F), ("beta2", _F), ("eps", _F), ("step", _I32), ("seed", ctypes.c_uint32)]
+    _fields_ = [("beta1", _F), ("beta2", _F), ("eps", _F), ("step", _I32), ("seed", ctypes.c_uint32), ("clocks", _P)]
 
 
 def _packer(structure):
@@ -412,11 +412,12 @@ class HashGridAdamWPlan:
     def set_rates(self, i: int, lr: float, weight_decay: float) -> None:
         self._c[i].lr, self._c[i].weight_decay = lr, weight_decay
 
-    def step(self, *, step: int, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8, seed: int = 0,
+    def step(self, *, step: int = 0, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8, seed: int = 0,
              grad_scale: torch.Tensor | None = None, zero_grad: bool = False, zero_skipped: bool = False,
-             stream=None) -> None:
+             clocks: torch.Tensor | None = None, stream=None) -> None:
         """Update every tensor; ``step`` is the 1-based index of this update, ``seed`` that of the 8-bit moments'
-        rounding noise (another one each step).  ``grad_scale``: a float32 GPU scalar the gradients are multiplied
+        rounding noise (another one each step).  With ``clocks``, an int32 [tensors, 4] GPU tensor, ``step`` is not
+        needed: column 0 counts each tensor's steps, those that were not skipped, and ``seed`` may stay the same.  ``grad_scale``: a float32 GPU scalar the gradients are multiplied
         by; when it is not finite the step changes nothing.  ``zero_grad`` clears the gradients, with ``zero_skipped``
         also those of a step that grad_scale skips."""
         if not self.tensors:
@@ -428,10 +429,14 @@ class HashGridAdamWPlan:
             if grad_scale.numel() != 1 or grad_scale.device != p.device:
                 raise ValueError(f"grad_scale must be a scalar on {p.device}")
             scale = grad_scale.data_ptr()
-        opt = _AdamW(beta1, beta2, eps, step, seed & 0xFFFFFFFF)
-        _check(_lib().hashgrid_adamw_step(ctypes.byref(opt), self._c, len(self.tensors), scale,
-                                          (HG_ADAM_ZERO_GRAD if zero_grad else 0) | (HG_ADAM_ZERO_SKIPPED if zero_skipped else 0),
-                                          _stream(p, stream)))
+        flags = (HG_ADAM_ZERO_GRAD if zero_grad else 0) | (HG_ADAM_ZERO_SKIPPED if zero_skipped else 0)
+        if clocks is not None:
+            _dev(clocks, "clocks", torch.int32)
+            if clocks.shape != (len(self.tensors), 4) or not clocks.is_contiguous() or clocks.device != p.device:
+                raise ValueError(f"clocks must be a contiguous [{len(self.tensors)}, 4] tensor on {p.device}")
+            flags |= HG_ADAM_CLOCK
+        opt = _AdamW(beta1, beta2, eps, step, seed & 0xFFFFFFFF, None if clocks is None else clocks.data_ptr())
+        _check(_lib().hashgrid_adamw_step(ctypes.byref(opt), self._c, len(self.tensors), scale, flags, _stream(p, stream)))
 
 
 def hashgrid_adamw_step(tensors, **kw) -> None:
@@ -573,8 +578,9 @@ class HashGridAdamW(torch.optim.Optimizer):
     """AdamW over the tables and a head's weights, all tensors in one call (hashgrid_adamw_step).  Groups have their own
     ``lr`` and ``weight_decay`` (the pages: no decay on the tables, a rate 5 to 10 times the head's); ``state_bits`` 8
     keeps the moments in 8 bits.  ``grad_scale`` of ``step`` is the float32 GPU scalar gradients are multiplied by; when
-    it is not finite the step leaves parameters and moments as they are.  ``zero_grad_in_step`` clears the gradients
-    inside the step, a skipped one too, so that the next backward can add to them."""
+    it is not finite the step leaves parameters and moments as they are and does not count: each state's "step" is an
+    int32 on the GPU.  ``zero_grad_in_step`` clears the gradients inside the step, a skipped one too, so that the next
+    backward can add to them."""
 
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.99), eps=1e-15, weight_decay=0.0, state_bits=32, seed=0,
                  zero_grad_in_step=False):
@@ -598,19 +604,39 @@ class HashGridAdamW(torch.optim.Optimizer):
                 if not st:
                     st["step"] = 0
                     st.update(AdamWTensor.states(p, group["state_bits"]))
-                st["step"] += 1
-                calls.setdefault((tuple(group["betas"]), group["eps"], st["step"]), []).append(
-                    AdamWTensor(p, p.grad, st["m"], st["v"], st.get("m_exp"), st.get("v_exp"), None, group["lr"],
-                                group["weight_decay"]))
-        for ((b1, b2), eps, t), tensors in calls.items():
-            HashGridAdamWPlan(tensors).step(step=t, beta1=b1, beta2=b2, eps=eps, seed=self.seed + t, grad_scale=grad_scale,
-                                            zero_grad=self.zero_grad_in_step, zero_skipped=self.zero_grad_in_step)
+                tensors, states = calls.setdefault((tuple(group["betas"]), group["eps"]), ([], []))
+                tensors.append(AdamWTensor(p, p.grad, st["m"], st["v"], st.get("m_exp"), st.get("v_exp"), None, group["lr"],
+                                           group["weight_decay"]))
+                states.append(st)
+        for ((b1, b2), eps), (tensors, states) in calls.items():
+            HashGridAdamWPlan(tensors).step(beta1=b1, beta2=b2, eps=eps, seed=self.seed, grad_scale=grad_scale,
+                                            zero_grad=self.zero_grad_in_step, zero_skipped=self.zero_grad_in_step,
+                                            clocks=self._clocks(states, tensors[0].param.device))
         return loss
 
+    @staticmethod
+    def _clocks(states, device) -> torch.Tensor:
+        """The [n, 4] clocks of a call, whose column 0 the states' "step" are: as they lie where the same states came
+        together before, else gathered anew (from a checkpoint's numbers too)."""
+        steps = [st["step"] for st in states]
+        if all(isinstance(s, torch.Tensor) and s.device == device and s.dtype == torch.int32 for s in steps):
+            at = steps[0].untyped_storage()
+            if at.nbytes() == 16 * len(steps) and all(s.data_ptr() == at.data_ptr() + 16 * i for i, s in enumerate(steps)):
+                return torch.as_strided(steps[0], (len(steps), 4), (4, 1), 0)
+        clocks = torch.zeros(len(steps), 4, dtype=torch.int32, device=device)
+        if any(isinstance(s, torch.Tensor) or s for s in steps):
+            clocks[:, 0] = torch.stack([torch.as_tensor(s, device=device).reshape(()).to(torch.int32) for s in steps])
+        for i, st in enumerate(states):
+            st["step"] = clocks[i, 0]
+        return clocks
+
     def load_state_dict(self, state_dict):
-        """Restores 8-bit moments in their own types, which Optimizer.load_state_dict turns into the parameter's."""
+        """Restores 8-bit moments in their own types, which Optimizer.load_state_dict turns into the parameter's, and
+        counts of its own, which it would share with the dict."""
         super().load_state_dict(state_dict)
         for st in self.state.values():
+            if isinstance(st.get("step"), torch.Tensor):
+                st["step"] = st["step"].clone()
             if "m_exp" in st:
                 st["m"] = st["m"].to(F8)
                 for k in ("v", "m_exp", "v_exp"):
