@@ -461,7 +461,8 @@ int hashgrid_linear_backward(const hg_linear_grad *op, void *workspace, size_t w
  * in fp32 between the loads and each output's one rounding (y is made from the
  * unrounded s).  With y_dtype HG_F8 each row has a scale, y_scale = max |s q w|
  * / 448, and y holds s q w / y_scale rounded to nearest even: the 8-bit operand
- * and x_scale of hashgrid_linear_forward.  A row of zeros has scale 0; a row
+ * and x_scale of hashgrid_linear_forward.  A row of zeros has scale 0 (as
+ * has one whose scale is below fp32's smallest value: its y are 0 too); a row
  * with a y that is not finite has scale NaN.  y and sum may be x or r themselves (same stride
  * and type). */
 typedef struct {

@@ -39,6 +39,21 @@ __device__ __forceinline__ float row_all(float v, float (*lds)[kThreads / 64], i
     return v;
 }
 
+// Of a row whose largest |y| is top: the scale of its 8-bit values, top / 448, and
+// the factors up and inv that take y to them.  448 / top leaves fp32 where top is
+// below 2^-119, so such rows are first moved up by a power of two, exactly.  A scale
+// of 0 (top too small for one) makes a row of zeros, as does NaN.
+struct Scaling {
+    float scale, up, inv;
+};
+__device__ __forceinline__ Scaling scaling_of(float top) {
+    Scaling s;
+    s.scale = top / 448.f;
+    s.up = top < 0x1p-100f ? 0x1p100f : 1.f;
+    s.inv = s.scale > 0.f ? 448.f / (top * s.up) : 0.f;
+    return s;
+}
+
 struct NormArgs {
     int64_t m, xs, rs, ys, ss;
     int c;
@@ -111,12 +126,17 @@ __global__ __launch_bounds__(kThreads) void norm_kernel(const NormArgs a) {
             if (bad != 0.f) top = __builtin_inff();  // a row with a NaN has the scale NaN: larger than any maximum on the way
             top = row_all<G, true>(top, lds, turn);
             if (top == __builtin_inff()) top = __builtin_nanf("");
-            const float inv = top > 0.f ? 448.f / top : 0.f;
+            const Scaling sc = scaling_of(top);
+            if (sc.up != 1.f)
+#pragma unroll
+                for (int i = 0; i < I; ++i)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[i][j] *= sc.up;
 #pragma unroll
             for (int i = 0; i < I; ++i)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[i][j] = fminf(fmaxf(v[i][j] * inv, -448.f), 448.f);
-            if (lane == 0) a.scale[row] = top / 448.f;
+                for (int j = 0; j < 8; ++j) v[i][j] = fminf(fmaxf(v[i][j] * sc.inv, -448.f), 448.f);
+            if (lane == 0) a.scale[row] = sc.scale;
         }
 #pragma unroll
         for (int i = 0; i < I; ++i) store8<G == 4>((Y *)a.y + row * a.ys, at[i], a.c, v[i]);
@@ -165,7 +185,7 @@ __global__ __launch_bounds__(kThreads) void norm_long_kernel(const NormArgs a) {
         sq = row_all<kThreads, false>(sq, lds, turn);
         const float q = 1.f / sqrtf(sq * a.inv_c + a.eps);
         if (a.rstd && threadIdx.x == 0) a.rstd[row] = q;
-        float inv = 1.f;
+        Scaling sc{};
         if constexpr (sizeof(Y) == 1) {
             float top = 0.f, bad = 0.f;
             for (int k = threadIdx.x * 8; k < a.c; k += kThreads * 8) {
@@ -182,8 +202,8 @@ __global__ __launch_bounds__(kThreads) void norm_long_kernel(const NormArgs a) {
             if (bad != 0.f) top = __builtin_inff();
             top = row_all<kThreads, true>(top, lds, turn);
             if (top == __builtin_inff()) top = __builtin_nanf("");
-            inv = top > 0.f ? 448.f / top : 0.f;
-            if (threadIdx.x == 0) a.scale[row] = top / 448.f;
+            sc = scaling_of(top);
+            if (threadIdx.x == 0) a.scale[row] = sc.scale;
         }
         for (int k = threadIdx.x * 8; k < a.c; k += kThreads * 8) {
             const Columns at = columns_of(k, a.c);
@@ -194,7 +214,7 @@ __global__ __launch_bounds__(kThreads) void norm_long_kernel(const NormArgs a) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 v[j] = v[j] * q * w[j];
-                if constexpr (sizeof(Y) == 1) v[j] = fminf(fmaxf(v[j] * inv, -448.f), 448.f);
+                if constexpr (sizeof(Y) == 1) v[j] = fminf(fmaxf(v[j] * sc.up * sc.inv, -448.f), 448.f);
             }
             store_own((Y *)a.y + row * a.ys, at, a.c, v);
         }
