@@ -545,9 +545,11 @@ class HashGridResidualHead(torch.nn.Module):
 
 def quantize_rows(w: torch.Tensor) -> tuple:
     """(e4m3 values, scales) of a matrix, one scale a row: the largest magnitude of a row at 448."""
-    scale = w.detach().float().abs().amax(1) / 448.0
-    inv = torch.where(scale > 0, 1.0 / scale, torch.zeros_like(scale))
-    return (w.detach().float() * inv[:, None]).clamp(-448.0, 448.0).to(F8), scale
+    w = w.detach().float()
+    scale = w.abs().amax(1) / 448.0
+    up = torch.where(scale < 2.0 ** -100, 2.0 ** 100, 1.0)  # 1 / scale of a tiny row would not be finite
+    inv = torch.where(scale > 0, 1.0 / (scale * up), torch.zeros_like(scale))
+    return (w * up[:, None] * inv[:, None]).clamp(-448.0, 448.0).to(F8), scale
 
 
 class HashGridResidualHead8:
