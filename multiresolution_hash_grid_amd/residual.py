@@ -481,6 +481,7 @@ class HashGridRmsNormFunction(torch.autograd.Function):
         out = hashgrid_rms_norm_forward(x, weight, residual=residual, eps=eps, save_sum=residual is not None, save_rstd=True)
         s = x if residual is None else out.sum
         ctx.save_for_backward(s, weight, out.rstd)
+        ctx.set_materialize_grads(False)  # an output that nothing reads has no gradient, not one of zeros
         return out.y if residual is None else (out.y, out.sum)
 
     @staticmethod
@@ -488,6 +489,8 @@ class HashGridRmsNormFunction(torch.autograd.Function):
     def backward(ctx, dy, ds=None):
         s, weight, rstd = ctx.saved_tensors
         need = ctx.needs_input_grad + (False,) * (4 - len(ctx.needs_input_grad))
+        if dy is None:  # s alone goes on
+            return ds, torch.zeros_like(weight) if need[1] else None, ds if need[2] else None, None
         dx, dw = hashgrid_rms_norm_backward(dy.contiguous(), s, weight, rstd, ds=None if ds is None else ds.contiguous(),
                                             need_dw=need[1])
         return dx, dw, dx if need[2] else None, None

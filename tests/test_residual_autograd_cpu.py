@@ -70,3 +70,24 @@ def test_rms_norm_cannot_be_differentiated_twice(calls, residual):
     r = leaf(5, 8) if residual else None
     out = R.HashGridRmsNormFunction.apply(x, w, r)
     refuses_second_derivatives(out[0] + out[1] if residual else out, [x, w] + ([r] if residual else []))
+
+
+def plain_norm(x, w, r, eps=1e-6):
+    s = x + r
+    return s * (s.square().mean(1, keepdim=True) + eps).rsqrt() * w, s
+
+
+@pytest.mark.parametrize("use_y,use_s", [(True, False), (False, True), (True, True)])
+def test_rms_norm_passes_on_only_the_gradients_there_are(calls, use_y, use_s):
+    # An output without a gradient (the sum in front of a head's last layer) is not one of zeros: those would be written and read.
+    x, w, r, c = leaf(6, 8), leaf(8), leaf(6, 8), torch.randn(6, 8)
+    want = torch.autograd.grad(sum(t.mul(c).sum() for t, u in zip(plain_norm(x, w, r), (use_y, use_s)) if u), [x, w, r],
+                               allow_unused=True)
+    y, s = R.HashGridRmsNormFunction.apply(x, w, r)
+    sum(t.mul(c).sum() for t, u in zip((y, s), (use_y, use_s)) if u).backward()
+    for t, g in zip((x, w, r), want):
+        assert t.grad.shape == t.shape
+        assert torch.allclose(t.grad, torch.zeros_like(t) if g is None else g, atol=1e-5)
+    assert len(calls) == (1 if use_y else 0)
+    if use_y:
+        assert (calls[0]["ds"] is not None) == use_s
