@@ -490,7 +490,8 @@ int hashgrid_rms_norm_forward(const hg_rms_norm *op, void *stream);
  *   dx = q (w dy - h mean(w dy h)) + ds,  h = s q,  dw = sum over rows of dy h
  * dx is the gradient of x and of r alike.  dw is WRITTEN, or added to with
  * accumulate (zero or unchanged with m == 0); its order of summation is fixed by
- * the sizes.  dx may be dy, s or ds itself (same stride) for c <= 4096. */
+ * the sizes.  dx may be dy, s or ds itself (same stride) for c <= 4096
+ * (above, HG_EINVAL: such rows are read again after dx is written). */
 typedef struct {
     int64_t m;
     int32_t c;

@@ -37,6 +37,12 @@ int check_rows(const char *name, const void *p, int64_t stride, int64_t m, int64
     return HG_OK;
 }
 
+// An output in place of an input: rows of the same stride, or they would meet others.
+int check_in_place(const char *out, const void *p, int64_t stride, const char *in, const void *q, int64_t q_stride, int64_t m) {
+    if (!p || p != q || m < 2 || stride == q_stride) return HG_OK;
+    return abi_fail(HG_EINVAL, "%s in place of %s needs its row stride (%lld, not %lld)", out, in, (long long)q_stride, (long long)stride);
+}
+
 int check_vector(const char *name, const float *p, bool needed) {
     if (!p) return needed ? abi_fail(HG_EINVAL, "%s is NULL", name) : HG_OK;
     if ((uintptr_t)p % 4) return abi_fail(HG_EINVAL, "%s is not 4-byte aligned", name);
@@ -81,6 +87,7 @@ int check_linear(const hg_linear *op) {
     if ((rc = check_rows("residual", op->residual, op->residual_stride, op->m, op->n, op->y_dtype, false))) return rc;
     if ((rc = check_rows("y", op->y, op->y_stride, op->m, op->n, op->y_dtype, true))) return rc;
     if ((rc = check_rows("pre", op->pre, op->pre_stride, op->m, op->n, op->x_dtype, false))) return rc;
+    if ((rc = check_in_place("y", op->y, op->y_stride, "residual", op->residual, op->residual_stride, op->m))) return rc;
     if ((rc = check_vector("x_scale", op->x_scale, eight)) || (rc = check_vector("w_scale", op->w_scale, eight))) return rc;
     return check_vector("bias", op->bias, false);
 }
@@ -124,6 +131,11 @@ int check_norm_grad(const hg_rms_norm_grad *op) {
     if ((rc = check_rows("sum", op->sum, op->sum_stride, op->m, op->c, op->dtype, rows))) return rc;
     if ((rc = check_rows("ds", op->ds, op->ds_stride, op->m, op->c, op->dtype, false))) return rc;
     if ((rc = check_rows("dx", op->dx, op->dx_stride, op->m, op->c, op->dtype, rows))) return rc;
+    if (rows && op->c > hg::res::kNormHeld && (op->dx == op->dy || op->dx == op->sum || op->dx == op->ds))
+        return abi_fail(HG_EINVAL, "dx in place of dy, sum or ds: c = %d > %d", op->c, hg::res::kNormHeld);
+    if ((rc = check_in_place("dx", op->dx, op->dx_stride, "dy", op->dy, op->dy_stride, op->m))) return rc;
+    if ((rc = check_in_place("dx", op->dx, op->dx_stride, "sum", op->sum, op->sum_stride, op->m))) return rc;
+    if ((rc = check_in_place("dx", op->dx, op->dx_stride, "ds", op->ds, op->ds_stride, op->m))) return rc;
     if ((rc = check_vector("w", op->w, rows)) || (rc = check_vector("rstd", op->rstd, rows))) return rc;
     return check_vector("dw", op->dw, false);
 }
@@ -170,6 +182,11 @@ int hashgrid_rms_norm_forward(const hg_rms_norm *op, void *stream) {
     if ((rc = check_rows("sum", op->sum, op->sum_stride, op->m, op->c, op->dtype, false))) return rc;
     if ((rc = check_vector("w", op->w, true)) || (rc = check_vector("y_scale", op->y_scale, eight))) return rc;
     if ((rc = check_vector("rstd", op->rstd, false))) return rc;
+    if (eight && (op->y == op->x || op->y == op->residual)) return abi_fail(HG_EINVAL, "y in place of x or residual needs their type");
+    if ((rc = check_in_place("y", op->y, op->y_stride, "x", op->x, op->x_stride, op->m))) return rc;
+    if ((rc = check_in_place("y", op->y, op->y_stride, "residual", op->residual, op->residual_stride, op->m))) return rc;
+    if ((rc = check_in_place("sum", op->sum, op->sum_stride, "x", op->x, op->x_stride, op->m))) return rc;
+    if ((rc = check_in_place("sum", op->sum, op->sum_stride, "residual", op->residual, op->residual_stride, op->m))) return rc;
     return launched(hg::res::launch_rms_norm_forward(*op, (hipStream_t)stream), "rms_norm forward");
 }
 

@@ -17,6 +17,7 @@ int abi_ok();
 
 namespace res {
 
+constexpr int kNormHeld = 4096;  // columns of a norm's row that a workgroup holds in registers (256 threads x 2 vectors of 8)
 constexpr int kCus = 256;  // MI355X: 8 XCDs of 32 CUs
 
 inline int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }

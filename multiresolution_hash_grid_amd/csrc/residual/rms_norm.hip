@@ -18,7 +18,6 @@ namespace res {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kWide = 4096;  // columns that a workgroup holds (256 threads x 2 vectors of 8)
 
 // Sum or maximum over the G lanes of a row, in each of them: lanes of a wave, or
 // (G = 256) the workgroup, through one of two LDS slots in turn, so that one
@@ -407,7 +406,7 @@ int grad_group(int c) {
 }
 // Workgroups (and partial rows) of a backward: as many as are resident.
 int64_t grad_groups(int64_t m, int c) {
-    if (c > kWide) return m < 256 ? m : 256;
+    if (c > kNormHeld) return m < 256 ? m : 256;
     if (m == 0) return 0;
     const int64_t need = div_up(m, kThreads / grad_group(c)), most = kCus * 8;
     return need < most ? need : most;

@@ -304,7 +304,8 @@ def hashgrid_rms_norm_backward(dy: torch.Tensor, s: torch.Tensor, weight: torch.
                                stream=None) -> tuple:
     """(dx, dweight) of hashgrid_rms_norm_forward for upstream ``dy``, from the saved sum ``s`` and ``rstd``; ``ds`` is
     the gradient that reaches s itself and is added.  dx is the gradient of x and of the residual; dweight is float32
-    (with ``accumulate``, ``dw`` must be given and is added to)."""
+    (with ``accumulate``, ``dw`` must be given and is added to).  ``dx`` receives the gradient; it may be dy, s or ds for
+    rows of up to 4096 columns."""
     _matrix(s, "s")
     m, c = mc = s.shape
     dtype, device = s.dtype, s.device
