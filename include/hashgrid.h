@@ -424,7 +424,7 @@ int hashgrid_linear_forward(const hg_linear *op, void *stream);
  * dw and db are WRITTEN, or added to their old values with accumulate; with
  * m == 0 they are zero (or unchanged).  The order of every sum is fixed by the
  * sizes: results do not depend on scheduling.  Row strides of dy, pre, x and dx are
- * at most 2^22. */
+ * at most 2^22 (with one row they are not looked at). */
 typedef struct {
     int64_t m;
     int32_t k, n;

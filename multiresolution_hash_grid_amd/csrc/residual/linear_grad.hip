@@ -43,7 +43,9 @@ GradPlan plan(const hg_linear_grad &op) {
 size_t linear_backward_bytes(const hg_linear_grad &op) { return plan(op).bytes; }
 
 hipError_t launch_linear_backward(const hg_linear_grad &op, void *workspace, hipStream_t stream) {
-    const GradArgs a{op.m, op.dy_stride, op.pre_stride, op.x_stride, op.w_stride, op.dx_stride, op.dw_stride,
+    // (one row has no stride; the kernels' 32-bit offsets hold those of more)
+    auto rows = [&](int64_t stride) { return op.m > 1 ? stride : 0; };
+    const GradArgs a{op.m, rows(op.dy_stride), rows(op.pre_stride), rows(op.x_stride), op.w_stride, rows(op.dx_stride), op.dw_stride,
                      op.k, op.n, op.act, op.accumulate, op.dw_dtype == HG_F32, op.dy, op.pre, op.x, op.w, op.dx, op.dw, op.db};
     if (!a.dx && !a.dw && !a.db) return hipSuccess;
     const auto run = op.dtype == HG_F16 ? linear_grad_f16 : linear_grad_bf16;

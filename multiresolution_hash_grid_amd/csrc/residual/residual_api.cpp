@@ -109,8 +109,13 @@ int check_linear_grad(const hg_linear_grad *op) {
     if ((rc = check_rows("w", op->w, op->w_stride, op->n, op->k, op->dtype, rows && op->dx))) return rc;
     if ((rc = check_rows("dx", op->dx, op->dx_stride, op->m, op->k, op->dtype, false))) return rc;
     if ((rc = check_rows("dw", op->dw, op->dw_stride, op->n, op->k, op->dw_dtype, false))) return rc;
-    for (const int64_t stride : {op->dy_stride, op->pre_stride, op->x_stride, op->dx_stride})
-        if (stride > kMaxGradStride) return abi_fail(HG_EINVAL, "row stride %lld > 2^22", (long long)stride);
+    const struct {
+        const void *p;
+        int64_t stride;
+    } matrices[] = {{op->dy, op->dy_stride}, {op->pre, op->pre_stride}, {op->x, op->x_stride}, {op->dx, op->dx_stride}};
+    for (const auto &t : matrices)
+        if (t.p && op->m > 1 && t.stride > kMaxGradStride)
+            return abi_fail(HG_EINVAL, "row stride %lld > 2^22", (long long)t.stride);
     return check_vector("db", op->db, false);
 }
 
