@@ -159,6 +159,15 @@ __device__ __forceinline__ void put(T *p, int left, Held<N, T> h) {
         if (j < left) p[j] = h.v[j];
 }
 
+// LDS written by other lanes of the wave may be read after this, and what they
+// read overwritten.  The hardware keeps a wave's LDS accesses in order; this keeps
+// the compiler from moving them.
+__device__ __forceinline__ void wave_exchange() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // Sum over aligned groups of G lanes, in every lane of the group.
 template <int G>
 __device__ __forceinline__ float group_sum(float v) {

@@ -70,13 +70,13 @@ __device__ __forceinline__ void stage_put(char *stage, int row, int eight, Held<
     }
 }
 // The first `pairs` * 32 values of each row to columns n .. of rows m1 ..; only
-// rows below `rows` and columns below `width` exist.  The wave's own writes are
-// in order before its reads.
+// rows below `rows` and columns below `width` exist.
 template <typename V>
 __device__ __forceinline__ void stage_store(V *y, int64_t stride, int64_t m1, int64_t rows, int n, int width, const char *stage,
                                             int pairs, int lane) {
     constexpr int per = 16 / (int)sizeof(V);  // values of a piece
     const int pieces = pairs * 32 / per;      // of a row: a multiple of 4
+    wave_exchange();
 #pragma unroll 1
     for (int at = lane; at < pieces * 16; at += 64) {
         const int row = at / pieces, c = at - row * pieces;
@@ -84,6 +84,7 @@ __device__ __forceinline__ void stage_store(V *y, int64_t stride, int64_t m1, in
         const Held<per, V> h = {__builtin_bit_cast(VP, *(const u32x4 *)(stage + row * 512 + ((c ^ row) << 4)))};
         if (m1 + row < rows) put(y + (m1 + row) * stride + n + c * per, width - n - c * per, h);
     }
+    wave_exchange();
 }
 
 // Many rows, a weight that fits LDS in a few slices.  A workgroup keeps its
