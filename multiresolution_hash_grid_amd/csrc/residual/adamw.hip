@@ -24,8 +24,9 @@
 // becomes fp32's smallest normal makes the truncation of fp32 bits the
 // truncation of the code, gradual underflow included: noise is added below
 // the last bit kept and the word is shifted.
-// Bound by memory: 28 + 2 bytes a value with fp32 state and a 16-bit copy, 18 with
-// 8-bit state; 2^24 and 2^25 values go at 5.2 TB/s.
+// Bound by memory: 28 + 2 bytes a value with fp32 state and a 16-bit copy, 16 + 2
+// with 8-bit state; 2^24 values of the one go in 105 us (4.8 TB/s), 2^25 of the
+// other in 119 (5.1 TB/s).
 // The state's arithmetic is one IEEE operation at a time (no contraction), so
 // that the codes do not depend on how a compiler pairs operations.
 #include "device_types.h"
@@ -59,8 +60,8 @@ static_assert(sizeof(Args) <= 4096, "kernel arguments");
 
 constexpr int kThreads = 256;
 constexpr int kPer = 4;                        // consecutive values of a thread: a wave has one 256-value block
-// One block a wave: 2^24 values of fp32 state and 2^25 of 8-bit state take 106 and 127 us;
-// with 2, 4, 8 blocks 112, 117, 123 and 135, 144, 154 (a wave's stores hold back its next loads).
+// One block a wave: with 2, 4, 8 blocks 2^24 values of fp32 state take 6, 10, 16 % longer and
+// 2^25 of 8-bit state 6, 13, 21 (a wave's stores hold back its next loads).
 constexpr int kChunk = kThreads * kPer;
 constexpr int64_t kMaxGroups = 1023 * kGridX;  // of a launch, in whole rows of the grid: their numbers are 32-bit
 

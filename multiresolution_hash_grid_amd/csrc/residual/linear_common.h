@@ -22,8 +22,9 @@ constexpr int kPiece = 16 / (int)sizeof(T);    // elements of a lane
 
 // 16 8-bit values as binary16, which holds every one of them exactly.  The
 // matrix cores' own 8-bit products sum with the smaller terms cut at about
-// 2^-14 of a step's largest (measured: errors up to 9e-5 of sum |x w|, both for
-// the 32- and the 128-deep instruction), so 8-bit operands are widened where
+// 2^-14 of a step's largest (128 products of random e4m3 codes against their exact
+// sum: errors up to 8e-5 of sum |x w|, alike for the 32- and the 128-deep
+// instruction; fp32 sums of 128 stay below 8e-6), so 8-bit operands are widened where
 // they enter a product and their sums are fp32 like the others'.
 struct Widened {
     u32x4 lo, hi;

@@ -185,7 +185,8 @@ __device__ __forceinline__ void put_db(const GradArgs &a, int n, float t) {
 // joined in a fixed order by grad_join_kernel; a workgroup alone with its tile
 // (few rows) writes them itself.
 // Wider layers: tiles of NT x KT (blockIdx.y over outputs, .z over inputs)
-// make dW and db alone, and the first column of tiles writes dz for dx's sake.
+// make dW and db alone, and the first column of tiles writes dz for dx's sake;
+// each column of tiles reads dy and z and works out the slopes again.
 // 2^18 x 256 x 256 bf16 with SiLU: 150 us with its join, 3.6 TB/s: W^T, dz and x fill
 // the LDS and the products' sums the registers, so one step's loads are all that
 // is on its way, and a step's products and its slope's arithmetic are not hidden

@@ -109,10 +109,11 @@ __device__ __forceinline__ void stage_store(V *y, int64_t stride, int64_t m1, in
 // rows, so x comes from HBM once.  A weight of more slices than an XCD's share of
 // the workgroups has fewer than 8 walkers a slice (1, 2 or 4): each keeps to its
 // XCDs, and the slices go around all of them.
-// Bound by memory, and at 8 bits by what a wave does per output (widening, GELU,
-// residual) between its loads.  2^20 x 256 x 256 bf16 with SiLU and residual: 300 us,
-// 5.4 TB/s; 2^18 x 32 x 256 f16 with z kept: 60 us, 4.8 TB/s; 10^5 x 256 x 4: 10.5 us;
-// 2^18 x 512 x 512 e4m3 with GELU and residual: 200 us, 3.4 TB/s.
+// Bound by memory, and at 8 bits by what a wave does (widening, GELU, residual)
+// between its loads, eight waves a CU: the VALU is 42 % busy, the matrix units 28.
+// 2^20 x 256 x 256 bf16 with SiLU and residual: 300-309 us, 5.2-5.4 TB/s; 2^18 x 32 x
+// 256 f16 with z kept: 60 us, 4.7 TB/s; 10^5 x 256 x 4: 10.8 us; 2^18 x 512 x 512 e4m3
+// with GELU and residual: 198-206 us, 3.3 TB/s.
 // kCut: 0 the contraction is whole fragments; 1 its last fragment is cut; 2 it
 // is shorter than a piece.
 template <typename T, typename Y, int KU, int RF, int FR, int GS, int kCut, bool kStage>
@@ -507,8 +508,11 @@ hipError_t run_long(const FwdArgs &a, hipStream_t stream) {
 // In LDS a row's eight pieces are permuted by three bits of its number, those in
 // which the 16 rows of a fragment read differ, lines of 256 bytes apart: rows
 // follow each other in x, and in W go as the outputs are dealt to the lanes.
-// Bound by the matrix units' feed from LDS: 2^16 x 1024 x 1024 bf16 240-290 us, 0.5-0.57
-// PFLOP/s.
+// No unit is: the matrix units are 23 % busy, LDS is active 18-20 % of the cycles
+// without conflicts.  A step's LDS writes, its reads and its products follow one
+// another between two barriers, and two workgroups a CU do not fill the gaps.  y
+// leaves in half lines: 1.7 times its bytes are written.  2^16 x 1024 x 1024 bf16
+// 240-290 us, 0.5-0.57 PFLOP/s.
 template <bool kDealt>
 __device__ __forceinline__ int block_at(int row, int piece) {
     const int turn = kDealt ? ((row >> 1) & 1) | ((row >> 2) & 6) : (row >> 1) & 7;

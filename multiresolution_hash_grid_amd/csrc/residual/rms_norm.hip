@@ -8,9 +8,10 @@
 // loads and the one rounding of each output; y is made from the unrounded s.
 // The 8-bit output is e4m3 with one scale a row, max |y| / 448: y is in
 // registers when the maximum is known, so the 8 bits cost no second pass.
-// Bound by memory: 2^18 x 256 bf16 with s kept 98 us (5.4 TB/s), 2^20 x 256 to 8 bits
-// 254 us (5.3 TB/s), backward of 200003 x 96 f16 38 us (4.1 TB/s, a second launch that
-// joins dw included).
+// Bound by memory: 2^18 x 256 bf16 with s kept 98-101 us (5.4 TB/s), 2^20 x 256 to 8
+// bits 254-259 us (5.2 TB/s), backward of 200003 x 96 f16 38 us (4.1 TB/s, a second
+// launch that joins dw included).  Backward of few long rows: a workgroup has one row
+// and writes a partial row of dw as long, so 2048 x 4096 bf16 takes 33 us.
 #include "device_types.h"
 
 namespace hg {

@@ -49,8 +49,9 @@ COPY_BYTES = 256 << 20
 
 
 def all_sources() -> tuple:
-    """Every file of the library's sources: kernels, their headers and the host
-    code that sizes and launches them."""
+    """Every file of the encoder's and its head's sources: kernels, their headers
+    and the host code that sizes and launches them (the residual head's operators
+    lie in a folder of their own)."""
     return tuple(sorted(f for f in os.listdir(CSRC) if f.endswith((".hip", ".h", ".cpp"))))
 
 
