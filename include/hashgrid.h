@@ -577,6 +577,180 @@ typedef struct {
 int hashgrid_adamw_step(const hg_adamw *opt, const hg_adamw_tensor *tensors, int32_t n, const float *grad_scale,
                         int32_t flags, void *stream);
 
+/* Rows of a table by their numbers: the codes of images or frames that a head
+ * reads beside the encoding (the page's 96-wide input: 32 features and a 64-wide
+ * code), or tokens' embeddings.
+ *   y[p] = scale * table[ids[p]]
+ * in fp32, rounded once.  An id outside 0..rows-1 names no row: its y is zero.
+ * y may be columns of a wider buffer; what lies beside them stays as it is.  y
+ * must not overlap the table. */
+typedef struct {
+    int64_t m;             /* ids, >= 0                                               */
+    int32_t rows, c;       /* of the table: 0..2^31-1 rows, 1..2^20 columns           */
+    const void *ids;       /* [m] of ids_bits                                         */
+    const void *table;     /* [rows][c] of table_dtype (not looked at with no rows)   */
+    int64_t table_stride;
+    void *y;               /* [m][c] of y_dtype, WRITTEN                              */
+    int64_t y_stride;
+    float scale;
+    int32_t ids_bits;      /* 32 or 64: signed whole numbers                          */
+    int32_t table_dtype;   /* HG_F32, HG_F16 or HG_BF16                               */
+    int32_t y_dtype;       /* table_dtype, or HG_F16 or HG_BF16 of an HG_F32 table    */
+} hg_embedding;
+int hashgrid_embedding_forward(const hg_embedding *op, void *stream);
+
+/* Gradient of the table for upstream dy = dL/dy:
+ *   dtable[v] = scale * (sum of dy[p] over the p with ids[p] = v)
+ * Sums are fp32, the scaled sum is rounded once; rows that no id names are zero.
+ * dtable is WRITTEN, or added to its old values with accumulate (rows that no id
+ * names then stay as they are).  The ids are sorted first, equal ones in the order
+ * they came, and each row's sum is split and joined in an order that the sizes and
+ * the ids alone decide: no atomics touch a sum, and results do not depend on
+ * scheduling.  dtable must not overlap dy. */
+typedef struct {
+    int64_t m;             /* ids, 0..2^30                                            */
+    int32_t rows, c;       /* 0..2^31-1, 1..2^20                                      */
+    const void *ids;       /* [m] of ids_bits                                         */
+    const void *dy;        /* [m][c] of dy_dtype                                      */
+    int64_t dy_stride;
+    void *dtable;          /* [rows][c] of dtable_dtype                               */
+    int64_t dtable_stride;
+    float scale;
+    int32_t ids_bits;      /* 32 or 64                                                */
+    int32_t dy_dtype;      /* HG_F32, HG_F16 or HG_BF16                               */
+    int32_t dtable_dtype;  /* dy_dtype or HG_F32                                      */
+    int32_t accumulate;    /* 1: add to dtable                                        */
+} hg_embedding_grad;
+int hashgrid_embedding_backward_workspace_size(const hg_embedding_grad *op, size_t *bytes_out);
+int hashgrid_embedding_backward(const hg_embedding_grad *op, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Layer norm with the residual's addition:
+ *   s = x + r,  mu = mean over the row of s,  q = 1 / sqrt(mean of (s - mu)^2 + eps)
+ *   y = (s - mu) q w + b
+ * in fp32 between the loads and each output's one rounding; the variance is the
+ * mean square of the differences, not a difference of means.  8-bit rows and their
+ * scales, rows that are not finite and outputs in place of inputs: as
+ * hashgrid_rms_norm_forward. */
+typedef struct {
+    int64_t m;             /* rows, >= 0                                              */
+    int32_t c;             /* columns, 1..2^20                                        */
+    const void *x;         /* [m][c] of dtype                                         */
+    int64_t x_stride;
+    const void *residual;  /* r: [m][c] of dtype, or NULL                             */
+    int64_t residual_stride;
+    const float *w;        /* [c], or NULL: ones                                      */
+    const float *b;        /* [c], or NULL: zeros                                     */
+    void *y;               /* [m][c] of y_dtype, WRITTEN                              */
+    int64_t y_stride;
+    float *y_scale;        /* [m], HG_F8 only (else NULL), WRITTEN                    */
+    void *sum;             /* NULL, or [m][c] of dtype that receives s                */
+    int64_t sum_stride;
+    float *mean;           /* NULL, or [m] that receives mu                           */
+    float *rstd;           /* NULL, or [m] that receives q                            */
+    float eps;             /* >= 0                                                    */
+    int32_t dtype;         /* HG_F32, HG_F16 or HG_BF16                               */
+    int32_t y_dtype;       /* dtype or HG_F8                                          */
+} hg_layer_norm;
+int hashgrid_layer_norm_forward(const hg_layer_norm *op, void *stream);
+
+/* Backward of the layer norm for upstream dy = dL/dy and, where s goes on as the
+ * residual stream, ds = dL/ds, with h = (s - mu) q and g = w dy:
+ *   dx = q (g - mean(g) - h mean(g h)) + ds
+ *   dw = sum over rows of dy h,  db = sum over rows of dy
+ * dx is the gradient of x and of r alike.  dw and db are WRITTEN, or added to with
+ * accumulate (zero or unchanged with m == 0); their order of summation is fixed by
+ * the sizes.  dx may be dy, s or ds itself as in hashgrid_rms_norm_backward. */
+typedef struct {
+    int64_t m;
+    int32_t c;
+    const void *dy;        /* [m][c] of dtype                                         */
+    int64_t dy_stride;
+    const void *sum;       /* s: [m][c] of dtype                                      */
+    int64_t sum_stride;
+    const float *w;        /* [c], or NULL: ones                                      */
+    const float *mean;     /* mu: [m]                                                 */
+    const float *rstd;     /* q: [m]                                                  */
+    const void *ds;        /* NULL, or [m][c] of dtype                                */
+    int64_t ds_stride;
+    void *dx;              /* [m][c] of dtype, WRITTEN                                */
+    int64_t dx_stride;
+    float *dw;             /* NULL, or [c]                                            */
+    float *db;             /* NULL, or [c]                                            */
+    int32_t dtype;         /* HG_F32, HG_F16 or HG_BF16                               */
+    int32_t accumulate;    /* 1: add to dw and db                                     */
+} hg_layer_norm_grad;
+int hashgrid_layer_norm_backward_workspace_size(const hg_layer_norm_grad *op, size_t *bytes_out);
+int hashgrid_layer_norm_backward(const hg_layer_norm_grad *op, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Gated feed-forward: both projections, the activation and the product,
+ *   g = x Wg^T + bg,  u = x Wu^T + bu,  h = act(g) u
+ * or, with 8-bit operands, sums scaled before the bias as in
+ * hashgrid_linear_forward.  (SiLU makes the SwiGLU block, GELU the GeGLU, ReLU the
+ * ReGLU, none the bilinear one; the product back to the model's width is a
+ * hashgrid_linear_forward.)  g and u stay fp32 on the way to h, which is rounded
+ * once, as are gate and up where they are kept for the backward.  Where an
+ * activation is 0 at an infinite g, as SiLU's at -inf, its limit 0 is taken; the
+ * product with u is IEEE's. */
+typedef struct {
+    int64_t m;             /* rows, >= 0                                              */
+    int32_t k, n;          /* inputs and hidden units, 1..65536                       */
+    const void *x;         /* [m][k] of x_dtype                                       */
+    int64_t x_stride;
+    const void *wg;        /* [n][k] of x_dtype                                       */
+    int64_t wg_stride;
+    const void *wu;        /* [n][k] of x_dtype                                       */
+    int64_t wu_stride;
+    const float *x_scale;  /* [m], HG_F8 only (else NULL)                             */
+    const float *g_scale;  /* [n], HG_F8 only (else NULL)                             */
+    const float *u_scale;  /* [n], HG_F8 only (else NULL)                             */
+    const float *bg;       /* [n] or NULL                                             */
+    const float *bu;       /* [n] or NULL                                             */
+    void *h;               /* [m][n] of h_dtype, WRITTEN; overlaps no input           */
+    int64_t h_stride;
+    void *gate, *up;       /* both NULL, or [m][n] of x_dtype that receive g and u
+                              (HG_F16 and HG_BF16 only)                               */
+    int64_t gate_stride, up_stride;
+    int32_t x_dtype;       /* HG_F16, HG_BF16 or HG_F8                                */
+    int32_t h_dtype;       /* x_dtype or HG_F32; with HG_F8: HG_F16, HG_BF16, HG_F32  */
+    int32_t act;           /* HG_ACT_*                                                */
+} hg_gated;
+int hashgrid_gated_forward(const hg_gated *op, void *stream);
+
+/* Backward of hashgrid_gated_forward for upstream dh = dL/dh, from g and u as the
+ * forward left them:
+ *   dg = dh u act'(g),  du = dh act(g)
+ *   dx = dg Wg + du Wu,  dwg = dg^T x,  dwu = du^T x,  dbg, dbu = sums of dg, du
+ * dg and du are rounded to the operands' type where they enter a product; dbg and
+ * dbu sum them unrounded; sums are fp32, outputs are rounded once.  Where ReLU's g
+ * is not above 0, dg and du are 0 whatever dh and u hold.  The weights' and biases'
+ * gradients are WRITTEN, or added to with accumulate; with m == 0 they are zero (or
+ * unchanged).  The order of every sum is fixed by the sizes.  Row strides of dh,
+ * gate, up, x and dx are at most 2^22 (with one row they are not looked at).
+ * Outputs overlap no input. */
+typedef struct {
+    int64_t m;
+    int32_t k, n;
+    const void *dh;        /* [m][n] of dtype                                         */
+    int64_t dh_stride;
+    const void *gate, *up; /* [m][n] of dtype                                         */
+    int64_t gate_stride, up_stride;
+    const void *x;         /* [m][k] of dtype (needed for dwg, dwu)                   */
+    int64_t x_stride;
+    const void *wg, *wu;   /* [n][k] of dtype (needed for dx)                         */
+    int64_t wg_stride, wu_stride;
+    void *dx;              /* NULL, or [m][k] of dtype, WRITTEN                       */
+    int64_t dx_stride;
+    void *dwg, *dwu;       /* both NULL, or [n][k] of dw_dtype                        */
+    int64_t dwg_stride, dwu_stride;
+    float *dbg, *dbu;      /* both NULL, or [n]                                       */
+    int32_t dtype;         /* HG_F16 or HG_BF16                                       */
+    int32_t dw_dtype;      /* dtype or HG_F32                                         */
+    int32_t act;           /* HG_ACT_*                                                */
+    int32_t accumulate;    /* 1: add to dwg, dwu, dbg and dbu                         */
+} hg_gated_grad;
+int hashgrid_gated_backward_workspace_size(const hg_gated_grad *op, size_t *bytes_out);
+int hashgrid_gated_backward(const hg_gated_grad *op, void *workspace, size_t workspace_bytes, void *stream);
+
 /* Performance knobs (launch shapes).  Two change results within rounding:
  * HG_TUNE_FWD_LANES (the order in which the blend's eight terms are added) and
  * HG_TUNE_BWD_BINNED (fixed-point binned accumulation or fp32 atomics, whose

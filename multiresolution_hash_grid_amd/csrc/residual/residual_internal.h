@@ -1,5 +1,5 @@
-// Launch descriptions of the residual head's operators (linear, RMS norm,
-// AdamW), shared by their host side and their kernels.  Not part of the
+// Launch descriptions of the residual head's operators (linear, norms,
+// codes, gated blocks, AdamW), shared by their host side and their kernels.  Not part of the
 // public ABI (include/hashgrid.h is).
 #pragma once
 
@@ -38,6 +38,18 @@ hipError_t launch_linear_backward(const hg_linear_grad &op, void *workspace, hip
 hipError_t launch_rms_norm_forward(const hg_rms_norm &op, hipStream_t stream);
 size_t rms_norm_backward_bytes(const hg_rms_norm_grad &op);
 hipError_t launch_rms_norm_backward(const hg_rms_norm_grad &op, void *workspace, hipStream_t stream);
+
+hipError_t launch_layer_norm_forward(const hg_layer_norm &op, hipStream_t stream);
+size_t layer_norm_backward_bytes(const hg_layer_norm_grad &op);
+hipError_t launch_layer_norm_backward(const hg_layer_norm_grad &op, void *workspace, hipStream_t stream);
+
+hipError_t launch_embedding_forward(const hg_embedding &op, hipStream_t stream);
+size_t embedding_backward_bytes(const hg_embedding_grad &op);
+hipError_t launch_embedding_backward(const hg_embedding_grad &op, void *workspace, hipStream_t stream);
+
+hipError_t launch_gated_forward(const hg_gated &op, hipStream_t stream);
+size_t gated_backward_bytes(const hg_gated_grad &op);
+hipError_t launch_gated_backward(const hg_gated_grad &op, void *workspace, hipStream_t stream);
 
 // Tensors per launch: their descriptions travel in the kernel's arguments.
 constexpr int kAdamwTensors = 36;
