@@ -26,7 +26,8 @@ def gen(*key):
 
 SIZES = [(1, 1, 1), (1, 256, 512), (3, 7, 5), (16, 32, 16), (17, 33, 19), (64, 64, 4), (65, 35, 64), (127, 31, 129), (130, 256, 256),
          (257, 96, 33), (1000, 130, 70), (300, 520, 300), (40, 1024, 512), (33, 8, 1024), (5000, 35, 93), (4100, 64, 40),
-         (2500, 256, 100), (2048, 384, 200), (1030, 640, 260)]
+         (2500, 256, 100), (2048, 384, 200), (1030, 640, 260), (1100, 32, 1300), (1300, 64, 700), (2100, 96, 450), (1025, 120, 300),
+         (1200, 192, 170), (3000, 250, 300)]
 
 
 @pytest.mark.parametrize("m,k,n", SIZES)
