@@ -1,0 +1,22 @@
+// How a gated block's backward is cut.
+#pragma once
+
+#include "gated_common.h"
+
+namespace hg {
+namespace res {
+
+// The weights' gradients: tiles of `units` hidden units (gate and up) by kt inputs,
+// ny x nz of them, each with `parts` workgroups over the rows.  dx: tiles of 256 rows
+// by kp * 32 inputs.
+struct GatedGradPlan {
+    int units, kt, ny, nz, parts, kp;
+    size_t bytes;
+};
+constexpr int kGateRows = 64;  // of a step
+
+hipError_t gated_grad_f16(const GatedGradArgs &a, const GatedGradPlan &p, float *part, hipStream_t stream);
+hipError_t gated_grad_bf16(const GatedGradArgs &a, const GatedGradPlan &p, float *part, hipStream_t stream);
+
+}  // namespace res
+}  // namespace hg

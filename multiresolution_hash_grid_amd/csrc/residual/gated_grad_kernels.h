@@ -1,0 +1,484 @@
+// Backward of h = act(x Wg^T + bg) (x Wu^T + bu) on the matrix cores; the sources
+// that include this instantiate one operand type each.
+//
+//   dg = dh u act'(g),  du = dh act(g)
+//   dx = dg Wg + du Wu,  dwg = dg^T x,  dwu = du^T x,  dbg, dbu = sums over the rows
+//
+// Two kernels read dh, g and u and each works dg and du out for itself, on their way
+// into a product: written once and read twice they would cost as many bytes, and a
+// workspace of two hidden layers.  They are rounded to the operands' type there, as
+// products of 16-bit operands need; the biases' gradients sum them unrounded.
+#pragma once
+
+#include "gated_grad.h"
+#include "grad_tiles.h"
+
+namespace hg {
+namespace res {
+namespace {
+
+constexpr int kGateThreads = 512;
+
+// Pieces of dh, g and u, and what becomes of them.
+struct RawGate {
+    u32x4 dh, g, u;
+};
+template <typename T>
+__device__ __forceinline__ void values(u32x4 v, float (&f)[8]) {
+    typedef T T8 __attribute__((ext_vector_type(8)));
+    const T8 t = __builtin_bit_cast(T8, v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = (float)t[j];
+}
+template <bool kShort, typename T>
+__device__ __forceinline__ RawGate load_gate(const GatedGradArgs &a, int64_t dh, int64_t g, int64_t u, Columns c) {
+    return {load_columns<kShort>((const T *)a.dh + dh, c, a.n), load_columns<kShort>((const T *)a.gate + g, c, a.n),
+            load_columns<kShort>((const T *)a.up + u, c, a.n)};
+}
+template <typename T>
+__device__ __forceinline__ void gate_of(const RawGate &raw, int act, float (&dg)[8], float (&du)[8]) {
+    float g[8], u[8], dh[8];
+    values<T>(raw.g, g);
+    values<T>(raw.u, u);
+    values<T>(raw.dh, dh);
+    gate_grad_all(g, u, dh, act, dg, du);
+}
+
+// This wave's LDS accesses are done, and so are the others'.
+__device__ __forceinline__ void step_barrier() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+// dx of 256 rows by KP * 32 inputs a workgroup.  A wave has 32 rows and all of the
+// tile's inputs: the sums lie in its registers while the hidden units come by, 32 at
+// a time.  Their dh, g and u come straight from memory as fragments (a lane has 8
+// units of one row) and become fragments of dg and du in place; the units' rows of
+// Wg and Wu lie in LDS, the next units' on their way into registers, and are read
+// transposed.  Their columns are dealt so that a lane ends with 8 consecutive inputs
+// of a row.
+// One barrier a stretch of units.  Between two of them waves 0 - 3 multiply first and
+// then work out the next dg and du, the others the other way around: of the two waves
+// of a SIMD one multiplies while the other computes.
+// Both kinds of loads, weights and units, are asked for a stretch ahead and
+// unconditionally (past the end they repeat others): the two orders are loops of
+// their own and without branches around loads, so that the compiler can count those
+// in flight and a wait for the older kind leaves the younger on its way.
+// kShort: rows of units or inputs may be shorter than a piece.
+template <typename T, int KP, bool kShort>
+__global__ __launch_bounds__(kGateThreads) void gated_dx_kernel(const GatedGradArgs a, int tiles_k, int64_t tiles_m) {
+    extern __shared__ __attribute__((aligned(16))) char lds[];
+    constexpr int C = KP * 32, kHalf = 32 * C * 2, kBuffer = 2 * kHalf, kPer = C / 64;  // pieces of a thread
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), row16 = lane & 15, group = lane >> 4;
+    // workgroups b, b + 8, ... share an XCD: the tiles of the same rows do
+    const int xcd = blockIdx.x & 7, in_xcd = blockIdx.x >> 3;
+    const int k0 = in_xcd % tiles_k * C;
+    const int64_t walker = (int64_t)(in_xcd / tiles_k) * 8 + xcd, walkers = (int64_t)(gridDim.x >> 3) / tiles_k * 8;
+    if (walker >= tiles_m) return;
+    const int chunks = (a.n + 31) / 32;
+    const int64_t all = ((tiles_m - 1 - walker) / walkers + 1) * chunks;
+
+    auto thread = [] {  // where this thread's pieces lie is worked out anew each time: held, it would cost registers
+        int t = threadIdx.x;
+        asm volatile("" : "+v"(t));
+        return t;
+    };
+    u32x4 staged[kPer];
+    int ahead = 0;  // the units whose weights are fetched next
+    auto fetch = [&]() __attribute__((always_inline)) {
+        const int t = thread();
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+            const int i = t + j * kGateThreads, half = i / (32 * C / 8), unit = ahead * 32 + i / (C / 8) % 32;
+            const Columns c = columns_of(k0 + i % (C / 8) * 8, a.k);
+            const T *const w = half ? (const T *)a.wu + (int64_t)(unit < a.n ? unit : 0) * a.us : (const T *)a.wg + (int64_t)(unit < a.n ? unit : 0) * a.gs;
+            staged[j] = load_columns<kShort>(w + c.at, c, a.k);
+        }
+        ahead = ahead + 1 < chunks ? ahead + 1 : 0;
+    };
+    auto stage = [&](char *to, int chunk) __attribute__((always_inline)) {
+        const int t = thread();
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+            const int i = t + j * kGateThreads, half = i / (32 * C / 8), row = i / (C / 8) % 32, piece = i % (C / 8);
+            const Columns c = columns_of(k0 + piece * 8, a.k);
+            u32x4 v = shifted(staged[j], c.drop & 7);
+            if (c.drop >= 8 || chunk * 32 + row >= a.n) v = u32x4{0, 0, 0, 0};
+            // columns 8 b .. + 3 of 32 are columns 4 b .. of the pair's first fragment, the next four of its second
+            char *const tile = to + half * kHalf;
+            const int s = piece >> 2, b = piece & 3;
+            *(u32x2 *)(tile + tile_at<C>(row, s * 4 + (b >> 1)) + (b & 1) * 8) = u32x2{v[0], v[1]};
+            *(u32x2 *)(tile + tile_at<C>(row, s * 4 + 2 + (b >> 1)) + (b & 1) * 8) = u32x2{v[2], v[3]};
+        }
+    };
+
+    RawGate raw[2];
+    u32x4 dz[2][2];  // gate and up, row fragments
+    int64_t raw_m = walker * 256 + wave * 32 + row16;
+    int raw_chunk = 0;
+    auto load = [&]() __attribute__((always_inline)) {  // the units after the last loaded ones
+        const Columns c = columns_of(raw_chunk * 32 + group * 8, a.n);
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int64_t m = raw_m + r * 16 < a.m ? raw_m + r * 16 : a.m - 1;
+            raw[r] = load_gate<kShort, T>(a, m * a.dhs + c.at, m * a.ps + c.at, m * a.qs + c.at, c);
+        }
+        raw_m += raw_chunk + 1 < chunks ? 0 : walkers * 256;
+        raw_chunk = raw_chunk + 1 < chunks ? raw_chunk + 1 : 0;
+    };
+    auto derive = [&](int chunk) __attribute__((always_inline)) {
+        const int drop = columns_of(chunk * 32 + group * 8, a.n).drop;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            float dg[8], du[8];
+            gate_of<T>(raw[r], a.act, dg, du);
+            dz[0][r] = shifted(pack8<T>(dg), drop & 7);
+            dz[1][r] = shifted(pack8<T>(du), drop & 7);
+            if (drop >= 8) dz[0][r] = dz[1][r] = u32x4{0, 0, 0, 0};
+        }
+    };
+
+    f32x4 acc[KP][2][2];  // pairs, fragments of a pair, row fragments
+    int64_t m0 = walker * 256 + wave * 32 + row16;
+    auto walk = [&](auto late) __attribute__((always_inline)) {
+        constexpr bool kLate = decltype(late)::value;
+        fetch();
+        stage(lds, 0);
+        fetch();
+        load();
+        if constexpr (!kLate) {
+            derive(0);
+            load();
+        }
+        int chunk = 0;
+        for (int64_t q = 0; q < all; ++q) {
+            step_barrier();  // these units' weights are in their buffer, and the last ones are done with
+            const int next = chunk + 1 < chunks ? chunk + 1 : 0;
+            stage(lds + ((q + 1) & 1) * kBuffer, next);
+            fetch();
+            if constexpr (kLate) {
+                derive(chunk);
+                load();
+            }
+            if (chunk == 0)
+#pragma unroll
+                for (int p = 0; p < KP; ++p)
+#pragma unroll
+                    for (int f = 0; f < 2; ++f) acc[p][f][0] = acc[p][f][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+            char *const buffer = lds + (q & 1) * kBuffer;
+            const int l = thread() & 63;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int p = 0; p < KP; ++p) {
+#pragma unroll
+                    for (int f = 0; f < 2; ++f) {
+                        const u32x4 w = tile_columns<C>(buffer + h * kHalf, 0, p * 2 + f, l);
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) acc[p][f][r] = mma<T>(w, dz[h][r], acc[p][f][r]);
+                    }
+                }
+            if (next == 0) {
+#pragma unroll
+                for (int p = 0; p < KP; ++p) {
+                    const int k = k0 + p * 32 + group * 8, left = a.k - k;
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        float v[8];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) v[j] = acc[p][j / 4][r][j % 4];
+                        if (m0 + r * 16 < a.m) put((T *)a.dx + (m0 + r * 16) * a.dxs + k, left, rounded<8, T>(v));
+                    }
+                }
+                m0 += walkers * 256;
+            }
+            if constexpr (!kLate) {
+                derive(next);
+                load();
+            }
+            chunk = next;
+        }
+    };
+    if (wave >= 4) walk(std::true_type{});
+    else walk(std::false_type{});
+}
+
+// Four values of dW, slots k .. k + 3 of slot n of a tile's 2 U (gate, then up),
+// rounded once.
+template <typename T, int U>
+__device__ __forceinline__ void put_gate_dw(const GatedGradArgs &a, int n0, int n, int k, f32x4 t) {
+    const bool up = n >= U;
+    const int row = column_of(n0 + n - (up ? U : 0), a.n);
+    if (row < 0) return;
+    auto into = [&](auto *w) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int c = column_of(k + j, a.k);
+            if (c >= 0) w[c] = (std::remove_reference_t<decltype(*w)>)(a.accumulate ? (float)w[c] + t[j] : t[j]);
+        }
+    };
+    void *const to = up ? a.dwu : a.dwg;
+    const int64_t stride = up ? a.dus : a.dgs;
+    if (a.dw_f32) into((float *)to + (int64_t)row * stride);
+    else into((T *)to + (int64_t)row * stride);
+}
+template <int U>
+__device__ __forceinline__ void put_gate_db(const GatedGradArgs &a, int n0, int n, float t) {
+    const bool up = n >= U;
+    const int c = column_of(n0 + n - (up ? U : 0), a.n);
+    float *const to = up ? a.dbu : a.dbg;
+    if (c >= 0) to[c] = a.accumulate ? to[c] + t : t;
+}
+
+// dW of U hidden units (2 U rows of gate and up) by KT inputs, and the biases'
+// gradients, over a share of the rows, 64 a step.  Each thread turns the pieces of
+// dh, g and u that it loaded a step ahead into dg and du, adds its columns up for
+// the biases, and lays them and x into LDS tiles, one of two sets; then each wave
+// adds the step's product to its part of dW, which stays in registers to the end
+// (4 x 2 waves over 2 U x KT).  Both operands are read transposed.  Between two
+// barriers waves 0 - 3 multiply this step first and prepare the next one then, the
+// others the other way around.  dW and db leave as one partial per workgroup, joined
+// in a fixed order by gated_join_kernel; a workgroup alone with its tile writes them
+// itself.
+template <typename T, int U, int KT, bool kShort>
+__global__ __launch_bounds__(kGateThreads) void gated_dw_kernel(const GatedGradArgs a, float *part) {
+    constexpr int R = kGateRows, NT = 2 * U, FN = NT / 64, FK = KT / 32;  // fragments of a wave
+    constexpr int PN = U / 8, PK = KT / 8;                               // pieces of a row
+    constexpr int LN = R * PN / kGateThreads, LK = R * PK / kGateThreads;  // pieces of a thread
+    constexpr int kBuffer = R * (NT + KT) * 2;
+    extern __shared__ __attribute__((aligned(16))) char lds[];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wn = wave >> 1, wk = wave & 1;
+    // (the two waves of a SIMD are a wave and the one four on)
+    const bool late = wave >= 4;
+    const int n0 = blockIdx.y * U, k0 = blockIdx.z * KT;
+    auto thread = [] {  // where this thread's pieces lie is worked out anew in every step
+        int t = threadIdx.x;
+        asm volatile("" : "+v"(t));
+        return t;
+    };
+
+    f32x4 acc[FN][FK];
+#pragma unroll
+    for (int i = 0; i < FN; ++i)
+#pragma unroll
+        for (int j = 0; j < FK; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    float dbg[8] = {}, dbu[8] = {};
+    RawGate raw[LN];
+    u32x4 nx[LK];
+    // Addresses: a uniform base for the step and i, and this thread's 32-bit offset
+    // of its row and column in a step (row strides are below 2^22).
+    auto fetch = [&](int64_t step) __attribute__((always_inline)) {
+        const int t = thread();
+        const Columns cn = columns_of(n0 + t % PN * 8, a.n), ck = columns_of(k0 + t % PK * 8, a.k);
+        const int64_t m = step * R;
+        const int last = a.m - m < R ? (int)(a.m - m) - 1 : R - 1;  // rows past the end read the last one
+#pragma unroll
+        for (int i = 0; i < LN; ++i) {
+            const int at = t / PN + i * (kGateThreads / PN), r = at < last ? at : last;
+            raw[i] = load_gate<kShort, T>(a, m * a.dhs + (uint32_t)(r * (int)a.dhs + cn.at), m * a.ps + (uint32_t)(r * (int)a.ps + cn.at),
+                                  m * a.qs + (uint32_t)(r * (int)a.qs + cn.at), cn);
+        }
+        if (a.dwg)
+#pragma unroll
+            for (int i = 0; i < LK; ++i) {
+                const int at = t / PK + i * (kGateThreads / PK), r = at < last ? at : last;
+                nx[i] = load_columns<kShort>((const T *)a.x + m * a.xs + (uint32_t)(r * (int)a.xs + ck.at), ck, a.k);
+            }
+    };
+    auto prepare = [&](int64_t step, char *dzt) __attribute__((always_inline)) {
+        char *const xt = dzt + R * NT * 2;
+        const int t = thread();
+        const Columns cn = columns_of(n0 + t % PN * 8, a.n), ck = columns_of(k0 + t % PK * 8, a.k);
+        const bool whole = (step + 1) * R <= a.m;
+        if (a.dwg)
+#pragma unroll
+            for (int i = 0; i < LK; ++i) {
+                const int r = t / PK + i * (kGateThreads / PK);
+                u32x4 v = nx[i];
+                if (ck.drop > 0)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) v[j] &= 2 * j >= ck.drop ? ~0u : 2 * j + 1 >= ck.drop ? 0xFFFF0000u : 0u;
+                if (!whole && step * R + r >= a.m) v = u32x4{0, 0, 0, 0};
+                *(u32x4 *)(xt + tile_at<KT>(r, t % PK)) = v;
+            }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < LN; ++i) {
+            const int r = t / PN + i * (kGateThreads / PN);
+            float dg[8], du[8];
+            gate_of<T>(raw[i], a.act, dg, du);
+            const int drop = whole || step * R + r < a.m ? cn.drop : 8;
+            if (drop > 0)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) dg[j] = j < drop ? 0.f : dg[j], du[j] = j < drop ? 0.f : du[j];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) dbg[j] += dg[j], dbu[j] += du[j];
+            *(u32x4 *)(dzt + tile_at<NT>(r, t % PN)) = pack8<T>(dg);
+            *(u32x4 *)(dzt + tile_at<NT>(r, PN + t % PN)) = pack8<T>(du);
+            __builtin_amdgcn_sched_barrier(0);  // one piece's values at a time: the registers hold no more
+        }
+    };
+
+    const int64_t steps = (a.m + R - 1) / R, by = gridDim.x;
+    if (blockIdx.x < steps) {
+        fetch(blockIdx.x);
+        prepare(blockIdx.x, lds);
+        if (blockIdx.x + by < steps) fetch(blockIdx.x + by);
+    }
+    int turn = 0;
+    for (int64_t step = blockIdx.x; step < steps; step += by, turn ^= 1) {
+        step_barrier();  // this step's tiles are whole, and the last step's are done with
+        auto ahead = [&]() __attribute__((always_inline)) {
+            if (step + by >= steps) return;
+            prepare(step + by, lds + (turn ^ 1) * kBuffer);
+            if (step + 2 * by < steps) fetch(step + 2 * by);
+        };
+        if (late) ahead();
+        if (a.dwg) {
+            char *const dzt = lds + turn * kBuffer, *const xt = dzt + R * NT * 2;
+            const int l = thread() & 63;
+#pragma unroll
+            for (int m = 0; m < R; m += 32) {
+                u32x4 dzf[FN];
+#pragma unroll
+                for (int i = 0; i < FN; ++i) dzf[i] = tile_columns<NT>(dzt, m, wn * FN + i, l);
+#pragma unroll
+                for (int j = 0; j < FK; ++j) {
+                    const u32x4 xf = tile_columns<KT>(xt, m, wk * FK + j, l);
+#pragma unroll
+                    for (int i = 0; i < FN; ++i) acc[i][j] = mma<T>(xf, dzf[i], acc[i][j]);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+        if (!late) ahead();
+    }
+
+    // Partials: dW as fragments, [tile][workgroup][NT x KT], then db, [unit tile][workgroup][NT].
+    const int tile = blockIdx.y * gridDim.z + blockIdx.z;
+    const bool alone = gridDim.x == 1;
+    if (a.dwg) {
+        float *p = part + ((int64_t)tile * gridDim.x + blockIdx.x) * (NT * KT);
+#pragma unroll
+        for (int i = 0; i < FN; ++i)
+#pragma unroll
+            for (int j = 0; j < FK; ++j) {
+                const int fn = wn * FN + i, fk = wk * FK + j;
+                if (alone) put_gate_dw<T, U>(a, n0, fn * 16 + (lane & 15), k0 + fk * 16 + (lane >> 4) * 4, acc[i][j]);
+                else *(f32x4 *)(p + (fn * (KT / 16) + fk) * 256 + lane * 4) = acc[i][j];
+            }
+    }
+    if (a.dbg && blockIdx.z == 0) {
+        float *const sums = (float *)lds;  // [512 / PN][U], for the gate and then for up
+        float *p = part + (a.dwg ? (int64_t)gridDim.y * gridDim.z * gridDim.x * (NT * KT) : 0) +
+                   ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * NT;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sums[threadIdx.x * 8 + j] = half ? dbu[j] : dbg[j];
+            __syncthreads();
+            for (int n = threadIdx.x; n < U; n += kGateThreads) {
+                float t = 0.f;
+                for (int r = 0; r < kGateThreads / PN; ++r) t += sums[r * U + n];
+                if (alone) put_gate_db<U>(a, n0, half * U + n, t);
+                else p[half * U + n] = t;
+            }
+        }
+    }
+}
+
+// dW = (dW +) the partials' sum, rounded once; db alike.  A workgroup takes 16
+// groups of four values; 32 threads share the partials of each, and their sums
+// are added in order, eight and then four.
+template <typename T, int U>
+__global__ __launch_bounds__(512) void gated_join_kernel(const float *part, int parts, int kt, int ny, int nz, GatedGradArgs a) {
+    __shared__ f32x4 lds[32][16];
+    constexpr int NT = 2 * U;
+    const int slot = threadIdx.x & 15, share = threadIdx.x >> 4;
+    const int64_t quads = a.dwg ? (int64_t)ny * nz * NT * kt / 4 : 0, all = quads + (a.dbg ? ny * NT / 4 : 0);
+    const int64_t q = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 16 + slot;
+    const int64_t per = q < quads ? NT * kt / 4 : NT / 4;      // quads of a partial
+    const int64_t local = q < quads ? q : q - quads;
+    const float *p = part + (q < quads ? 0 : quads * 4 * parts) + (local / per * per * parts + local % per) * 4;
+    f32x4 t = {0.f, 0.f, 0.f, 0.f};
+    if (q < all)
+#pragma unroll 8
+        for (int i = share; i < parts; i += 32) t += *(const f32x4 *)(p + i * per * 4);
+    lds[share][slot] = t;
+    __syncthreads();
+    if (share < 4) {
+        t = lds[share * 8][slot];
+#pragma unroll
+        for (int i = 1; i < 8; ++i) t += lds[share * 8 + i][slot];
+    }
+    __syncthreads();
+    if (share < 4) lds[share][slot] = t;
+    __syncthreads();
+    if (share || q >= all) return;
+    for (int i = 1; i < 4; ++i) t += lds[i][slot];
+    const int tile = (int)(local / per), e = (int)(local % per);
+    if (q < quads) {
+        const int frag = e / 64, l = e % 64;
+        put_gate_dw<T, U>(a, tile / nz * U, frag / (kt / 16) * 16 + (l & 15), tile % nz * kt + frag % (kt / 16) * 16 + (l >> 4) * 4, t);
+    } else {
+        for (int j = 0; j < 4; ++j) put_gate_db<U>(a, tile * U, e * 4 + j, t[j]);
+    }
+}
+
+template <typename T, int KP, bool kShort = false>
+hipError_t gated_dx_launch(const GatedGradArgs &a, hipStream_t stream) {
+    const auto kernel = gated_dx_kernel<T, KP, kShort>;
+    const int bytes = 2 * 2 * 32 * KP * 32 * 2, tiles_k = (int)div_up(a.k, KP * 32);
+    if (bytes > 65536) {
+        const hipError_t e = hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e != hipSuccess) return e;
+    }
+    const int64_t tiles_m = div_up(a.m, 256);
+    int64_t walkers = kCus / tiles_k < tiles_m ? kCus / tiles_k : tiles_m;
+    walkers = div_up(walkers < 1 ? 1 : walkers, 8) * 8;  // whole rounds over the XCDs
+    kernel<<<dim3((unsigned)(walkers * tiles_k)), kGateThreads, bytes, stream>>>(a, tiles_k, tiles_m);
+    return hipGetLastError();
+}
+
+template <typename T, int U, int KT, bool kShort = false>
+hipError_t gated_dw_launch(const GatedGradArgs &a, const GatedGradPlan &p, float *part, hipStream_t stream) {
+    const auto kernel = gated_dw_kernel<T, U, KT, kShort>;
+    const int bytes = 2 * kGateRows * (2 * U + KT) * 2;
+    if (bytes > 65536) {
+        const hipError_t e = hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e != hipSuccess) return e;
+    }
+    kernel<<<dim3((unsigned)p.parts, (unsigned)p.ny, (unsigned)p.nz), kGateThreads, bytes, stream>>>(a, part);
+    return hipGetLastError();
+}
+
+template <typename T>
+hipError_t gated_grad_run(const GatedGradArgs &a, const GatedGradPlan &p, float *part, hipStream_t stream) {
+    hipError_t e = hipSuccess;
+    if (a.m > 0 && (a.dwg || a.dbg)) {
+        if (a.n < 8 || a.k < 8) e = gated_dw_launch<T, 64, 64, true>(a, p, part, stream);
+        else if (p.units == 128) e = p.kt == 64 ? gated_dw_launch<T, 128, 64>(a, p, part, stream)
+                              : p.kt == 128 ? gated_dw_launch<T, 128, 128>(a, p, part, stream)
+                                            : gated_dw_launch<T, 128, 256>(a, p, part, stream);
+        else e = p.kt == 64 ? gated_dw_launch<T, 64, 64>(a, p, part, stream)
+               : p.kt == 128 ? gated_dw_launch<T, 64, 128>(a, p, part, stream)
+                             : gated_dw_launch<T, 64, 256>(a, p, part, stream);
+        if (e != hipSuccess) return e;
+    }
+    if ((a.dwg || a.dbg) && !(a.m > 0 && p.parts == 1)) {
+        const int64_t quads = (a.dwg ? (int64_t)p.ny * p.nz * 2 * p.units * p.kt : 0) / 4 + (a.dbg ? p.ny * p.units / 2 : 0);
+        const int parts = a.m > 0 ? p.parts : 0;
+        if (p.units == 128) gated_join_kernel<T, 128><<<grid_of(div_up(quads, 16)), 512, 0, stream>>>(part, parts, p.kt, p.ny, p.nz, a);
+        else gated_join_kernel<T, 64><<<grid_of(div_up(quads, 16)), 512, 0, stream>>>(part, parts, p.kt, p.ny, p.nz, a);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    if (!a.dx || a.m == 0) return hipSuccess;
+    if (a.n < 8 || a.k < 8) return gated_dx_launch<T, 2, true>(a, stream);
+    return p.kp == 2 ? gated_dx_launch<T, 2>(a, stream) : p.kp == 4 ? gated_dx_launch<T, 4>(a, stream) : gated_dx_launch<T, 8>(a, stream);
+}
+
+}  // namespace
+}  // namespace res
+}  // namespace hg

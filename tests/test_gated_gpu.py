@@ -226,7 +226,8 @@ def test_refusals_of_the_binding():
         with pytest.raises(ValueError):
             call()
     with pytest.raises(hg.HashGridError, match="workspace"):
-        hg.hashgrid_gated_backward(h, x, w, w, h, h, workspace=None)
+        xs, hs = x.repeat(100, 1), h.repeat(100, 1)
+        hg.hashgrid_gated_backward(hs, xs, w, w, hs, hs, workspace=None)
     with pytest.raises(hg.HashGridError, match="together"):
         R_ = torch.empty(6, 8, device=DEV)
         hg.blocks._check(hg.blocks._lib().hashgrid_gated_backward(hg.blocks._gated_grad(
