@@ -13,12 +13,12 @@ GatedGradPlan plan_of(const hg_gated_grad &op) {
     if (op.n < 8 || op.k < 8) p.units = p.kt = 64;  // rows shorter than a piece take the narrowest tiles
     p.kp = p.kt / 32;
     p.ny = (int)div_up(op.n, p.units), p.nz = (int)div_up(op.k, p.kt);
-    if (!op.dwg) p.nz = 1;  // the biases' gradients need one column of tiles
     // One workgroup a CU over all tiles, and no more than there are steps.
-    const int64_t steps = div_up(op.m, kGateRows);
+    const int64_t steps = div_up(op.m, gate_rows(p.units, p.kt));
     int64_t parts = kCus / (p.ny * p.nz);
     if (parts > steps) parts = steps;
     p.parts = (int)(parts < 1 ? 1 : parts);
+    if (!op.dwg) p.nz = 1;  // the biases' gradients need one column of tiles
     const size_t tile = 2 * (size_t)p.units;
     if (op.m > 0 && p.parts > 1)
         p.bytes = ((op.dwg ? (size_t)p.ny * p.nz * tile * p.kt : 0) + (op.dbg ? (size_t)p.ny * tile : 0)) * p.parts * sizeof(float);

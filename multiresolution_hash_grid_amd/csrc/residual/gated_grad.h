@@ -13,7 +13,8 @@ struct GatedGradPlan {
     int units, kt, ny, nz, parts, kp;
     size_t bytes;
 };
-constexpr int kGateRows = 64;  // of a step
+// Rows of a step: the widest tile's sums leave registers for the pieces of 32.
+constexpr int gate_rows(int units, int kt) { return units == 128 && kt == 256 ? 32 : 64; }
 
 hipError_t gated_grad_f16(const GatedGradArgs &a, const GatedGradPlan &p, float *part, hipStream_t stream);
 hipError_t gated_grad_bf16(const GatedGradArgs &a, const GatedGradPlan &p, float *part, hipStream_t stream);

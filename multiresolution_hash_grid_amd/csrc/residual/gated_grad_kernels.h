@@ -44,6 +44,25 @@ __device__ __forceinline__ void gate_of(const RawGate &raw, int act, float (&dg)
     gate_grad_all(g, u, dh, act, dg, du);
 }
 
+// The first `left` values of a piece.
+template <typename T>
+__device__ __forceinline__ void put_piece(T *p, int left, u32x4 v) {
+    if (left >= 8) {
+        store_loose(p, v);
+        return;
+    }
+    if (left <= 0) return;
+    if (left & 4) {
+        store_loose(p, u32x2{v[0], v[1]});
+        v[0] = v[2], v[1] = v[3], p += 4;
+    }
+    if (left & 2) {
+        store_loose(p, v[0]);
+        v[0] = v[1], p += 2;
+    }
+    if (left & 1) store_loose(p, (uint16_t)v[0]);
+}
+
 // This wave's LDS accesses are done, and so are the others'.
 __device__ __forceinline__ void step_barrier() {
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
@@ -84,32 +103,46 @@ __global__ __launch_bounds__(kGateThreads) void gated_dx_kernel(const GatedGradA
         asm volatile("" : "+v"(t));
         return t;
     };
+    // This thread's pieces of a stretch's weights: one column, rows kStep apart of the
+    // gate's 32 and then of up's.
+    constexpr int kRow = C / 8, kStep = kGateThreads / kRow;
     u32x4 staged[kPer];
     int ahead = 0;  // the units whose weights are fetched next
     auto fetch = [&]() __attribute__((always_inline)) {
-        const int t = thread();
+        const int t = thread(), room = a.n - 1 - ahead * 32;
+        const Columns c = columns_of(k0 + t % kRow * 8, a.k);
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
-            const int i = t + j * kGateThreads, half = i / (32 * C / 8), unit = ahead * 32 + i / (C / 8) % 32;
-            const Columns c = columns_of(k0 + i % (C / 8) * 8, a.k);
-            const T *const w = half ? (const T *)a.wu + (int64_t)(unit < a.n ? unit : 0) * a.us : (const T *)a.wg + (int64_t)(unit < a.n ? unit : 0) * a.gs;
+            const int at = kPer == 1 ? t / kRow : j * kStep % 32 + t / kRow, row = kPer == 1 ? at & 31 : at;
+            const bool up = kPer == 1 ? at >= 32 : j * kStep >= 32;
+            const T *const w = (const T *)(up ? a.wu : a.wg) + (int64_t)(ahead * 32 + (row < room ? row : room)) * (up ? a.us : a.gs);
             staged[j] = load_columns<kShort>(w + c.at, c, a.k);
         }
         ahead = ahead + 1 < chunks ? ahead + 1 : 0;
     };
+    // (Columns past k become inputs that are not stored; units past n must be zero.)
     auto stage = [&](char *to, int chunk) __attribute__((always_inline)) {
-        const int t = thread();
+        const int t = thread(), piece = t % kRow;
+        if (a.k % 8) {
+            const int drop = columns_of(k0 + piece * 8, a.k).drop;
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) staged[j] = shifted(staged[j], drop & 7);
+        }
+        const int room = a.n - chunk * 32;
+        if (room < 32)
+#pragma unroll
+            for (int j = 0; j < kPer; ++j)
+                if (((kPer == 1 ? 0 : j * kStep % 32) + t / kRow) % 32 >= room) staged[j] = u32x4{0, 0, 0, 0};
+        // columns 8 b .. + 3 of 32 are columns 4 b .. of the pair's first fragment, the next four of its second;
+        // rows 16 apart lie alike
+        const int at = t / kRow, first = (piece >> 2) * 4 + ((piece & 3) >> 1);
+        char *const lo = to + (kPer == 1 ? (at >> 5) * kHalf : 0) + tile_at<C>(at & 31, first) + (piece & 1) * 8;
+        char *const hi = to + (kPer == 1 ? (at >> 5) * kHalf : 0) + tile_at<C>(at & 31, first + 2) + (piece & 1) * 8;
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
-            const int i = t + j * kGateThreads, half = i / (32 * C / 8), row = i / (C / 8) % 32, piece = i % (C / 8);
-            const Columns c = columns_of(k0 + piece * 8, a.k);
-            u32x4 v = shifted(staged[j], c.drop & 7);
-            if (c.drop >= 8 || chunk * 32 + row >= a.n) v = u32x4{0, 0, 0, 0};
-            // columns 8 b .. + 3 of 32 are columns 4 b .. of the pair's first fragment, the next four of its second
-            char *const tile = to + half * kHalf;
-            const int s = piece >> 2, b = piece & 3;
-            *(u32x2 *)(tile + tile_at<C>(row, s * 4 + (b >> 1)) + (b & 1) * 8) = u32x2{v[0], v[1]};
-            *(u32x2 *)(tile + tile_at<C>(row, s * 4 + 2 + (b >> 1)) + (b & 1) * 8) = u32x2{v[2], v[3]};
+            const int skip = j * kStep / 32 * kHalf + j * kStep % 32 * (C * 2);
+            *(u32x2 *)(lo + skip) = u32x2{staged[j][0], staged[j][1]};
+            *(u32x2 *)(hi + skip) = u32x2{staged[j][2], staged[j][3]};
         }
     };
 
@@ -128,14 +161,19 @@ __global__ __launch_bounds__(kGateThreads) void gated_dx_kernel(const GatedGradA
         raw_chunk = raw_chunk + 1 < chunks ? raw_chunk + 1 : 0;
     };
     auto derive = [&](int chunk) __attribute__((always_inline)) {
-        const int drop = columns_of(chunk * 32 + group * 8, a.n).drop;
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             float dg[8], du[8];
             gate_of<T>(raw[r], a.act, dg, du);
-            dz[0][r] = shifted(pack8<T>(dg), drop & 7);
-            dz[1][r] = shifted(pack8<T>(du), drop & 7);
-            if (drop >= 8) dz[0][r] = dz[1][r] = u32x4{0, 0, 0, 0};
+            dz[0][r] = pack8<T>(dg);
+            dz[1][r] = pack8<T>(du);
+        }
+        if (chunk * 32 + 32 > a.n) {  // pieces that the rows' end cuts, and those past it
+            const int drop = columns_of(chunk * 32 + group * 8, a.n).drop;
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) dz[h][r] = drop >= 8 ? u32x4{0, 0, 0, 0} : shifted(dz[h][r], drop);
         }
     };
 
@@ -188,7 +226,7 @@ __global__ __launch_bounds__(kGateThreads) void gated_dx_kernel(const GatedGradA
                         float v[8];
 #pragma unroll
                         for (int j = 0; j < 8; ++j) v[j] = acc[p][j / 4][r][j % 4];
-                        if (m0 + r * 16 < a.m) put((T *)a.dx + (m0 + r * 16) * a.dxs + k, left, rounded<8, T>(v));
+                        if (m0 + r * 16 < a.m) put_piece((T *)a.dx + (m0 + r * 16) * a.dxs + k, left, pack8<T>(v));
                     }
                 }
                 m0 += walkers * 256;
@@ -232,7 +270,7 @@ __device__ __forceinline__ void put_gate_db(const GatedGradArgs &a, int n0, int 
 }
 
 // dW of U hidden units (2 U rows of gate and up) by KT inputs, and the biases'
-// gradients, over a share of the rows, 64 a step.  Each thread turns the pieces of
+// gradients, over a share of the rows, 64 or 32 a step.  Each thread turns the pieces of
 // dh, g and u that it loaded a step ahead into dg and du, adds its columns up for
 // the biases, and lays them and x into LDS tiles, one of two sets; then each wave
 // adds the step's product to its part of dW, which stays in registers to the end
@@ -243,14 +281,12 @@ __device__ __forceinline__ void put_gate_db(const GatedGradArgs &a, int n0, int 
 // itself.
 template <typename T, int U, int KT, bool kShort>
 __global__ __launch_bounds__(kGateThreads) void gated_dw_kernel(const GatedGradArgs a, float *part) {
-    constexpr int R = kGateRows, NT = 2 * U, FN = NT / 64, FK = KT / 32;  // fragments of a wave
+    constexpr int R = gate_rows(U, KT), NT = 2 * U, FN = NT / 64, FK = KT / 32;  // fragments of a wave
     constexpr int PN = U / 8, PK = KT / 8;                               // pieces of a row
     constexpr int LN = R * PN / kGateThreads, LK = R * PK / kGateThreads;  // pieces of a thread
     constexpr int kBuffer = R * (NT + KT) * 2;
     extern __shared__ __attribute__((aligned(16))) char lds[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wn = wave >> 1, wk = wave & 1;
-    // (the two waves of a SIMD are a wave and the one four on)
-    const bool late = wave >= 4;
     const int n0 = blockIdx.y * U, k0 = blockIdx.z * KT;
     auto thread = [] {  // where this thread's pieces lie is worked out anew in every step
         int t = threadIdx.x;
@@ -266,18 +302,19 @@ __global__ __launch_bounds__(kGateThreads) void gated_dw_kernel(const GatedGradA
     float dbg[8] = {}, dbu[8] = {};
     RawGate raw[LN];
     u32x4 nx[LK];
-    // Addresses: a uniform base for the step and i, and this thread's 32-bit offset
-    // of its row and column in a step (row strides are below 2^22).
+    const int64_t steps = (a.m + R - 1) / R, by = gridDim.x;
+    // Addresses: a uniform base for the step and this thread's 32-bit offset of its row
+    // and column in a step (row strides are below 2^22).  Past the last step it is read again.
     auto fetch = [&](int64_t step) __attribute__((always_inline)) {
         const int t = thread();
         const Columns cn = columns_of(n0 + t % PN * 8, a.n), ck = columns_of(k0 + t % PK * 8, a.k);
-        const int64_t m = step * R;
+        const int64_t m = (step < steps ? step : steps - 1) * R;
         const int last = a.m - m < R ? (int)(a.m - m) - 1 : R - 1;  // rows past the end read the last one
 #pragma unroll
         for (int i = 0; i < LN; ++i) {
             const int at = t / PN + i * (kGateThreads / PN), r = at < last ? at : last;
             raw[i] = load_gate<kShort, T>(a, m * a.dhs + (uint32_t)(r * (int)a.dhs + cn.at), m * a.ps + (uint32_t)(r * (int)a.ps + cn.at),
-                                  m * a.qs + (uint32_t)(r * (int)a.qs + cn.at), cn);
+                                          m * a.qs + (uint32_t)(r * (int)a.qs + cn.at), cn);
         }
         if (a.dwg)
 #pragma unroll
@@ -289,29 +326,33 @@ __global__ __launch_bounds__(kGateThreads) void gated_dw_kernel(const GatedGradA
     auto prepare = [&](int64_t step, char *dzt) __attribute__((always_inline)) {
         char *const xt = dzt + R * NT * 2;
         const int t = thread();
-        const Columns cn = columns_of(n0 + t % PN * 8, a.n), ck = columns_of(k0 + t % PK * 8, a.k);
         const bool whole = (step + 1) * R <= a.m;
-        if (a.dwg)
+        if (a.dwg) {
+            if (a.k % 8) {  // pieces that the rows' end cuts: the slots of the piece before
+                const int drop = columns_of(k0 + t % PK * 8, a.k).drop;
 #pragma unroll
-            for (int i = 0; i < LK; ++i) {
-                const int r = t / PK + i * (kGateThreads / PK);
-                u32x4 v = nx[i];
-                if (ck.drop > 0)
+                for (int i = 0; i < LK; ++i)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) v[j] &= 2 * j >= ck.drop ? ~0u : 2 * j + 1 >= ck.drop ? 0xFFFF0000u : 0u;
-                if (!whole && step * R + r >= a.m) v = u32x4{0, 0, 0, 0};
-                *(u32x4 *)(xt + tile_at<KT>(r, t % PK)) = v;
+                    for (int j = 0; j < 4; ++j) nx[i][j] &= 2 * j >= drop ? ~0u : 2 * j + 1 >= drop ? 0xFFFF0000u : 0u;
             }
+            if (!whole)
+#pragma unroll
+                for (int i = 0; i < LK; ++i)
+                    if (step * R + t / PK + i * (kGateThreads / PK) >= a.m) nx[i] = u32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int i = 0; i < LK; ++i) *(u32x4 *)(xt + tile_at<KT>(t / PK + i * (kGateThreads / PK), t % PK)) = nx[i];
+        }
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int i = 0; i < LN; ++i) {
             const int r = t / PN + i * (kGateThreads / PN);
             float dg[8], du[8];
             gate_of<T>(raw[i], a.act, dg, du);
-            const int drop = whole || step * R + r < a.m ? cn.drop : 8;
-            if (drop > 0)
+            if (!whole || a.n % 8 || n0 + U > a.n) {
+                const int drop = step * R + r < a.m ? columns_of(n0 + t % PN * 8, a.n).drop : 8;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) dg[j] = j < drop ? 0.f : dg[j], du[j] = j < drop ? 0.f : du[j];
+            }
 #pragma unroll
             for (int j = 0; j < 8; ++j) dbg[j] += dg[j], dbu[j] += du[j];
             *(u32x4 *)(dzt + tile_at<NT>(r, t % PN)) = pack8<T>(dg);
@@ -319,41 +360,39 @@ __global__ __launch_bounds__(kGateThreads) void gated_dw_kernel(const GatedGradA
             __builtin_amdgcn_sched_barrier(0);  // one piece's values at a time: the registers hold no more
         }
     };
-
-    const int64_t steps = (a.m + R - 1) / R, by = gridDim.x;
-    if (blockIdx.x < steps) {
+    auto multiply = [&](char *dzt) __attribute__((always_inline)) {
+        if (!a.dwg) return;
+        char *const xt = dzt + R * NT * 2;
+        const int l = thread() & 63;
+#pragma unroll
+        for (int m = 0; m < R; m += 32) {
+            u32x4 dzf[FN];
+#pragma unroll
+            for (int i = 0; i < FN; ++i) dzf[i] = tile_columns<NT>(dzt, m, wn * FN + i, l);
+#pragma unroll
+            for (int j = 0; j < FK; ++j) {
+                const u32x4 xf = tile_columns<KT>(xt, m, wk * FK + j, l);
+#pragma unroll
+                for (int i = 0; i < FN; ++i) acc[i][j] = mma<T>(xf, dzf[i], acc[i][j]);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    auto walk = [&](auto late) __attribute__((always_inline)) {
         fetch(blockIdx.x);
         prepare(blockIdx.x, lds);
-        if (blockIdx.x + by < steps) fetch(blockIdx.x + by);
-    }
-    int turn = 0;
-    for (int64_t step = blockIdx.x; step < steps; step += by, turn ^= 1) {
-        step_barrier();  // this step's tiles are whole, and the last step's are done with
-        auto ahead = [&]() __attribute__((always_inline)) {
-            if (step + by >= steps) return;
+        fetch(blockIdx.x + by);
+        int turn = 0;
+        for (int64_t step = blockIdx.x; step < steps; step += by, turn ^= 1) {
+            step_barrier();  // this step's tiles are whole, and the last step's are done with
+            if constexpr (!decltype(late)::value) multiply(lds + turn * kBuffer);
             prepare(step + by, lds + (turn ^ 1) * kBuffer);
-            if (step + 2 * by < steps) fetch(step + 2 * by);
-        };
-        if (late) ahead();
-        if (a.dwg) {
-            char *const dzt = lds + turn * kBuffer, *const xt = dzt + R * NT * 2;
-            const int l = thread() & 63;
-#pragma unroll
-            for (int m = 0; m < R; m += 32) {
-                u32x4 dzf[FN];
-#pragma unroll
-                for (int i = 0; i < FN; ++i) dzf[i] = tile_columns<NT>(dzt, m, wn * FN + i, l);
-#pragma unroll
-                for (int j = 0; j < FK; ++j) {
-                    const u32x4 xf = tile_columns<KT>(xt, m, wk * FK + j, l);
-#pragma unroll
-                    for (int i = 0; i < FN; ++i) acc[i][j] = mma<T>(xf, dzf[i], acc[i][j]);
-                }
-                __builtin_amdgcn_sched_barrier(0);
-            }
+            fetch(step + 2 * by);
+            if constexpr (decltype(late)::value) multiply(lds + turn * kBuffer);
         }
-        if (!late) ahead();
-    }
+    };
+    if (wave >= 4) walk(std::true_type{});  // (the two waves of a SIMD are a wave and the one four on)
+    else walk(std::false_type{});
 
     // Partials: dW as fragments, [tile][workgroup][NT x KT], then db, [unit tile][workgroup][NT].
     const int tile = blockIdx.y * gridDim.z + blockIdx.z;
@@ -445,7 +484,7 @@ hipError_t gated_dx_launch(const GatedGradArgs &a, hipStream_t stream) {
 template <typename T, int U, int KT, bool kShort = false>
 hipError_t gated_dw_launch(const GatedGradArgs &a, const GatedGradPlan &p, float *part, hipStream_t stream) {
     const auto kernel = gated_dw_kernel<T, U, KT, kShort>;
-    const int bytes = 2 * kGateRows * (2 * U + KT) * 2;
+    const int bytes = 2 * gate_rows(U, KT) * (2 * U + KT) * 2;
     if (bytes > 65536) {
         const hipError_t e = hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != hipSuccess) return e;
