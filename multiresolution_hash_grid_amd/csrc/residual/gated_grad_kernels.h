@@ -85,10 +85,12 @@ __device__ __forceinline__ void step_barrier() {
 // their own and without branches around loads, so that the compiler can count those
 // in flight and a wait for the older kind leaves the younger on its way.
 // kShort: rows of units or inputs may be shorter than a piece.
-template <typename T, int KP, bool kShort>
-__global__ __launch_bounds__(kGateThreads) void gated_dx_kernel(const GatedGradArgs a, int tiles_k, int64_t tiles_m) {
+template <typename T, int KP, int NW, bool kShort>
+__global__ __launch_bounds__(NW * 64) void gated_dx_kernel(const GatedGradArgs a, int tiles_k, int64_t tiles_m) {
     extern __shared__ __attribute__((aligned(16))) char lds[];
-    constexpr int C = KP * 32, kHalf = 32 * C * 2, kBuffer = 2 * kHalf, kPer = C / 64;  // pieces of a thread
+    constexpr int C = KP * 32, kHalf = 32 * C * 2, kBuffer = 2 * kHalf;
+    constexpr int RF = NW == 8 ? 2 : 1, kRows = NW * RF * 16;         // row fragments of a wave; rows of a workgroup
+    constexpr int kStagers = NW == 16 ? 16 : 8, kThreads = kStagers * 64, kPer = 8 * C / kThreads;  // waves that bring weights; pieces of a thread
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), row16 = lane & 15, group = lane >> 4;
     // workgroups b, b + 8, ... share an XCD: the tiles of the same rows do
     const int xcd = blockIdx.x & 7, in_xcd = blockIdx.x >> 3;
@@ -105,7 +107,7 @@ __global__ __launch_bounds__(kGateThreads) void gated_dx_kernel(const GatedGradA
     };
     // This thread's pieces of a stretch's weights: one column, rows kStep apart of the
     // gate's 32 and then of up's.
-    constexpr int kRow = C / 8, kStep = kGateThreads / kRow;
+    constexpr int kRow = C / 8, kStep = kThreads / kRow;
     u32x4 staged[kPer];
     int ahead = 0;  // the units whose weights are fetched next
     auto fetch = [&]() __attribute__((always_inline)) {
@@ -146,23 +148,23 @@ __global__ __launch_bounds__(kGateThreads) void gated_dx_kernel(const GatedGradA
         }
     };
 
-    RawGate raw[2];
-    u32x4 dz[2][2];  // gate and up, row fragments
-    int64_t raw_m = walker * 256 + wave * 32 + row16;
+    RawGate raw[RF];
+    u32x4 dz[2][RF];  // gate and up, row fragments
+    int64_t raw_m = walker * kRows + wave * RF * 16 + row16;
     int raw_chunk = 0;
     auto load = [&]() __attribute__((always_inline)) {  // the units after the last loaded ones
         const Columns c = columns_of(raw_chunk * 32 + group * 8, a.n);
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
+        for (int r = 0; r < RF; ++r) {
             const int64_t m = raw_m + r * 16 < a.m ? raw_m + r * 16 : a.m - 1;
             raw[r] = load_gate<kShort, T>(a, m * a.dhs + c.at, m * a.ps + c.at, m * a.qs + c.at, c);
         }
-        raw_m += raw_chunk + 1 < chunks ? 0 : walkers * 256;
+        raw_m += raw_chunk + 1 < chunks ? 0 : walkers * kRows;
         raw_chunk = raw_chunk + 1 < chunks ? raw_chunk + 1 : 0;
     };
     auto derive = [&](int chunk) __attribute__((always_inline)) {
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
+        for (int r = 0; r < RF; ++r) {
             float dg[8], du[8];
             gate_of<T>(raw[r], a.act, dg, du);
             dz[0][r] = pack8<T>(dg);
@@ -171,19 +173,21 @@ __global__ __launch_bounds__(kGateThreads) void gated_dx_kernel(const GatedGradA
         if (chunk * 32 + 32 > a.n) {  // pieces that the rows' end cuts, and those past it
             const int drop = columns_of(chunk * 32 + group * 8, a.n).drop;
 #pragma unroll
-            for (int r = 0; r < 2; ++r)
+            for (int r = 0; r < RF; ++r)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) dz[h][r] = drop >= 8 ? u32x4{0, 0, 0, 0} : shifted(dz[h][r], drop);
         }
     };
 
-    f32x4 acc[KP][2][2];  // pairs, fragments of a pair, row fragments
-    int64_t m0 = walker * 256 + wave * 32 + row16;
-    auto walk = [&](auto late) __attribute__((always_inline)) {
-        constexpr bool kLate = decltype(late)::value;
-        fetch();
-        stage(lds, 0);
-        fetch();
+    f32x4 acc[KP][2][RF];  // pairs, fragments of a pair, row fragments
+    int64_t m0 = walker * kRows + wave * RF * 16 + row16;
+    auto walk = [&](auto late, auto stages) __attribute__((always_inline)) {
+        constexpr bool kLate = decltype(late)::value, kStage = decltype(stages)::value;
+        if constexpr (kStage) {
+            fetch();
+            stage(lds, 0);
+            fetch();
+        }
         load();
         if constexpr (!kLate) {
             derive(0);
@@ -193,8 +197,10 @@ __global__ __launch_bounds__(kGateThreads) void gated_dx_kernel(const GatedGradA
         for (int64_t q = 0; q < all; ++q) {
             step_barrier();  // these units' weights are in their buffer, and the last ones are done with
             const int next = chunk + 1 < chunks ? chunk + 1 : 0;
-            stage(lds + ((q + 1) & 1) * kBuffer, next);
-            fetch();
+            if constexpr (kStage) {
+                stage(lds + ((q + 1) & 1) * kBuffer, next);
+                fetch();
+            }
             if constexpr (kLate) {
                 derive(chunk);
                 load();
@@ -203,33 +209,42 @@ __global__ __launch_bounds__(kGateThreads) void gated_dx_kernel(const GatedGradA
 #pragma unroll
                 for (int p = 0; p < KP; ++p)
 #pragma unroll
-                    for (int f = 0; f < 2; ++f) acc[p][f][0] = acc[p][f][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+                    for (int f = 0; f < 2; ++f)
+#pragma unroll
+                        for (int r = 0; r < RF; ++r) acc[p][f][r] = f32x4{0.f, 0.f, 0.f, 0.f};
             char *const buffer = lds + (q & 1) * kBuffer;
             const int l = thread() & 63;
+            // A weight fragment is read kAhead fragments before its products, and no earlier:
+            // the registers hold no more.
+            constexpr int kAll = 4 * KP, kAhead = NW == 12 ? 2 : 4;
+            u32x4 w[kAhead];
+            auto read = [&](int i) __attribute__((always_inline)) {
+                w[i % kAhead] = tile_columns<C>(buffer + i / (2 * KP) * kHalf, 0, i % (2 * KP), l);
+            };
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+            for (int i = 0; i < kAhead; ++i) read(i);
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int p = 0; p < KP; ++p) {
+            for (int i = 0; i < kAll; ++i) {
+                const int h = i / (2 * KP), p = i / 2 % KP, f = i & 1;
 #pragma unroll
-                    for (int f = 0; f < 2; ++f) {
-                        const u32x4 w = tile_columns<C>(buffer + h * kHalf, 0, p * 2 + f, l);
-#pragma unroll
-                        for (int r = 0; r < 2; ++r) acc[p][f][r] = mma<T>(w, dz[h][r], acc[p][f][r]);
-                    }
-                }
+                for (int r = 0; r < RF; ++r) acc[p][f][r] = mma<T>(w[i % kAhead], dz[h][r], acc[p][f][r]);
+                if (i + kAhead < kAll) read(i + kAhead);
+                __builtin_amdgcn_sched_barrier(0);
+            }
             if (next == 0) {
 #pragma unroll
                 for (int p = 0; p < KP; ++p) {
                     const int k = k0 + p * 32 + group * 8, left = a.k - k;
 #pragma unroll
-                    for (int r = 0; r < 2; ++r) {
+                    for (int r = 0; r < RF; ++r) {
                         float v[8];
 #pragma unroll
                         for (int j = 0; j < 8; ++j) v[j] = acc[p][j / 4][r][j % 4];
                         if (m0 + r * 16 < a.m) put_piece((T *)a.dx + (m0 + r * 16) * a.dxs + k, left, pack8<T>(v));
                     }
                 }
-                m0 += walkers * 256;
+                m0 += walkers * kRows;
             }
             if constexpr (!kLate) {
                 derive(next);
@@ -238,8 +253,9 @@ __global__ __launch_bounds__(kGateThreads) void gated_dx_kernel(const GatedGradA
             chunk = next;
         }
     };
-    if (wave >= 4) walk(std::true_type{});
-    else walk(std::false_type{});
+    if (wave & 4) walk(std::true_type{}, std::true_type{});
+    else if (wave < kStagers) walk(std::false_type{}, std::true_type{});
+    else walk(std::false_type{}, std::false_type{});
 }
 
 // Four values of dW, slots k .. k + 3 of slot n of a tile's 2 U (gate, then up),
@@ -375,6 +391,14 @@ __global__ __launch_bounds__(kGateThreads) void gated_dw_kernel(const GatedGradA
 #pragma unroll
                 for (int i = 0; i < FN; ++i) acc[i][j] = mma<T>(xf, dzf[i], acc[i][j]);
             }
+            // x's fragments are read (two reads each) two before their products
+            __builtin_amdgcn_sched_group_barrier(0x100, 2 * FN + 4, 0);
+#pragma unroll
+            for (int j = 0; j < FK - 2; ++j) {
+                __builtin_amdgcn_sched_group_barrier(0x008, FN, 0);
+                __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+            }
+            __builtin_amdgcn_sched_group_barrier(0x008, 2 * FN, 0);
             __builtin_amdgcn_sched_barrier(0);
         }
     };
@@ -466,18 +490,18 @@ __global__ __launch_bounds__(512) void gated_join_kernel(const float *part, int 
     }
 }
 
-template <typename T, int KP, bool kShort = false>
+template <typename T, int KP, int NW, bool kShort = false>
 hipError_t gated_dx_launch(const GatedGradArgs &a, hipStream_t stream) {
-    const auto kernel = gated_dx_kernel<T, KP, kShort>;
+    const auto kernel = gated_dx_kernel<T, KP, NW, kShort>;
     const int bytes = 2 * 2 * 32 * KP * 32 * 2, tiles_k = (int)div_up(a.k, KP * 32);
     if (bytes > 65536) {
         const hipError_t e = hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != hipSuccess) return e;
     }
-    const int64_t tiles_m = div_up(a.m, 256);
+    const int64_t tiles_m = div_up(a.m, NW == 12 ? 192 : 256);
     int64_t walkers = kCus / tiles_k < tiles_m ? kCus / tiles_k : tiles_m;
     walkers = div_up(walkers < 1 ? 1 : walkers, 8) * 8;  // whole rounds over the XCDs
-    kernel<<<dim3((unsigned)(walkers * tiles_k)), kGateThreads, bytes, stream>>>(a, tiles_k, tiles_m);
+    kernel<<<dim3((unsigned)(walkers * tiles_k)), NW * 64, bytes, stream>>>(a, tiles_k, tiles_m);
     return hipGetLastError();
 }
 
@@ -514,8 +538,8 @@ hipError_t gated_grad_run(const GatedGradArgs &a, const GatedGradPlan &p, float 
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     if (!a.dx || a.m == 0) return hipSuccess;
-    if (a.n < 8 || a.k < 8) return gated_dx_launch<T, 2, true>(a, stream);
-    return p.kp == 2 ? gated_dx_launch<T, 2>(a, stream) : p.kp == 4 ? gated_dx_launch<T, 4>(a, stream) : gated_dx_launch<T, 8>(a, stream);
+    if (a.n < 8 || a.k < 8) return gated_dx_launch<T, 2, 8, true>(a, stream);
+    return p.kp == 2 ? gated_dx_launch<T, 2, 8>(a, stream) : p.kp == 4 ? gated_dx_launch<T, 4, 16>(a, stream) : gated_dx_launch<T, 8, 12>(a, stream);
 }
 
 }  // namespace
