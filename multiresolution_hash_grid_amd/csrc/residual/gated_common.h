@@ -37,9 +37,8 @@ __device__ __forceinline__ void gate_all(float (&g)[N], const float (&u)[N], int
     for (int j = 0; j < N; ++j) g[j] *= u[j];
 }
 
-// dg and du of one hidden unit.  The activation's value and slope share their
-// logistic function p: SiLU z p and p (1 + z (1 - p)), GELU z p and
-// p + z p (1 - p) d(2u)/dz.
+// dg and du of one hidden unit.  The activation's value v = g p and slope share their
+// logistic function p: SiLU's slope is p + v (1 - p), GELU's p + v (1 - p) d(2u)/dg.
 template <int kAct>
 __device__ __forceinline__ void gate_grad(float g, float u, float dh, float &dg, float &du) {
     if constexpr (kAct == HG_ACT_NONE) {
@@ -48,10 +47,11 @@ __device__ __forceinline__ void gate_grad(float g, float u, float dh, float &dg,
         const bool on = !(g <= 0.f);  // (a NaN stays one)
         dg = on ? dh * u * (g != g ? g : 1.f) : 0.f, du = on ? dh * g : 0.f;
     } else {
-        const float p = kAct == HG_ACT_SILU ? logistic(g) : gelu_logistic(g);
-        const float t = kAct == HG_ACT_SILU ? g : g * fmaf(g * g, 0.21406447f, 1.59576912f);
-        dg = dh * u * mul0(p, 1.f + mul0(t, 1.f - p));
-        du = dh * mul0(g, p);
+        const float p = kAct == HG_ACT_SILU ? logistic(g) : gelu_logistic(g), value = mul0(g, p);
+        // (1 - p is 0 where g is so large that value may be infinite)
+        const float t = kAct == HG_ACT_SILU ? value : mul0(value, fmaf(g * g, 0.21406447f, 1.59576912f));
+        dg = dh * u * (p + mul0(t, 1.f - p));
+        du = dh * value;
     }
 }
 template <int N>

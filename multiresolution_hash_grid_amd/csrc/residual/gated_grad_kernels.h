@@ -30,11 +30,6 @@ __device__ __forceinline__ void values(u32x4 v, float (&f)[8]) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) f[j] = (float)t[j];
 }
-template <bool kShort, typename T>
-__device__ __forceinline__ RawGate load_gate(const GatedGradArgs &a, int64_t dh, int64_t g, int64_t u, Columns c) {
-    return {load_columns<kShort>((const T *)a.dh + dh, c, a.n), load_columns<kShort>((const T *)a.gate + g, c, a.n),
-            load_columns<kShort>((const T *)a.up + u, c, a.n)};
-}
 template <typename T>
 __device__ __forceinline__ void gate_of(const RawGate &raw, int act, float (&dg)[8], float (&du)[8]) {
     float g[8], u[8], dh[8];
@@ -63,6 +58,26 @@ __device__ __forceinline__ void put_piece(T *p, int left, u32x4 v) {
     if (left & 1) store_loose(p, (uint16_t)v[0]);
 }
 
+// tile_columns of the tile of 32 rows at `tile` + m rows: the lane's place is worked
+// out once, and a fragment's number only turns bits of it.
+// (A multiple of 512 bytes may be added to the place, as to `tile`.)
+template <int C>
+__device__ __forceinline__ int columns_base(int lane) {
+    const int i = lane & 15;
+    return tile_at<C>((lane >> 4) * 8 + (i >> 2), (i >> 1) & 1) + (i & 1) * 8;
+}
+template <int C>
+__device__ __forceinline__ u32x4 columns_at(char *tile, int base, int m, int q) {
+    union {
+        s16x4 h[2];
+        u32x4 v;
+    } r;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)  // rows four on: one bit of the turn, which a piece's place is XORed with
+        r.h[h] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(tile + ((base ^ ((2 * q ^ h) << 4)) + (m + 4 * h) * (C * 2))));
+    return r.v;
+}
+
 // This wave's LDS accesses are done, and so are the others'.
 __device__ __forceinline__ void step_barrier() {
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
@@ -85,12 +100,10 @@ __device__ __forceinline__ void step_barrier() {
 // their own and without branches around loads, so that the compiler can count those
 // in flight and a wait for the older kind leaves the younger on its way.
 // kShort: rows of units or inputs may be shorter than a piece.
-template <typename T, int KP, int NW, bool kShort>
-__global__ __launch_bounds__(NW * 64) void gated_dx_kernel(const GatedGradArgs a, int tiles_k, int64_t tiles_m) {
+template <typename T, int KP, bool kShort>
+__global__ __launch_bounds__(kGateThreads) void gated_dx_kernel(const GatedGradArgs a, int tiles_k, int64_t tiles_m) {
     extern __shared__ __attribute__((aligned(16))) char lds[];
-    constexpr int C = KP * 32, kHalf = 32 * C * 2, kBuffer = 2 * kHalf;
-    constexpr int RF = NW == 8 ? 2 : 1, kRows = NW * RF * 16;         // row fragments of a wave; rows of a workgroup
-    constexpr int kStagers = NW == 16 ? 16 : 8, kThreads = kStagers * 64, kPer = 8 * C / kThreads;  // waves that bring weights; pieces of a thread
+    constexpr int C = KP * 32, kHalf = 32 * C * 2, kBuffer = 2 * kHalf, kPer = C / 64;  // pieces of a thread
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), row16 = lane & 15, group = lane >> 4;
     // workgroups b, b + 8, ... share an XCD: the tiles of the same rows do
     const int xcd = blockIdx.x & 7, in_xcd = blockIdx.x >> 3;
@@ -100,71 +113,76 @@ __global__ __launch_bounds__(NW * 64) void gated_dx_kernel(const GatedGradArgs a
     const int chunks = (a.n + 31) / 32;
     const int64_t all = ((tiles_m - 1 - walker) / walkers + 1) * chunks;
 
+    // This thread's pieces of a stretch's weights: one column, rows kStep apart of the
+    // gate's 32 and then of up's.
+    constexpr int kRow = C / 8, kStep = kGateThreads / kRow;
     auto thread = [] {  // where this thread's pieces lie is worked out anew each time: held, it would cost registers
         int t = threadIdx.x;
         asm volatile("" : "+v"(t));
         return t;
     };
-    // This thread's pieces of a stretch's weights: one column, rows kStep apart of the
-    // gate's 32 and then of up's.
-    constexpr int kRow = C / 8, kStep = kThreads / kRow;
     u32x4 staged[kPer];
     int ahead = 0;  // the units whose weights are fetched next
     auto fetch = [&]() __attribute__((always_inline)) {
-        const int t = thread(), room = a.n - 1 - ahead * 32;
-        const Columns c = columns_of(k0 + t % kRow * 8, a.k);
+        const int t = thread(), w_row = t / kRow, room = a.n - 1 - ahead * 32;
+        const Columns w_col = columns_of(k0 + t % kRow * 8, a.k);
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
-            const int at = kPer == 1 ? t / kRow : j * kStep % 32 + t / kRow, row = kPer == 1 ? at & 31 : at;
+            const int at = kPer == 1 ? w_row : j * kStep % 32 + w_row, row = kPer == 1 ? at & 31 : at;
             const bool up = kPer == 1 ? at >= 32 : j * kStep >= 32;
             const T *const w = (const T *)(up ? a.wu : a.wg) + (int64_t)(ahead * 32 + (row < room ? row : room)) * (up ? a.us : a.gs);
-            staged[j] = load_columns<kShort>(w + c.at, c, a.k);
+            staged[j] = load_columns<kShort>(w + w_col.at, w_col, a.k);
         }
         ahead = ahead + 1 < chunks ? ahead + 1 : 0;
     };
     // (Columns past k become inputs that are not stored; units past n must be zero.)
+    // columns 8 b .. + 3 of 32 are columns 4 b .. of the pair's first fragment, the next four of its second;
+    // rows 16 apart lie alike
     auto stage = [&](char *to, int chunk) __attribute__((always_inline)) {
-        const int t = thread(), piece = t % kRow;
+        const int t = thread(), w_row = t / kRow, w_piece = t % kRow;
+        const int w_to = (kPer == 1 ? (w_row >> 5) * kHalf : 0) + tile_at<C>(w_row & 31, (w_piece >> 2) * 4 + ((w_piece & 3) >> 1)) + (w_piece & 1) * 8;
         if (a.k % 8) {
-            const int drop = columns_of(k0 + piece * 8, a.k).drop;
+            const int drop = columns_of(k0 + w_piece * 8, a.k).drop & 7;
 #pragma unroll
-            for (int j = 0; j < kPer; ++j) staged[j] = shifted(staged[j], drop & 7);
+            for (int j = 0; j < kPer; ++j) staged[j] = shifted(staged[j], drop);
         }
         const int room = a.n - chunk * 32;
         if (room < 32)
 #pragma unroll
             for (int j = 0; j < kPer; ++j)
-                if (((kPer == 1 ? 0 : j * kStep % 32) + t / kRow) % 32 >= room) staged[j] = u32x4{0, 0, 0, 0};
-        // columns 8 b .. + 3 of 32 are columns 4 b .. of the pair's first fragment, the next four of its second;
-        // rows 16 apart lie alike
-        const int at = t / kRow, first = (piece >> 2) * 4 + ((piece & 3) >> 1);
-        char *const lo = to + (kPer == 1 ? (at >> 5) * kHalf : 0) + tile_at<C>(at & 31, first) + (piece & 1) * 8;
-        char *const hi = to + (kPer == 1 ? (at >> 5) * kHalf : 0) + tile_at<C>(at & 31, first + 2) + (piece & 1) * 8;
+                if (((kPer == 1 ? 0 : j * kStep % 32) + w_row) % 32 >= room) staged[j] = u32x4{0, 0, 0, 0};
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
             const int skip = j * kStep / 32 * kHalf + j * kStep % 32 * (C * 2);
-            *(u32x2 *)(lo + skip) = u32x2{staged[j][0], staged[j][1]};
-            *(u32x2 *)(hi + skip) = u32x2{staged[j][2], staged[j][3]};
+            *(u32x2 *)(to + w_to + skip) = u32x2{staged[j][0], staged[j][1]};
+            *(u32x2 *)(to + (w_to ^ 32) + skip) = u32x2{staged[j][2], staged[j][3]};
         }
     };
 
-    RawGate raw[RF];
-    u32x4 dz[2][RF];  // gate and up, row fragments
-    int64_t raw_m = walker * kRows + wave * RF * 16 + row16;
+    RawGate raw[2];
+    u32x4 dz[2][2];  // gate and up, row fragments
+    int64_t raw_tile = walker;
     int raw_chunk = 0;
     auto load = [&]() __attribute__((always_inline)) {  // the units after the last loaded ones
         const Columns c = columns_of(raw_chunk * 32 + group * 8, a.n);
+        const int64_t m = (raw_tile < tiles_m ? raw_tile : tiles_m - 1) * 256;
+        const int last = a.m - m < 256 ? (int)(a.m - m) - 1 : 255;  // rows past the end read the last one
+        const char *const dh = (const char *)a.dh + m * a.dhs * 2, *const g = (const char *)a.gate + m * a.ps * 2,
+                   *const u = (const char *)a.up + m * a.qs * 2;
 #pragma unroll
-        for (int r = 0; r < RF; ++r) {
-            const int64_t m = raw_m + r * 16 < a.m ? raw_m + r * 16 : a.m - 1;
-            raw[r] = load_gate<kShort, T>(a, m * a.dhs + c.at, m * a.ps + c.at, m * a.qs + c.at, c);
+        for (int r = 0; r < 2; ++r) {
+            const int row = wave * 32 + r * 16 + row16;
+            const uint32_t at = row < last ? row : last;  // (row strides are below 2^22)
+            raw[r] = {load_columns<kShort>((const T *)(dh + (at * (uint32_t)a.dhs + c.at) * 2u), c, a.n),
+                      load_columns<kShort>((const T *)(g + (at * (uint32_t)a.ps + c.at) * 2u), c, a.n),
+                      load_columns<kShort>((const T *)(u + (at * (uint32_t)a.qs + c.at) * 2u), c, a.n)};
         }
-        raw_m += raw_chunk + 1 < chunks ? 0 : walkers * kRows;
+        raw_tile += raw_chunk + 1 < chunks ? 0 : walkers;
         raw_chunk = raw_chunk + 1 < chunks ? raw_chunk + 1 : 0;
     };
     auto derive = [&](int chunk) __attribute__((always_inline)) {
 #pragma unroll
-        for (int r = 0; r < RF; ++r) {
+        for (int r = 0; r < 2; ++r) {
             float dg[8], du[8];
             gate_of<T>(raw[r], a.act, dg, du);
             dz[0][r] = pack8<T>(dg);
@@ -173,53 +191,52 @@ __global__ __launch_bounds__(NW * 64) void gated_dx_kernel(const GatedGradArgs a
         if (chunk * 32 + 32 > a.n) {  // pieces that the rows' end cuts, and those past it
             const int drop = columns_of(chunk * 32 + group * 8, a.n).drop;
 #pragma unroll
-            for (int r = 0; r < RF; ++r)
+            for (int r = 0; r < 2; ++r)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) dz[h][r] = drop >= 8 ? u32x4{0, 0, 0, 0} : shifted(dz[h][r], drop);
         }
     };
 
-    f32x4 acc[KP][2][RF];  // pairs, fragments of a pair, row fragments
-    int64_t m0 = walker * kRows + wave * RF * 16 + row16;
-    auto walk = [&](auto late, auto stages) __attribute__((always_inline)) {
-        constexpr bool kLate = decltype(late)::value, kStage = decltype(stages)::value;
-        if constexpr (kStage) {
-            fetch();
-            stage(lds, 0);
-            fetch();
-        }
+    const int columns = columns_base<C>(lane);
+    f32x4 acc[KP][2][2];  // pairs, fragments of a pair, row fragments
+    int64_t m0 = walker * 256 + wave * 32 + row16;
+    auto walk = [&](auto late) __attribute__((always_inline)) {
+        constexpr bool kLate = decltype(late)::value;
+        fetch();
+        stage(lds, 0);
+        fetch();
+        __builtin_amdgcn_sched_barrier(0);  // (the order of the loads in flight is the loop's)
         load();
         if constexpr (!kLate) {
             derive(0);
             load();
         }
+        __builtin_amdgcn_sched_barrier(0);
         int chunk = 0;
         for (int64_t q = 0; q < all; ++q) {
             step_barrier();  // these units' weights are in their buffer, and the last ones are done with
             const int next = chunk + 1 < chunks ? chunk + 1 : 0;
-            if constexpr (kStage) {
-                stage(lds + ((q + 1) & 1) * kBuffer, next);
-                fetch();
-            }
+            stage(lds + ((q + 1) & 1) * kBuffer, next);
+            fetch();
+            __builtin_amdgcn_sched_barrier(0);
             if constexpr (kLate) {
                 derive(chunk);
                 load();
+                __builtin_amdgcn_sched_barrier(0);
             }
             if (chunk == 0)
 #pragma unroll
                 for (int p = 0; p < KP; ++p)
 #pragma unroll
-                    for (int f = 0; f < 2; ++f)
-#pragma unroll
-                        for (int r = 0; r < RF; ++r) acc[p][f][r] = f32x4{0.f, 0.f, 0.f, 0.f};
-            char *const buffer = lds + (q & 1) * kBuffer;
-            const int l = thread() & 63;
+                    for (int f = 0; f < 2; ++f) acc[p][f][0] = acc[p][f][1] = f32x4{0.f, 0.f, 0.f, 0.f};
             // A weight fragment is read kAhead fragments before its products, and no earlier:
             // the registers hold no more.
-            constexpr int kAll = 4 * KP, kAhead = NW == 12 ? 2 : 4;
+            constexpr int kAll = 4 * KP, kAhead = KP == 8 ? 2 : 4;
             u32x4 w[kAhead];
+            int at = columns + (int)(q & 1) * kBuffer;
+            asm volatile("" : "+v"(at));  // each fragment's place is worked out anew: held, they would cost registers
             auto read = [&](int i) __attribute__((always_inline)) {
-                w[i % kAhead] = tile_columns<C>(buffer + i / (2 * KP) * kHalf, 0, i % (2 * KP), l);
+                w[i % kAhead] = columns_at<C>(lds + i / (2 * KP) * kHalf, at, 0, i % (2 * KP));
             };
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) read(i);
@@ -228,7 +245,7 @@ __global__ __launch_bounds__(NW * 64) void gated_dx_kernel(const GatedGradArgs a
             for (int i = 0; i < kAll; ++i) {
                 const int h = i / (2 * KP), p = i / 2 % KP, f = i & 1;
 #pragma unroll
-                for (int r = 0; r < RF; ++r) acc[p][f][r] = mma<T>(w[i % kAhead], dz[h][r], acc[p][f][r]);
+                for (int r = 0; r < 2; ++r) acc[p][f][r] = mma<T>(w[i % kAhead], dz[h][r], acc[p][f][r]);
                 if (i + kAhead < kAll) read(i + kAhead);
                 __builtin_amdgcn_sched_barrier(0);
             }
@@ -237,14 +254,14 @@ __global__ __launch_bounds__(NW * 64) void gated_dx_kernel(const GatedGradArgs a
                 for (int p = 0; p < KP; ++p) {
                     const int k = k0 + p * 32 + group * 8, left = a.k - k;
 #pragma unroll
-                    for (int r = 0; r < RF; ++r) {
+                    for (int r = 0; r < 2; ++r) {
                         float v[8];
 #pragma unroll
                         for (int j = 0; j < 8; ++j) v[j] = acc[p][j / 4][r][j % 4];
                         if (m0 + r * 16 < a.m) put_piece((T *)a.dx + (m0 + r * 16) * a.dxs + k, left, pack8<T>(v));
                     }
                 }
-                m0 += walkers * kRows;
+                m0 += walkers * 256;
             }
             if constexpr (!kLate) {
                 derive(next);
@@ -253,9 +270,8 @@ __global__ __launch_bounds__(NW * 64) void gated_dx_kernel(const GatedGradArgs a
             chunk = next;
         }
     };
-    if (wave & 4) walk(std::true_type{}, std::true_type{});
-    else if (wave < kStagers) walk(std::false_type{}, std::true_type{});
-    else walk(std::false_type{}, std::false_type{});
+    if (wave >= 4) walk(std::true_type{});
+    else walk(std::false_type{});
 }
 
 // Four values of dW, slots k .. k + 3 of slot n of a tile's 2 U (gate, then up),
@@ -304,12 +320,6 @@ __global__ __launch_bounds__(kGateThreads) void gated_dw_kernel(const GatedGradA
     extern __shared__ __attribute__((aligned(16))) char lds[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wn = wave >> 1, wk = wave & 1;
     const int n0 = blockIdx.y * U, k0 = blockIdx.z * KT;
-    auto thread = [] {  // where this thread's pieces lie is worked out anew in every step
-        int t = threadIdx.x;
-        asm volatile("" : "+v"(t));
-        return t;
-    };
-
     f32x4 acc[FN][FK];
 #pragma unroll
     for (int i = 0; i < FN; ++i)
@@ -319,75 +329,82 @@ __global__ __launch_bounds__(kGateThreads) void gated_dw_kernel(const GatedGradA
     RawGate raw[LN];
     u32x4 nx[LK];
     const int64_t steps = (a.m + R - 1) / R, by = gridDim.x;
-    // Addresses: a uniform base for the step and this thread's 32-bit offset of its row
-    // and column in a step (row strides are below 2^22).  Past the last step it is read again.
-    auto fetch = [&](int64_t step) __attribute__((always_inline)) {
-        const int t = thread();
-        const Columns cn = columns_of(n0 + t % PN * 8, a.n), ck = columns_of(k0 + t % PK * 8, a.k);
-        const int64_t m = (step < steps ? step : steps - 1) * R;
-        const int last = a.m - m < R ? (int)(a.m - m) - 1 : R - 1;  // rows past the end read the last one
+    const int rn = threadIdx.x / PN, rk = threadIdx.x / PK;  // this thread's first rows in a step
+    const Columns cn = columns_of(n0 + threadIdx.x % PN * 8, a.n), ck = columns_of(k0 + threadIdx.x % PK * 8, a.k);
+    // Bytes of this thread's pieces from a step's first row (row strides are below 2^22).
+    uint32_t at_dh[LN], at_g[LN], at_u[LN], at_x[LK];
+    auto rows_of = [&](int last) __attribute__((always_inline)) {  // rows past the end read the last one
 #pragma unroll
         for (int i = 0; i < LN; ++i) {
-            const int at = t / PN + i * (kGateThreads / PN), r = at < last ? at : last;
-            raw[i] = load_gate<kShort, T>(a, m * a.dhs + (uint32_t)(r * (int)a.dhs + cn.at), m * a.ps + (uint32_t)(r * (int)a.ps + cn.at),
-                                          m * a.qs + (uint32_t)(r * (int)a.qs + cn.at), cn);
+            const int at = rn + i * (kGateThreads / PN), r = at < last ? at : last;
+            at_dh[i] = ((uint32_t)r * (uint32_t)a.dhs + cn.at) * 2u, at_g[i] = ((uint32_t)r * (uint32_t)a.ps + cn.at) * 2u,
+            at_u[i] = ((uint32_t)r * (uint32_t)a.qs + cn.at) * 2u;
         }
+#pragma unroll
+        for (int i = 0; i < LK; ++i) {
+            const int at = rk + i * (kGateThreads / PK), r = at < last ? at : last;
+            at_x[i] = ((uint32_t)r * (uint32_t)a.xs + ck.at) * 2u;
+        }
+    };
+    rows_of(R - 1);
+    auto fetch = [&](int64_t step) __attribute__((always_inline)) {  // past the last step it is read again
+        const int64_t m = (step < steps ? step : steps - 1) * R;
+        if (a.m - m < R) rows_of((int)(a.m - m) - 1);
+        const char *const dh = (const char *)a.dh + m * a.dhs * 2, *const g = (const char *)a.gate + m * a.ps * 2,
+                   *const u = (const char *)a.up + m * a.qs * 2, *const x = (const char *)a.x + m * a.xs * 2;
+#pragma unroll
+        for (int i = 0; i < LN; ++i)
+            raw[i] = {load_columns<kShort>((const T *)(dh + at_dh[i]), cn, a.n), load_columns<kShort>((const T *)(g + at_g[i]), cn, a.n),
+                      load_columns<kShort>((const T *)(u + at_u[i]), cn, a.n)};
         if (a.dwg)
 #pragma unroll
-            for (int i = 0; i < LK; ++i) {
-                const int at = t / PK + i * (kGateThreads / PK), r = at < last ? at : last;
-                nx[i] = load_columns<kShort>((const T *)a.x + m * a.xs + (uint32_t)(r * (int)a.xs + ck.at), ck, a.k);
-            }
+            for (int i = 0; i < LK; ++i) nx[i] = load_columns<kShort>((const T *)(x + at_x[i]), ck, a.k);
     };
-    auto prepare = [&](int64_t step, char *dzt) __attribute__((always_inline)) {
-        char *const xt = dzt + R * NT * 2;
-        const int t = thread();
+    const int to_dz = tile_at<NT>(rn, threadIdx.x % PN), to_x = R * NT * 2 + tile_at<KT>(rk, threadIdx.x % PK);  // (rows 16 apart lie alike)
+    auto prepare = [&](int64_t step, char *tiles) __attribute__((always_inline)) {
         const bool whole = (step + 1) * R <= a.m;
         if (a.dwg) {
-            if (a.k % 8) {  // pieces that the rows' end cuts: the slots of the piece before
-                const int drop = columns_of(k0 + t % PK * 8, a.k).drop;
+            if (a.k % 8)  // pieces that the rows' end cuts: the slots of the piece before
 #pragma unroll
                 for (int i = 0; i < LK; ++i)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) nx[i][j] &= 2 * j >= drop ? ~0u : 2 * j + 1 >= drop ? 0xFFFF0000u : 0u;
-            }
+                    for (int j = 0; j < 4; ++j) nx[i][j] &= 2 * j >= ck.drop ? ~0u : 2 * j + 1 >= ck.drop ? 0xFFFF0000u : 0u;
             if (!whole)
 #pragma unroll
                 for (int i = 0; i < LK; ++i)
-                    if (step * R + t / PK + i * (kGateThreads / PK) >= a.m) nx[i] = u32x4{0, 0, 0, 0};
+                    if (step * R + rk + i * (kGateThreads / PK) >= a.m) nx[i] = u32x4{0, 0, 0, 0};
 #pragma unroll
-            for (int i = 0; i < LK; ++i) *(u32x4 *)(xt + tile_at<KT>(t / PK + i * (kGateThreads / PK), t % PK)) = nx[i];
+            for (int i = 0; i < LK; ++i) *(u32x4 *)(tiles + to_x + i * (kGateThreads / PK) * (KT * 2)) = nx[i];
         }
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int i = 0; i < LN; ++i) {
-            const int r = t / PN + i * (kGateThreads / PN);
             float dg[8], du[8];
             gate_of<T>(raw[i], a.act, dg, du);
             if (!whole || a.n % 8 || n0 + U > a.n) {
-                const int drop = step * R + r < a.m ? columns_of(n0 + t % PN * 8, a.n).drop : 8;
+                const int drop = step * R + rn + i * (kGateThreads / PN) < a.m ? cn.drop : 8;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) dg[j] = j < drop ? 0.f : dg[j], du[j] = j < drop ? 0.f : du[j];
             }
 #pragma unroll
             for (int j = 0; j < 8; ++j) dbg[j] += dg[j], dbu[j] += du[j];
-            *(u32x4 *)(dzt + tile_at<NT>(r, t % PN)) = pack8<T>(dg);
-            *(u32x4 *)(dzt + tile_at<NT>(r, PN + t % PN)) = pack8<T>(du);
+            *(u32x4 *)(tiles + to_dz + i * (kGateThreads / PN) * (NT * 2)) = pack8<T>(dg);
+            *(u32x4 *)(tiles + (to_dz ^ (PN << 4)) + i * (kGateThreads / PN) * (NT * 2)) = pack8<T>(du);
             __builtin_amdgcn_sched_barrier(0);  // one piece's values at a time: the registers hold no more
         }
     };
-    auto multiply = [&](char *dzt) __attribute__((always_inline)) {
+    const int columns_n = columns_base<NT>(lane) ^ (2 * wn * FN << 4), columns_k = columns_base<KT>(lane) ^ (2 * wk * FK << 4);
+    auto multiply = [&](int turn) __attribute__((always_inline)) {
         if (!a.dwg) return;
-        char *const xt = dzt + R * NT * 2;
-        const int l = thread() & 63;
+        const int at_n = columns_n + turn * kBuffer, at_k = columns_k + turn * kBuffer;
 #pragma unroll
         for (int m = 0; m < R; m += 32) {
             u32x4 dzf[FN];
 #pragma unroll
-            for (int i = 0; i < FN; ++i) dzf[i] = tile_columns<NT>(dzt, m, wn * FN + i, l);
+            for (int i = 0; i < FN; ++i) dzf[i] = columns_at<NT>(lds, at_n, m, i);
 #pragma unroll
             for (int j = 0; j < FK; ++j) {
-                const u32x4 xf = tile_columns<KT>(xt, m, wk * FK + j, l);
+                const u32x4 xf = columns_at<KT>(lds + R * NT * 2, at_k, m, j);
 #pragma unroll
                 for (int i = 0; i < FN; ++i) acc[i][j] = mma<T>(xf, dzf[i], acc[i][j]);
             }
@@ -409,10 +426,10 @@ __global__ __launch_bounds__(kGateThreads) void gated_dw_kernel(const GatedGradA
         int turn = 0;
         for (int64_t step = blockIdx.x; step < steps; step += by, turn ^= 1) {
             step_barrier();  // this step's tiles are whole, and the last step's are done with
-            if constexpr (!decltype(late)::value) multiply(lds + turn * kBuffer);
+            if constexpr (!decltype(late)::value) multiply(turn);
             prepare(step + by, lds + (turn ^ 1) * kBuffer);
             fetch(step + 2 * by);
-            if constexpr (decltype(late)::value) multiply(lds + turn * kBuffer);
+            if constexpr (decltype(late)::value) multiply(turn);
         }
     };
     if (wave >= 4) walk(std::true_type{});  // (the two waves of a SIMD are a wave and the one four on)
@@ -490,18 +507,18 @@ __global__ __launch_bounds__(512) void gated_join_kernel(const float *part, int 
     }
 }
 
-template <typename T, int KP, int NW, bool kShort = false>
+template <typename T, int KP, bool kShort = false>
 hipError_t gated_dx_launch(const GatedGradArgs &a, hipStream_t stream) {
-    const auto kernel = gated_dx_kernel<T, KP, NW, kShort>;
+    const auto kernel = gated_dx_kernel<T, KP, kShort>;
     const int bytes = 2 * 2 * 32 * KP * 32 * 2, tiles_k = (int)div_up(a.k, KP * 32);
     if (bytes > 65536) {
         const hipError_t e = hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != hipSuccess) return e;
     }
-    const int64_t tiles_m = div_up(a.m, NW == 12 ? 192 : 256);
-    int64_t walkers = kCus / tiles_k < tiles_m ? kCus / tiles_k : tiles_m;
+    const int64_t tiles_m = div_up(a.m, 256), most = kCus * (KP == 2 ? 2 : 1) / tiles_k;  // (registers of one or two workgroups a CU)
+    int64_t walkers = most < tiles_m ? most : tiles_m;
     walkers = div_up(walkers < 1 ? 1 : walkers, 8) * 8;  // whole rounds over the XCDs
-    kernel<<<dim3((unsigned)(walkers * tiles_k)), NW * 64, bytes, stream>>>(a, tiles_k, tiles_m);
+    kernel<<<dim3((unsigned)(walkers * tiles_k)), kGateThreads, bytes, stream>>>(a, tiles_k, tiles_m);
     return hipGetLastError();
 }
 
@@ -538,8 +555,8 @@ hipError_t gated_grad_run(const GatedGradArgs &a, const GatedGradPlan &p, float 
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     if (!a.dx || a.m == 0) return hipSuccess;
-    if (a.n < 8 || a.k < 8) return gated_dx_launch<T, 2, 8, true>(a, stream);
-    return p.kp == 2 ? gated_dx_launch<T, 2, 8>(a, stream) : p.kp == 4 ? gated_dx_launch<T, 4, 16>(a, stream) : gated_dx_launch<T, 8, 12>(a, stream);
+    if (a.n < 8 || a.k < 8) return gated_dx_launch<T, 2, true>(a, stream);
+    return p.kp == 2 ? gated_dx_launch<T, 2>(a, stream) : p.kp == 4 ? gated_dx_launch<T, 4>(a, stream) : gated_dx_launch<T, 8>(a, stream);
 }
 
 }  // namespace
