@@ -270,7 +270,7 @@ __global__ __launch_bounds__(kGateThreads) void gated_dx_kernel(const GatedGradA
             chunk = next;
         }
     };
-    if (wave >= 4) walk(std::true_type{});
+    if (wave & 2) walk(std::true_type{});
     else walk(std::false_type{});
 }
 
@@ -432,7 +432,7 @@ __global__ __launch_bounds__(kGateThreads) void gated_dw_kernel(const GatedGradA
             if constexpr (decltype(late)::value) multiply(turn);
         }
     };
-    if (wave >= 4) walk(std::true_type{});  // (the two waves of a SIMD are a wave and the one four on)
+    if (wave & 2) walk(std::true_type{});
     else walk(std::false_type{});
 
     // Partials: dW as fragments, [tile][workgroup][NT x KT], then db, [unit tile][workgroup][NT].
