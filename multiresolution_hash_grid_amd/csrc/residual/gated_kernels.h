@@ -195,11 +195,9 @@ hipError_t rows_launch(const GatedArgs &a, const RowsPlan &p, hipStream_t stream
 // fragments, x is read once for every slice of 256 * HS units (the slices of a row
 // chunk are on one XCD, next to each other), and nothing but rows moves, so loads,
 // products and stores overlap all the way.
-// One barrier a chunk.  Waves 4 - 7 take it between a chunk's last products and their
-// gating, the others after both: of the two waves of a SIMD one gates while the other
-// multiplies.  Those last units are stored after the next chunk's rows have come and
-// before those of the one after are asked for, so that a wait for loads never waits
-// for young stores.
+// One barrier a chunk.  The last units of a chunk are stored after the next chunk's rows
+// have come and before those of the one after are asked for, so that a wait for loads
+// never waits for young stores.
 constexpr int kUnitThreads = 512;
 template <int KU>
 constexpr int kUnitRows = KU <= 4 ? 128 : 64;
@@ -214,7 +212,6 @@ __global__ __launch_bounds__(kUnitThreads) void gated_units_kernel(const GatedAr
     constexpr int kHalves = sizeof(T) == 1 ? 2 : 1, HS = kUnitSets<KU>, R = kUnitRows<KU>, kPer = R / 16 * KU / 8;
     constexpr int kBuffer = kUnitBuffer<T, KU>, kScales = R * KU * 64 * kHalves, kUnits = 256 * HS, kRounds = R / 16 / RF;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), row16 = lane & 15, group = lane >> 4;
-    const bool late = wave >= 4;
     const int xcd = blockIdx.x & 7, in_xcd = blockIdx.x >> 3;
     const int n0 = in_xcd % slices * slice_n, nn = a.n - n0 < slice_n ? a.n - n0 : slice_n;
     const int64_t walker = (int64_t)(in_xcd / slices) * 8 + xcd, walkers = (int64_t)(gridDim.x >> 3) / slices * 8;
@@ -381,10 +378,6 @@ __global__ __launch_bounds__(kUnitThreads) void gated_units_kernel(const GatedAr
                             }
                     }
             }
-            auto next = [&] {
-                if (++q < all) advance();
-            };
-            if (p == kRounds - 1 && late) next();
             if (first < nn) {
                 flush();
 #pragma unroll
@@ -400,8 +393,8 @@ __global__ __launch_bounds__(kUnitThreads) void gated_units_kernel(const GatedAr
                     }
                 pending = m0 + p * RF * 16;
             }
-            if (p == kRounds - 1 && !late) next();
         }
+        if (++q < all) advance();
     }
     flush();
 }
@@ -433,6 +426,164 @@ hipError_t rows_pick(const GatedArgs &a, hipStream_t stream) {
     return fits ? rows_launch<T, Y, KU, false>(a, p, stream) : units_launch<T, Y, KU, 2, false>(a, stream);
 }
 
+// Many rows, a contraction longer than a wave's registers hold: blocks of 256 rows by
+// 128 hidden units (256 rows of weights) over steps of 64 values of the contraction.
+// Eight waves make 128 rows by 32 units of both projections each.  A step's pieces lie
+// in LDS as fragments, in one of two buffers; the next step's are written into the
+// other, and those of the one after are on their way into registers, across the ends
+// of blocks too: one barrier a step, and a workgroup's next block begins while its last
+// one is gated.
+// The blocks of an XCD are dealt in runs, those of one row tile next to each other, so
+// x and the weights come from its L2 after their first reader.
+constexpr int kBlockRows = 256, kBlockUnits = 128, kBlockThreads = 512;
+template <typename T, typename Y, bool kPre>
+__global__ __launch_bounds__(kBlockThreads) void gated_block_kernel(const GatedArgs a, int tiles_n, int64_t tiles, int64_t per_xcd) {
+    extern __shared__ __attribute__((aligned(16))) char lds[];
+    constexpr int kHalves = sizeof(T) == 1 ? 2 : 1, kU = sizeof(T) == 1 ? 1 : 2;  // f16 fragments of a raw one; raw ones of a step
+    constexpr int kStep = 64, kSide = 16 * 2 * 1024, kBuffer = 2 * kSide;        // x's 16 row fragments, then the weights' 16
+    constexpr int kPer = 32 * kU / 8;                                             // raw fragments a wave brings
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), row16 = lane & 15, group = lane >> 4;
+    const int wm = wave & 1, wn = wave >> 1;
+    const int64_t walker = blockIdx.x >> 3, walkers = gridDim.x >> 3, base = (int64_t)(blockIdx.x & 7) * per_xcd;
+    const int64_t mine = tiles - base < per_xcd ? tiles - base : per_xcd;  // blocks of this XCD
+    if (walker >= mine) return;
+    const int steps = (a.k + kStep - 1) / kStep;
+    const int64_t all = ((mine - 1 - walker) / walkers + 1) * steps;
+
+    // What is fetched next: a block and a step of it.
+    int64_t next_tile = walker;
+    int next_k = 0;
+    u32x4 staged[kPer];
+    auto fetch = [&]() __attribute__((always_inline)) {
+        const int64_t tile = base + (next_tile < mine ? next_tile : mine - 1);
+        const int64_t m0 = tile / tiles_n * kBlockRows;
+        const int n0 = (int)(tile % tiles_n) * kBlockUnits;
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+            const int b = wave * (kPer / 2) + j % (kPer / 2), f = b / kU, u = b % kU;  // half of them x's, half the weights'
+            const int k = next_k + u * kStretch<T> + group * kPiece<T>, at = k + kPiece<T> <= a.k ? k : a.k - kPiece<T>;
+            const T *row;
+            if (j < kPer / 2) {
+                const int64_t m = m0 + f * 16 + row16;
+                row = (const T *)a.x + (m < a.m ? m : a.m - 1) * a.xs;
+            } else {
+                // 32 units: fragments of gate rows 2, of up rows 2
+                const int unit = n0 + (f >> 2) * 32 + (row16 >> 2) * 8 + (f & 1) * 4 + (row16 & 3), n = unit < a.n ? unit : a.n - 1;
+                row = f & 2 ? (const T *)a.wu + (int64_t)n * a.us : (const T *)a.wg + (int64_t)n * a.gs;
+            }
+            staged[j] = load_loose<u32x4>(row + at);
+        }
+        next_tile += next_k + kStep < a.k ? 0 : walkers;
+        next_k = next_k + kStep < a.k ? next_k + kStep : 0;
+    };
+    auto stage = [&](char *to, int k0) __attribute__((always_inline)) {
+        if (k0 + kStep > a.k)  // the step that the contraction's end cuts
+#pragma unroll
+            for (int j = 0; j < kPer; ++j)
+                staged[j] &= cut_piece<T>(k0 + (wave * (kPer / 2) + j % (kPer / 2)) % kU * kStretch<T> + group * kPiece<T>, a.k).mask;
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+            u32x4 *const p = (u32x4 *)(to + (j < kPer / 2 ? 0 : kSide)) + (wave * (kPer / 2) + j % (kPer / 2)) * kHalves * 64 + lane;
+            if constexpr (sizeof(T) == 1) {
+                const Widened v = widen(staged[j]);
+                p[0] = v.lo, p[64] = v.hi;
+            } else {
+                *p = staged[j];
+            }
+        }
+    };
+    auto barrier = [] {  // this wave's LDS writes are done, and so are the others'
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+    };
+
+    fetch();
+    stage(lds, 0);
+    fetch();
+    f32x4 acc[8][4];
+    int k0 = 0;
+    int64_t tile = walker;
+    for (int64_t q = 0; q < all; ++q) {
+        barrier();  // this step is in its buffer, and the last one's is done with
+        const int next = k0 + kStep < a.k ? k0 + kStep : 0;
+        stage(lds + ((q + 1) & 1) * kBuffer, next);
+        fetch();
+        if (k0 == 0)
+#pragma unroll
+            for (int r = 0; r < 8; ++r)
+#pragma unroll
+                for (int f = 0; f < 4; ++f) acc[r][f] = f32x4{0.f, 0.f, 0.f, 0.f};
+        const u32x4 *const x = (const u32x4 *)(lds + (q & 1) * kBuffer), *const w = (const u32x4 *)(lds + (q & 1) * kBuffer + kSide);
+        typedef std::conditional_t<sizeof(T) == 1, f16, T> P;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            u32x4 v[4];
+#pragma unroll
+            for (int f = 0; f < 4; ++f) v[f] = w[((wn * 4 + f) * 2 + u) * 64 + lane];
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+                const u32x4 t = x[((wm * 8 + r) * 2 + u) * 64 + lane];
+#pragma unroll
+                for (int f = 0; f < 4; ++f) acc[r][f] = mma16<P>(v[f], t, acc[r][f]);
+            }
+        }
+        k0 = next;
+        if (next) continue;
+        // The block is whole.
+        const int64_t at = base + tile, m0 = at / tiles_n * kBlockRows + wm * 128 + row16;
+        const int n = (int)(at % tiles_n) * kBlockUnits + wn * 32 + group * 8, left = a.n - n;
+        tile += walkers;
+        if (left <= 0) continue;
+        float bg[8], bu[8], sg[8], su[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int c = j < left ? n + j : n;
+            bg[j] = a.bg ? a.bg[c] : 0.f, bu[j] = a.bu ? a.bu[c] : 0.f;
+            if constexpr (sizeof(T) == 1) sg[j] = a.g_scale[c], su[j] = a.u_scale[c];
+        }
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+            const int64_t m = m0 + r * 16;
+            if (m >= a.m) continue;
+            float xs = 1.f;
+            if constexpr (sizeof(T) == 1) xs = a.x_scale[m];
+            float g[8], v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                g[j] = acc[r][j / 4][j % 4], v[j] = acc[r][2 + j / 4][j % 4];
+                if constexpr (sizeof(T) == 1) g[j] = fmaf(g[j] * xs, sg[j], bg[j]), v[j] = fmaf(v[j] * xs, su[j], bu[j]);
+                else g[j] += bg[j], v[j] += bu[j];
+            }
+            if constexpr (kPre) {
+                put((T *)a.gate + m * a.ps + n, left, rounded<8, T>(g));
+                put((T *)a.up + m * a.qs + n, left, rounded<8, T>(v));
+            }
+            gate_all(g, v, a.act);
+            put((Y *)a.h + m * a.hs + n, left, rounded<8, Y>(g));
+        }
+    }
+}
+
+template <typename T, typename Y, bool kPre>
+hipError_t block_launch(const GatedArgs &a, hipStream_t stream) {
+    const auto kernel = gated_block_kernel<T, Y, kPre>;
+    constexpr int bytes = 2 * 2 * 16 * 2 * 1024;
+    const hipError_t e = hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != hipSuccess) return e;
+    const int tiles_n = (int)div_up(a.n, kBlockUnits);
+    const int64_t tiles = div_up(a.m, kBlockRows) * tiles_n, per_xcd = div_up(tiles, 8);
+    const int64_t walkers = per_xcd < kCus / 8 ? per_xcd : kCus / 8;
+    kernel<<<dim3((unsigned)(walkers * 8)), kBlockThreads, bytes, stream>>>(a, tiles_n, tiles, per_xcd);
+    return hipGetLastError();
+}
+template <typename T, typename Y>
+hipError_t run_block(const GatedArgs &a, hipStream_t stream) {
+    if constexpr (sizeof(T) == 2)
+        if (a.gate) return block_launch<T, Y, true>(a, stream);
+    return block_launch<T, Y, false>(a, stream);
+}
+
 // Fragments of the contraction: those that are instantiated.
 template <typename T>
 int rows_fragments(const GatedArgs &a) {
@@ -454,7 +605,13 @@ hipError_t run_rows(const GatedArgs &a, hipStream_t stream) {
 
 template <typename T, typename Y>
 hipError_t gated_run(const GatedArgs &a, hipStream_t stream) {
-    if (a.m >= 1024 && rows_fragments<T>(a)) return run_rows<T, Y>(a, stream);
+    // The tile kernel reads both weights for every 16 rows, in whole 16 x 32 tiles; the
+    // others first bring weights in: some units' (6 us; at 2048 x 256 -> 128 7.8 against 5), or a step of 64 of the
+    // contraction at a time in 2.1 us.
+    const double tile_us = 2.5 + 4e-8 * (16 * div_up(a.m, 16)) * (double)(16 * div_up(a.n, 16)) * (32 * div_up(a.k, 32));
+    const double block_us = 7 + 2.1 * div_up(a.k, 64) * div_up(div_up(a.m, kBlockRows) * div_up(a.n, kBlockUnits), kCus);
+    if (rows_fragments<T>(a) ? tile_us > 6 : a.k >= kPiece<T> && tile_us > block_us)
+        return rows_fragments<T>(a) ? run_rows<T, Y>(a, stream) : run_block<T, Y>(a, stream);
     GatedArgs part = a;
     const int64_t most = 65535LL * 16;  // rows a grid's second dimension reaches
     for (int64_t m = 0; m < a.m; m += most) {
