@@ -36,8 +36,24 @@ struct LookupArgs {
     void *y;
 };
 
-// G lanes a row, 8 columns a lane at a time.
-template <typename T, typename Y, typename Id, int G>
+// A piece of a row of 16-bit values, past the caches.
+template <typename Y>
+__device__ __forceinline__ void stream8(Y *row, Columns c, const float (&v)[8]) {
+    if (c.drop >= 8) return;
+    typedef Y Y8 __attribute__((ext_vector_type(8)));
+    Y8 a;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) a[j] = (Y)v[j];
+    if constexpr (sizeof(Y) == 2) {
+        store_stream(row + c.at, __builtin_bit_cast(u32x4, a));
+    } else {
+        store_stream(row + c.at, f32x4{a[0], a[1], a[2], a[3]});
+        store_stream(row + c.at + 4, f32x4{a[4], a[5], a[6], a[7]});
+    }
+}
+
+// G lanes a row, 8 columns a lane at a time.  kStream: y is larger than the caches.
+template <typename T, typename Y, typename Id, int G, bool kStream>
 __global__ __launch_bounds__(kLookupThreads) void lookup_kernel(const LookupArgs a) {
     constexpr int kGroups = kLookupThreads / G;
     const int lane = threadIdx.x % G, pieces = (a.c + 7) / 8;
@@ -62,7 +78,11 @@ __global__ __launch_bounds__(kLookupThreads) void lookup_kernel(const LookupArgs
             for (int u = 0; u < kLookupRows; ++u) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) v[u][j] = known[u] ? v[u][j] * a.scale : 0.f;
-                if (r0 + u * kGroups < a.m) store8<G == 1>((Y *)a.y + (r0 + u * kGroups) * a.ys, col, a.c, v[u]);
+                if (r0 + u * kGroups < a.m) {
+                    Y *const row = (Y *)a.y + (r0 + u * kGroups) * a.ys;
+                    if constexpr (kStream) stream8(row, col, v[u]);
+                    else store8<G == 1>(row, col, a.c, v[u]);
+                }
             }
         }
     }
@@ -74,7 +94,9 @@ hipError_t lookup_pick(const LookupArgs &a, hipStream_t stream) {
     auto run = [&](auto g) {
         constexpr int G = decltype(g)::value;
         const int64_t need = div_up(a.m, (int64_t)kLookupThreads / G * kLookupRows), most = kCus * 16;
-        lookup_kernel<T, Y, Id, G><<<dim3((unsigned)(need < most ? need : most)), kLookupThreads, 0, stream>>>(a);
+        const dim3 grid((unsigned)(need < most ? need : most));
+        if (a.c >= 8 && a.m * a.c * (int64_t)sizeof(Y) > kStreamBytes) lookup_kernel<T, Y, Id, G, true><<<grid, kLookupThreads, 0, stream>>>(a);
+        else lookup_kernel<T, Y, Id, G, false><<<grid, kLookupThreads, 0, stream>>>(a);
     };
     if (pieces <= 1) run(std::integral_constant<int, 1>{});
     else if (pieces <= 2) run(std::integral_constant<int, 2>{});
@@ -142,7 +164,17 @@ __device__ __forceinline__ uint32_t key_of(const SortArgs &a, int i) {
     }
 }
 
-// Workgroup t < tiles: histogram of tile t's digits.  The others fill.
+// The lanes of the wave, of those in `lanes`, whose digit is this lane's.
+__device__ __forceinline__ uint64_t peers_of(uint32_t digit, int bits, uint64_t lanes) {
+    for (int bit = 0; bit < bits; ++bit) {
+        const uint64_t set = __ballot((digit >> bit) & 1);
+        lanes &= (digit >> bit) & 1 ? set : ~set;
+    }
+    return lanes;
+}
+
+// Workgroup t < tiles: histogram of tile t's digits, equal ones of a wave added by one
+// lane (ids often come in runs).  The others fill.
 template <typename Id>
 __global__ __launch_bounds__(kSortThreads) void count_kernel(const SortArgs a) {
     __shared__ uint32_t bins[kBins];
@@ -154,8 +186,12 @@ __global__ __launch_bounds__(kSortThreads) void count_kernel(const SortArgs a) {
     for (int i = threadIdx.x; i < digits; i += kSortThreads) bins[i] = 0;
     __syncthreads();
     const int end = a.m - blockIdx.x * a.tile < a.tile ? a.m : (blockIdx.x + 1) * a.tile;
-    for (int i = blockIdx.x * a.tile + threadIdx.x; i < end; i += kSortThreads)
-        atomicAdd(&bins[(key_of<Id>(a, i) >> a.shift) & (digits - 1)], 1u);
+    for (int i0 = blockIdx.x * a.tile + (int)(threadIdx.x & ~63u); i0 < end; i0 += kSortThreads) {
+        const int i = i0 + (int)(threadIdx.x & 63);
+        const uint32_t d = (key_of<Id>(a, i < end ? i : end - 1) >> a.shift) & (digits - 1);
+        const uint64_t peers = peers_of(d, a.bits, __ballot(i < end));
+        if (i < end && (peers & ((1ull << (threadIdx.x & 63)) - 1)) == 0) atomicAdd(&bins[d], (uint32_t)__popcll(peers));
+    }
     __syncthreads();
     for (int i = threadIdx.x; i < digits; i += kSortThreads) a.counts[blockIdx.x * kBins + i] = bins[i];
 }
@@ -164,7 +200,9 @@ __global__ __launch_bounds__(kSortThreads) void count_kernel(const SortArgs a) {
 // the tile and goes through it 64 keys at a time: a key's rank among the equal
 // digits of its 64 comes from one ballot a bit, and a counter for each wave and
 // digit in LDS carries on from there, so equal keys keep their order.  A tile that
-// is the only one needs no histograms of others.
+// is the only one needs no histograms of others.  Stretches of up to 512 keys stay in
+// registers between their histogram and their move.
+constexpr int kHeldKeys = 8;
 template <typename Id>
 __global__ __launch_bounds__(kSortThreads) void scatter_kernel(const SortArgs a) {
     __shared__ uint32_t at[kSortWaves][kBins], before[kSortThreads], total[kSortThreads], wave_sum[kSortWaves];
@@ -180,16 +218,41 @@ __global__ __launch_bounds__(kSortThreads) void scatter_kernel(const SortArgs a)
     const int have = a.m - t * a.tile < a.tile ? a.m - t * a.tile : a.tile;
     const int per = (have + kSortWaves * 64 - 1) / (kSortWaves * 64) * 64;
     const int begin = t * a.tile + (wave * per < have ? wave * per : have), end = t * a.tile + ((wave + 1) * per < have ? (wave + 1) * per : have);
-    for (int i = begin + lane; i < end; i += 64) atomicAdd(&at[wave][(key_of<Id>(a, i) >> a.shift) & mask], 1u);
+    const bool hold = per <= kHeldKeys * 64;
+    const uint64_t below = (1ull << lane) - 1;
+    uint32_t held[kHeldKeys], held_place[kHeldKeys], rank[kHeldKeys], equal[kHeldKeys];  // equal: of the first lane of its digit, else 0
+    if (hold) {
+#pragma unroll
+        for (int j = 0; j < kHeldKeys; ++j) {
+            if (begin + j * 64 >= end) break;
+            const int i = begin + j * 64 + lane, e = i < end ? i : t * a.tile;
+            held[j] = key_of<Id>(a, e);
+            if constexpr (__is_same(Id, uint32_t)) held_place[j] = a.places[e];
+            else held_place[j] = i;
+        }
+#pragma unroll
+        for (int j = 0; j < kHeldKeys; ++j) {
+            if (begin + j * 64 >= end) break;
+            const bool is = begin + j * 64 + lane < end;
+            const uint32_t d = (held[j] >> a.shift) & mask;
+            const uint64_t peers = peers_of(d, a.bits, __ballot(is));
+            rank[j] = __popcll(peers & below);
+            equal[j] = is && rank[j] == 0 ? __popcll(peers) : 0;
+            if (equal[j]) atomicAdd(&at[wave][d], equal[j]);
+        }
+    } else {
+        for (int i = begin + lane; i < end; i += 64) atomicAdd(&at[wave][(key_of<Id>(a, i) >> a.shift) & mask], 1u);
+    }
     __syncthreads();
     // of each digit: its entries in earlier tiles, and in all
     const int shares = kSortThreads / digits, digit = threadIdx.x & mask, share = threadIdx.x >> a.bits;
     uint32_t b = 0, all = 0;
     if (a.tiles == 1) {
         if (share == 0)
+#pragma unroll
             for (int w = 0; w < kSortWaves; ++w) all += at[w][digit];
     } else {
-#pragma unroll 4
+#pragma unroll 16
         for (int i = share; i < a.tiles; i += shares) {
             const uint32_t n = a.counts[i * kBins + digit];
             b += i < t ? n : 0;
@@ -212,31 +275,43 @@ __global__ __launch_bounds__(kSortThreads) void scatter_kernel(const SortArgs a)
     if ((int)threadIdx.x < digits) {
         uint32_t base = sum - all + b;
         for (int w = 0; w < wave; ++w) base += wave_sum[w];
-        for (int w = 0; w < kSortWaves; ++w) {  // counts of a wave's stretch become its counters' start
-            const uint32_t n = at[w][threadIdx.x];
+        uint32_t n[kSortWaves];  // counts of a wave's stretch become its counters' start
+#pragma unroll
+        for (int w = 0; w < kSortWaves; ++w) n[w] = at[w][threadIdx.x];
+#pragma unroll
+        for (int w = 0; w < kSortWaves; ++w) {
             at[w][threadIdx.x] = base;
-            base += n;
+            base += n[w];
         }
     }
     __syncthreads();
-    for (int i0 = begin; i0 < end; i0 += 64) {
-        const bool mine = i0 + lane < end;
-        const int i = mine ? i0 + lane : end - 1;
-        const uint32_t key = key_of<Id>(a, i), d = (key >> a.shift) & mask;
-        uint64_t peers = __ballot(mine);
-        for (int bit = 0; bit < a.bits; ++bit) {
-            const uint64_t set = __ballot((d >> bit) & 1);
-            peers &= (d >> bit) & 1 ? set : ~set;
-        }
-        const int rank = __popcll(peers & ((1ull << lane) - 1));
-        const uint32_t to = at[wave][d] + rank;
+    // A key to its place: its digit's counter and its rank; the first lane of the digit counts on.
+    auto move = [&](bool mine, uint32_t key, uint32_t place, uint32_t rank, uint32_t equal) __attribute__((always_inline)) {
+        const uint32_t d = (key >> a.shift) & mask, to = at[wave][d] + rank;
         wave_exchange();
-        if (mine && rank == 0) at[wave][d] += __popcll(peers);
+        if (equal) at[wave][d] = to + equal;
         wave_exchange();
         if (mine) {
             a.keys_out[to] = key;
-            if constexpr (__is_same(Id, uint32_t)) a.places_out[to] = a.places[i];
-            else a.places_out[to] = i;
+            a.places_out[to] = place;
+        }
+    };
+    if (hold) {
+#pragma unroll
+        for (int j = 0; j < kHeldKeys; ++j) {
+            if (begin + j * 64 >= end) break;
+            move(begin + j * 64 + lane < end, held[j], held_place[j], rank[j], equal[j]);
+        }
+    } else {
+        for (int i0 = begin; i0 < end; i0 += 64) {
+            const bool is = i0 + lane < end;
+            const int i = is ? i0 + lane : end - 1;
+            const uint32_t key = key_of<Id>(a, i);
+            uint32_t place = i;
+            if constexpr (__is_same(Id, uint32_t)) place = a.places[i];
+            const uint64_t peers = peers_of((key >> a.shift) & mask, a.bits, __ballot(is));
+            const uint32_t r = __popcll(peers & below);
+            move(is, key, place, r, is && r == 0 ? (uint32_t)__popcll(peers) : 0u);
         }
     }
 }
@@ -297,24 +372,35 @@ __global__ __launch_bounds__(kSumThreads) void sum_kernel(const SumArgs a) {
                 if (j >= col.drop && col.at + j < a.c) p[col.at + j] = (D)(a.accumulate ? (float)p[col.at + j] + v[j] : v[j]);
         }
     };
+    float acc[8] = {};
+    bool whole = false;
+    uint32_t whole_key = kNoKey;
     if (i0 < i1) {
-        uint32_t now = a.keys[i0];
-        const uint32_t next = i1 < a.m ? a.keys[i1] : kNoKey;
-        bool open = i0 > 0 && a.keys[i0 - 1] == now;  // the segment began before this slot
-        float acc[8] = {};
-        for (int64_t i = i0; i < i1 && now < (uint32_t)a.rows; i += kSumRows) {
-            uint32_t key[kSumRows];
-            float v[kSumRows][8];
+        uint32_t key[kSumRows], place[kSumRows];
+        auto entries = [&](int64_t i) __attribute__((always_inline)) {
 #pragma unroll
             for (int u = 0; u < kSumRows; ++u) {
                 const int64_t e = i + u < i1 ? i + u : i1 - 1;
-                key[u] = a.keys[e];
-                load8<G == 1>((const T *)a.dy + (int64_t)a.places[e] * a.dys, col, a.c, v[u]);
+                key[u] = a.keys[e], place[u] = a.places[e];
             }
+        };
+        entries(i0);
+        const uint32_t next = i1 < a.m ? a.keys[i1] : kNoKey, prev = i0 > 0 ? a.keys[i0 - 1] : kNoKey;
+        uint32_t now = key[0];
+        bool open = prev == now;  // the segment began before this slot
+        for (int64_t i = i0; i < i1 && now < (uint32_t)a.rows; i += kSumRows) {
+            uint32_t k[kSumRows];
+            float v[kSumRows][8];
+#pragma unroll
+            for (int u = 0; u < kSumRows; ++u) {
+                k[u] = key[u];
+                load8<G == 1>((const T *)a.dy + (int64_t)place[u] * a.dys, col, a.c, v[u]);
+            }
+            if (i + kSumRows < i1) entries(i + kSumRows);  // the next rows' while these are on their way
 #pragma unroll
             for (int u = 0; u < kSumRows; ++u) {
                 if (i + u >= i1) break;
-                if (key[u] != now) {
+                if (k[u] != now) {
                     if (open) {
 #pragma unroll
                         for (int j = 0; j < 8; ++j) first[slot][lane * 8 + j] = acc[j];
@@ -323,7 +409,7 @@ __global__ __launch_bounds__(kSumThreads) void sum_kernel(const SumArgs a) {
                     } else {
                         put8(now, acc);
                     }
-                    now = key[u];
+                    now = k[u];
 #pragma unroll
                     for (int j = 0; j < 8; ++j) acc[j] = 0.f;
                 }
@@ -331,11 +417,12 @@ __global__ __launch_bounds__(kSumThreads) void sum_kernel(const SumArgs a) {
                 for (int j = 0; j < 8; ++j) acc[j] += v[u][j];
             }
         }
-        if (now < (uint32_t)a.rows) {
+        whole = open && next == now && now < (uint32_t)a.rows;
+        if (now < (uint32_t)a.rows && !whole) {
             if (open) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) first[slot][lane * 8 + j] = acc[j];
-                if (lane == 0) first_key[slot] = now, through[slot] = next == now;
+                if (lane == 0) first_key[slot] = now;
             } else if (next == now) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) last[slot][lane * 8 + j] = acc[j];
@@ -344,28 +431,58 @@ __global__ __launch_bounds__(kSumThreads) void sum_kernel(const SumArgs a) {
                 put8(now, acc);
             }
         }
+        whole_key = now;
+    }
+    // Slots that lie within one segment: where all of a wave's do, they are one.
+    const bool together = G < 64 && __ballot(whole) == ~0ull;
+    if (together)
+#pragma unroll
+        for (int o = G; o < 64; o <<= 1)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) acc[j] += __shfl_xor(acc[j], o, 64);
+    if (whole && (!together || slot % (64 / G) == 0)) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) first[slot][lane * 8 + j] = acc[j];
+        if (lane == 0) first_key[slot] = whole_key, through[slot] = 1;
     }
     __syncthreads();
-    // The slots' ends, in order, one column a thread.
+    // The slots' ends, in order, one column a thread: only the slots that have some.
+    // Bit s % 64 of word s / 64: slot s has a first sum, it goes through, it has a last one.
+    constexpr int kWords = (kSlots + 63) / 64;
+    uint64_t some[kWords], passes[kWords], starts[kWords];
+    {
+        const int l = threadIdx.x & 63;
+#pragma unroll
+        for (int w = 0; w < kWords; ++w) {
+            const int s = w * 64 + l < kSlots ? w * 64 + l : kSlots - 1;
+            const bool is = w * 64 + l < kSlots;
+            some[w] = __ballot(is && first_key[s] != kNoKey);
+            passes[w] = __ballot(is && through[s]);
+            starts[w] = __ballot(is && last_key[s] != kNoKey);
+        }
+    }
     for (int k = threadIdx.x; k < G * 8; k += kSumThreads) {
         const int column = column_of(c0 + k, a.c);
         if (column < 0) continue;
-        bool before = true;   // the open segment began before this workgroup
+        bool before = (some[0] & 1) != 0;   // the open segment began before this workgroup
         float carry = 0.f;
-        uint32_t open = kNoKey;
-        for (int s = 0; s < kSlots; ++s) {
-            if (first_key[s] != kNoKey) {
-                open = first_key[s];
-                carry += first[s][k];
-                if (through[s]) continue;
-                if (before) a.heads[(int64_t)blockIdx.x * a.c + column] = carry;
-                else put_one<D>(a, open, column, carry);
-                carry = 0.f, open = kNoKey;
+        bool open = false;
+#pragma unroll
+        for (int w = 0; w < kWords; ++w)
+            for (uint64_t left = some[w] | starts[w]; left; left &= left - 1) {
+                const int bit = __builtin_ctzll(left), s = w * 64 + bit;
+                if (some[w] >> bit & 1) {
+                    carry += first[s][k];
+                    open = true;
+                    if (passes[w] >> bit & 1) continue;
+                    if (before) a.heads[(int64_t)blockIdx.x * a.c + column] = carry;
+                    else put_one<D>(a, first_key[s], column, carry);
+                    before = open = false;
+                }
+                if (starts[w] >> bit & 1) open = true, before = false, carry = last[s][k];
+                else carry = 0.f;
             }
-            before = false;
-            if (last_key[s] != kNoKey) open = last_key[s], carry = last[s][k];
-        }
-        if (open != kNoKey) (before ? a.heads : a.tails)[(int64_t)blockIdx.x * a.c + column] = carry;
+        if (open) (before ? a.heads : a.tails)[(int64_t)blockIdx.x * a.c + column] = carry;
     }
 }
 
@@ -380,11 +497,10 @@ __global__ __launch_bounds__(kSumThreads) void segment_join_kernel(const SumArgs
     if (end >= a.m) return;
     const uint32_t key = a.keys[end];
     if (key >= (uint32_t)a.rows || a.keys[end - 1] != key || (w > 0 && a.keys[end - per - 1] == key)) return;
-    int lo = w + 1, hi = groups - 1;  // the last workgroup whose first entry has this key
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) / 2;
-        if (a.keys[(int64_t)mid * per] == key) lo = mid;
-        else hi = mid - 1;
+    int lo = w;  // the last workgroup whose first entry has this key
+    for (int n = kSumThreads; n == kSumThreads; lo += n) {
+        const int z = lo + 1 + (int)threadIdx.x;
+        n = __syncthreads_count(z < groups && a.keys[(int64_t)z * per] == key);
     }
     const int lane = threadIdx.x % G, slot = threadIdx.x / G, c0 = blockIdx.y * kSumColumns;
     const Columns col = columns_of(c0 + lane * 8, a.c);
