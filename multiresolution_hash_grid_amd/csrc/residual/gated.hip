@@ -1,5 +1,7 @@
 // h = act(x Wg^T + bg) (x Wu^T + bu) and its backward: how the backward is cut, and
 // the operands' types, each in a source of its own.
+#include <math.h>
+
 #include "gated_grad.h"
 
 namespace hg {
@@ -11,11 +13,19 @@ GatedGradPlan plan_of(const hg_gated_grad &op) {
     p.units = op.n <= 64 ? 64 : 128;
     p.kt = op.k <= 64 ? 64 : op.k <= 128 ? 128 : 256;
     if (op.n < 8 || op.k < 8) p.units = p.kt = 64;  // rows shorter than a piece take the narrowest tiles
+    // Fewer tiles of dx than half the CUs: narrower ones, which work dg and du out again but
+    // bring fewer weights for each stretch of units (4096 x 256 -> 512: dx 56 us, 42 so).
     p.kp = p.kt / 32;
+    while (p.kp > 2 && div_up(op.m, 256) * div_up(op.k, p.kp * 32) < kCus / 2) p.kp /= 2;
     p.ny = (int)div_up(op.n, p.units), p.nz = (int)div_up(op.k, p.kt);
-    // One workgroup a CU over all tiles, and no more than there are steps.
+    // One workgroup a CU over all tiles, and no more than there are steps; fewer where a
+    // workgroup's partial sums (written and joined at some 5 MB/us) cost more than the steps
+    // (2 us each) it saves: at the least of steps / parts * 2 + parts * its partials.
     const int64_t steps = div_up(op.m, gate_rows(p.units, p.kt));
+    const double partial_us = (double)p.ny * p.nz * 2 * p.units * p.kt * 8 / 5e6;
     int64_t parts = kCus / (p.ny * p.nz);
+    const int64_t worth = (int64_t)sqrt(2. * (double)steps / partial_us);
+    if (parts > worth) parts = worth;
     if (parts > steps) parts = steps;
     p.parts = (int)(parts < 1 ? 1 : parts);
     if (!op.dwg) p.nz = 1;  // the biases' gradients need one column of tiles

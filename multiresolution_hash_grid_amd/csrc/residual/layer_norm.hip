@@ -404,9 +404,19 @@ __global__ __launch_bounds__(kThreads) void layer_dw_long_kernel(const LayerGrad
     if (a.want_db) store8<false>(part + (a.want_dw ? a.c : 0), at, a.c, db);
 }
 
+// Workgroups (and partial rows) of a backward: as those of the RMS norm, but of rows
+// that take a whole workgroup at least four each, where the card stays full: their
+// partial rows are as long as the rows, twice (2048 x 4096: 52 us, 28 so).
+int64_t layer_groups(int64_t m, int c) {
+    const int64_t most = grad_groups(m, c);
+    if (c > kNormHeld || grad_group(c) < kThreads || most <= kCus * 2) return most;
+    const int64_t want = div_up(m, 4) > kCus * 2 ? div_up(m, 4) : kCus * 2;
+    return want < most ? want : most;
+}
+
 template <typename T, int G, int I>
 void layer_grad_run(const LayerGradArgs &a, hipStream_t stream) {
-    layer_grad_kernel<T, G, I><<<dim3((unsigned)grad_groups(a.m, a.c)), kThreads, 0, stream>>>(a);
+    layer_grad_kernel<T, G, I><<<dim3((unsigned)layer_groups(a.m, a.c)), kThreads, 0, stream>>>(a);
 }
 
 template <typename T>
@@ -424,7 +434,7 @@ void layer_grad_pick(const LayerGradArgs &a, hipStream_t stream) {
         const int64_t most = kCus * 8;
         layer_grad_long_kernel<T><<<dim3((unsigned)(a.m < most ? a.m : most)), kThreads, 0, stream>>>(a);
         if (a.part)
-            layer_dw_long_kernel<T><<<dim3((unsigned)div_up(a.c, kThreads * 8), (unsigned)grad_groups(a.m, a.c)), kThreads, 0,
+            layer_dw_long_kernel<T><<<dim3((unsigned)div_up(a.c, kThreads * 8), (unsigned)layer_groups(a.m, a.c)), kThreads, 0,
                                       stream>>>(a);
     }
 }
@@ -444,7 +454,7 @@ hipError_t launch_layer_norm_forward(const hg_layer_norm &op, hipStream_t stream
 }
 
 size_t layer_norm_backward_bytes(const hg_layer_norm_grad &op) {
-    return (size_t)grad_groups(op.m, op.c) * op.c * outputs_of(op) * sizeof(float);
+    return (size_t)layer_groups(op.m, op.c) * op.c * outputs_of(op) * sizeof(float);
 }
 
 hipError_t launch_layer_norm_backward(const hg_layer_norm_grad &op, void *workspace, hipStream_t stream) {
@@ -459,7 +469,7 @@ hipError_t launch_layer_norm_backward(const hg_layer_norm_grad &op, void *worksp
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !outputs) return e;
     const int c = op.c * outputs;
-    dw_join_kernel<<<dim3((unsigned)div_up(c, 16)), 1024, 0, stream>>>((const float *)workspace, (int)grad_groups(op.m, op.c), c, op.dw,
+    dw_join_kernel<<<dim3((unsigned)div_up(c, 16)), 1024, 0, stream>>>((const float *)workspace, (int)layer_groups(op.m, op.c), c, op.dw,
                                                                        op.dw ? op.c : 0, op.db, op.accumulate);
     return hipGetLastError();
 }
