@@ -13,10 +13,19 @@ GatedGradPlan plan_of(const hg_gated_grad &op) {
     p.units = op.n <= 64 ? 64 : 128;
     p.kt = op.k <= 64 ? 64 : op.k <= 128 ? 128 : 256;
     if (op.n < 8 || op.k < 8) p.units = p.kt = 64;  // rows shorter than a piece take the narrowest tiles
-    // Fewer tiles of dx than half the CUs: narrower ones, which work dg and du out again but
-    // bring fewer weights for each stretch of units (4096 x 256 -> 512: dx 56 us, 42 so).
     p.kp = p.kt / 32;
-    while (p.kp > 2 && div_up(op.m, 256) * div_up(op.k, p.kp * 32) < kCus / 2) p.kp /= 2;
+    // Fewer tiles of dx than half the CUs: the units in slices, for at the least of
+    // stretches / slices * 3 us and what the slices' sums cost, written and joined.
+    const int64_t tiles = div_up(op.m, 256) * div_up(op.k, p.kp * 32), stretches = div_up(op.n, 32);
+    p.slices = 1;
+    if (op.dx && op.m > 0 && tiles < kCus / 2) {
+        int64_t want = (int64_t)sqrt(3. * (double)stretches * 5e6 / (8. * (double)op.m * op.k));
+        if (want > kCus / tiles) want = kCus / tiles;
+        if (want > stretches / 2) want = stretches / 2;
+        if (want > 1) p.slices = (int)want;
+    }
+    p.per = (int)div_up(stretches, p.slices);
+    p.slices = (int)div_up(stretches, p.per);
     p.ny = (int)div_up(op.n, p.units), p.nz = (int)div_up(op.k, p.kt);
     // One workgroup a CU over all tiles, and no more than there are steps; fewer where a
     // workgroup's partial sums (written and joined at some 5 MB/us) cost more than the steps
@@ -32,6 +41,10 @@ GatedGradPlan plan_of(const hg_gated_grad &op) {
     const size_t tile = 2 * (size_t)p.units;
     if (op.m > 0 && p.parts > 1)
         p.bytes = ((op.dwg ? (size_t)p.ny * p.nz * tile * p.kt : 0) + (op.dbg ? (size_t)p.ny * tile : 0)) * p.parts * sizeof(float);
+    if (p.slices > 1) {
+        p.dx_at = (p.bytes + 255) / 256 * 256;
+        p.bytes = p.dx_at + (size_t)p.slices * op.m * op.k * sizeof(float);
+    }
     return p;
 }
 

@@ -8,10 +8,11 @@ namespace res {
 
 // The weights' gradients: tiles of `units` hidden units (gate and up) by kt inputs,
 // ny x nz of them, each with `parts` workgroups over the rows.  dx: tiles of 256 rows
-// by kp * 32 inputs.
+// by kp * 32 inputs, the units in `slices` of `per` stretches of 32 (their sums from
+// dx_at on in the workspace, where there are several).
 struct GatedGradPlan {
-    int units, kt, ny, nz, parts, kp;
-    size_t bytes;
+    int units, kt, ny, nz, parts, kp, slices, per;
+    size_t dx_at, bytes;
 };
 // Rows of a step: the widest tile's sums leave registers for the pieces of 32.
 constexpr int gate_rows(int units, int kt) { return units == 128 && kt == 256 ? 32 : 64; }

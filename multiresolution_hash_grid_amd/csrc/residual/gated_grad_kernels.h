@@ -101,16 +101,17 @@ __device__ __forceinline__ void step_barrier() {
 // in flight and a wait for the older kind leaves the younger on its way.
 // kShort: rows of units or inputs may be shorter than a piece.
 template <typename T, int KP, bool kShort>
-__global__ __launch_bounds__(kGateThreads) void gated_dx_kernel(const GatedGradArgs a, int tiles_k, int64_t tiles_m) {
+__global__ __launch_bounds__(kGateThreads) void gated_dx_kernel(const GatedGradArgs a, int tiles_k, int64_t tiles_m, int slices, int per,
+                                                                   float *part) {
     extern __shared__ __attribute__((aligned(16))) char lds[];
     constexpr int C = KP * 32, kHalf = 32 * C * 2, kBuffer = 2 * kHalf, kPer = C / 64;  // pieces of a thread
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), row16 = lane & 15, group = lane >> 4;
     // workgroups b, b + 8, ... share an XCD: the tiles of the same rows do
     const int xcd = blockIdx.x & 7, in_xcd = blockIdx.x >> 3;
-    const int k0 = in_xcd % tiles_k * C;
-    const int64_t walker = (int64_t)(in_xcd / tiles_k) * 8 + xcd, walkers = (int64_t)(gridDim.x >> 3) / tiles_k * 8;
+    const int k0 = in_xcd % tiles_k * C, slice = in_xcd / tiles_k % slices, u0 = slice * per * 32;
+    const int64_t walker = (int64_t)(in_xcd / tiles_k / slices) * 8 + xcd, walkers = (int64_t)(gridDim.x >> 3) / tiles_k / slices * 8;
     if (walker >= tiles_m) return;
-    const int chunks = (a.n + 31) / 32;
+    const int units = a.n - u0 < per * 32 ? a.n - u0 : per * 32, chunks = (units + 31) / 32;  // of this slice
     const int64_t all = ((tiles_m - 1 - walker) / walkers + 1) * chunks;
 
     // This thread's pieces of a stretch's weights: one column, rows kStep apart of the
@@ -124,13 +125,13 @@ __global__ __launch_bounds__(kGateThreads) void gated_dx_kernel(const GatedGradA
     u32x4 staged[kPer];
     int ahead = 0;  // the units whose weights are fetched next
     auto fetch = [&]() __attribute__((always_inline)) {
-        const int t = thread(), w_row = t / kRow, room = a.n - 1 - ahead * 32;
+        const int t = thread(), w_row = t / kRow, room = units - 1 - ahead * 32;
         const Columns w_col = columns_of(k0 + t % kRow * 8, a.k);
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
             const int at = kPer == 1 ? w_row : j * kStep % 32 + w_row, row = kPer == 1 ? at & 31 : at;
             const bool up = kPer == 1 ? at >= 32 : j * kStep >= 32;
-            const T *const w = (const T *)(up ? a.wu : a.wg) + (int64_t)(ahead * 32 + (row < room ? row : room)) * (up ? a.us : a.gs);
+            const T *const w = (const T *)(up ? a.wu : a.wg) + (int64_t)(u0 + ahead * 32 + (row < room ? row : room)) * (up ? a.us : a.gs);
             staged[j] = load_columns<kShort>(w + w_col.at, w_col, a.k);
         }
         ahead = ahead + 1 < chunks ? ahead + 1 : 0;
@@ -146,7 +147,7 @@ __global__ __launch_bounds__(kGateThreads) void gated_dx_kernel(const GatedGradA
 #pragma unroll
             for (int j = 0; j < kPer; ++j) staged[j] = shifted(staged[j], drop);
         }
-        const int room = a.n - chunk * 32;
+        const int room = units - chunk * 32;
         if (room < 32)
 #pragma unroll
             for (int j = 0; j < kPer; ++j)
@@ -164,7 +165,7 @@ __global__ __launch_bounds__(kGateThreads) void gated_dx_kernel(const GatedGradA
     int64_t raw_tile = walker;
     int raw_chunk = 0;
     auto load = [&]() __attribute__((always_inline)) {  // the units after the last loaded ones
-        const Columns c = columns_of(raw_chunk * 32 + group * 8, a.n);
+        const Columns c = columns_of(u0 + raw_chunk * 32 + group * 8, a.n);
         const int64_t m = (raw_tile < tiles_m ? raw_tile : tiles_m - 1) * 256;
         const int last = a.m - m < 256 ? (int)(a.m - m) - 1 : 255;  // rows past the end read the last one
         const char *const dh = (const char *)a.dh + m * a.dhs * 2, *const g = (const char *)a.gate + m * a.ps * 2,
@@ -188,8 +189,8 @@ __global__ __launch_bounds__(kGateThreads) void gated_dx_kernel(const GatedGradA
             dz[0][r] = pack8<T>(dg);
             dz[1][r] = pack8<T>(du);
         }
-        if (chunk * 32 + 32 > a.n) {  // pieces that the rows' end cuts, and those past it
-            const int drop = columns_of(chunk * 32 + group * 8, a.n).drop;
+        if (u0 + chunk * 32 + 32 > a.n) {  // pieces that the rows' end cuts, and those past it
+            const int drop = columns_of(u0 + chunk * 32 + group * 8, a.n).drop;
 #pragma unroll
             for (int r = 0; r < 2; ++r)
 #pragma unroll
@@ -258,7 +259,20 @@ __global__ __launch_bounds__(kGateThreads) void gated_dx_kernel(const GatedGradA
                         float v[8];
 #pragma unroll
                         for (int j = 0; j < 8; ++j) v[j] = acc[p][j / 4][r][j % 4];
-                        if (m0 + r * 16 < a.m) put_piece((T *)a.dx + (m0 + r * 16) * a.dxs + k, left, pack8<T>(v));
+                        if (m0 + r * 16 >= a.m) continue;
+                        if (part) {
+                            float *const to = part + ((int64_t)slice * a.m + m0 + r * 16) * a.k + k;
+                            if (left >= 8) {
+                                store_loose(to, f32x4{v[0], v[1], v[2], v[3]});
+                                store_loose(to + 4, f32x4{v[4], v[5], v[6], v[7]});
+                            } else {
+#pragma unroll
+                                for (int j = 0; j < 8; ++j)
+                                    if (j < left) to[j] = v[j];
+                            }
+                        } else {
+                            put_piece((T *)a.dx + (m0 + r * 16) * a.dxs + k, left, pack8<T>(v));
+                        }
                     }
                 }
                 m0 += walkers * 256;
@@ -272,6 +286,18 @@ __global__ __launch_bounds__(kGateThreads) void gated_dx_kernel(const GatedGradA
     };
     if (wave & 2) walk(std::true_type{});
     else walk(std::false_type{});
+}
+
+// dx of few rows: the slices' sums, in order.
+template <typename T>
+__global__ __launch_bounds__(256) void dx_join_kernel(const GatedGradArgs a, const float *part, int slices) {
+    const int64_t values = a.m * a.k, step = (int64_t)gridDim.x * 256;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < values; i += step) {
+        float t = part[i];
+#pragma unroll 8
+        for (int s = 1; s < slices; ++s) t += part[(int64_t)s * values + i];
+        ((T *)a.dx)[i / a.k * a.dxs + i % a.k] = (T)t;
+    }
 }
 
 // Four values of dW, slots k .. k + 3 of slot n of a tile's 2 U (gate, then up),
@@ -469,6 +495,18 @@ __global__ __launch_bounds__(kGateThreads) void gated_dw_kernel(const GatedGradA
     }
 }
 
+// Four joined values, quad `local` of the tiles' dW or of the db, to their places.
+template <typename T, int U>
+__device__ __forceinline__ void gated_join_put(const GatedGradArgs &a, f32x4 t, int64_t local, int64_t per, bool weights, int kt, int nz) {
+    const int tile = (int)(local / per), e = (int)(local % per);
+    if (weights) {
+        const int frag = e / 64, l = e % 64;
+        put_gate_dw<T, U>(a, tile / nz * U, frag / (kt / 16) * 16 + (l & 15), tile % nz * kt + frag % (kt / 16) * 16 + (l >> 4) * 4, t);
+    } else {
+        for (int j = 0; j < 4; ++j) put_gate_db<U>(a, tile * U, e * 4 + j, t[j]);
+    }
+}
+
 // dW = (dW +) the partials' sum, rounded once; db alike.  A workgroup takes 16
 // groups of four values; 32 threads share the partials of each, and their sums
 // are added in order, eight and then four.
@@ -498,27 +536,41 @@ __global__ __launch_bounds__(512) void gated_join_kernel(const float *part, int 
     __syncthreads();
     if (share || q >= all) return;
     for (int i = 1; i < 4; ++i) t += lds[i][slot];
-    const int tile = (int)(local / per), e = (int)(local % per);
-    if (q < quads) {
-        const int frag = e / 64, l = e % 64;
-        put_gate_dw<T, U>(a, tile / nz * U, frag / (kt / 16) * 16 + (l & 15), tile % nz * kt + frag % (kt / 16) * 16 + (l >> 4) * 4, t);
-    } else {
-        for (int j = 0; j < 4; ++j) put_gate_db<U>(a, tile * U, e * 4 + j, t[j]);
-    }
+    gated_join_put<T, U>(a, t, local, per, q < quads, kt, nz);
+}
+// The same of few partials, a thread a group of four values.
+constexpr int kFewParts = 16;
+template <typename T, int U>
+__global__ __launch_bounds__(256) void gated_join_few_kernel(const float *part, int parts, int kt, int ny, int nz, GatedGradArgs a) {
+    constexpr int NT = 2 * U;
+    const int64_t quads = a.dwg ? (int64_t)ny * nz * NT * kt / 4 : 0, all = quads + (a.dbg ? ny * NT / 4 : 0);
+    const int64_t q = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 256 + threadIdx.x;
+    if (q >= all) return;
+    const int64_t per = q < quads ? NT * kt / 4 : NT / 4, local = q < quads ? q : q - quads;
+    const float *p = part + (q < quads ? 0 : quads * 4 * parts) + (local / per * per * parts + local % per) * 4;
+    f32x4 t = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+    for (int i = 0; i < parts; ++i) t += *(const f32x4 *)(p + i * per * 4);
+    gated_join_put<T, U>(a, t, local, per, q < quads, kt, nz);
 }
 
 template <typename T, int KP, bool kShort = false>
-hipError_t gated_dx_launch(const GatedGradArgs &a, hipStream_t stream) {
+hipError_t gated_dx_launch(const GatedGradArgs &a, const GatedGradPlan &p, float *part, hipStream_t stream) {
     const auto kernel = gated_dx_kernel<T, KP, kShort>;
     const int bytes = 2 * 2 * 32 * KP * 32 * 2, tiles_k = (int)div_up(a.k, KP * 32);
     if (bytes > 65536) {
         const hipError_t e = hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != hipSuccess) return e;
     }
-    const int64_t tiles_m = div_up(a.m, 256), most = kCus * (KP == 2 ? 2 : 1) / tiles_k;  // (registers of one or two workgroups a CU)
+    const int64_t tiles_m = div_up(a.m, 256), most = kCus * (KP == 2 ? 2 : 1) / (tiles_k * p.slices);  // (registers of one or two workgroups a CU)
     int64_t walkers = most < tiles_m ? most : tiles_m;
     walkers = div_up(walkers < 1 ? 1 : walkers, 8) * 8;  // whole rounds over the XCDs
-    kernel<<<dim3((unsigned)(walkers * tiles_k)), kGateThreads, bytes, stream>>>(a, tiles_k, tiles_m);
+    part = p.slices > 1 ? part : nullptr;
+    kernel<<<dim3((unsigned)(walkers * tiles_k * p.slices)), kGateThreads, bytes, stream>>>(a, tiles_k, tiles_m, p.slices, p.per, part);
+    if (part) {
+        const int64_t groups = div_up(a.m * a.k, 256);
+        dx_join_kernel<T><<<dim3((unsigned)(groups < kCus * 8 ? groups : kCus * 8)), 256, 0, stream>>>(a, part, p.slices);
+    }
     return hipGetLastError();
 }
 
@@ -550,13 +602,19 @@ hipError_t gated_grad_run(const GatedGradArgs &a, const GatedGradPlan &p, float 
     if ((a.dwg || a.dbg) && !(a.m > 0 && p.parts == 1)) {
         const int64_t quads = (a.dwg ? (int64_t)p.ny * p.nz * 2 * p.units * p.kt : 0) / 4 + (a.dbg ? p.ny * p.units / 2 : 0);
         const int parts = a.m > 0 ? p.parts : 0;
-        if (p.units == 128) gated_join_kernel<T, 128><<<grid_of(div_up(quads, 16)), 512, 0, stream>>>(part, parts, p.kt, p.ny, p.nz, a);
+        if (parts <= kFewParts) {
+            if (p.units == 128) gated_join_few_kernel<T, 128><<<grid_of(div_up(quads, 256)), 256, 0, stream>>>(part, parts, p.kt, p.ny, p.nz, a);
+            else gated_join_few_kernel<T, 64><<<grid_of(div_up(quads, 256)), 256, 0, stream>>>(part, parts, p.kt, p.ny, p.nz, a);
+        } else if (p.units == 128) gated_join_kernel<T, 128><<<grid_of(div_up(quads, 16)), 512, 0, stream>>>(part, parts, p.kt, p.ny, p.nz, a);
         else gated_join_kernel<T, 64><<<grid_of(div_up(quads, 16)), 512, 0, stream>>>(part, parts, p.kt, p.ny, p.nz, a);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     if (!a.dx || a.m == 0) return hipSuccess;
-    if (a.n < 8 || a.k < 8) return gated_dx_launch<T, 2, true>(a, stream);
-    return p.kp == 2 ? gated_dx_launch<T, 2>(a, stream) : p.kp == 4 ? gated_dx_launch<T, 4>(a, stream) : gated_dx_launch<T, 8>(a, stream);
+    float *const dx_part = (float *)((char *)part + p.dx_at);
+    if (a.n < 8 || a.k < 8) return gated_dx_launch<T, 2, true>(a, p, dx_part, stream);
+    return p.kp == 2 ? gated_dx_launch<T, 2>(a, p, dx_part, stream)
+           : p.kp == 4 ? gated_dx_launch<T, 4>(a, p, dx_part, stream)
+                       : gated_dx_launch<T, 8>(a, p, dx_part, stream);
 }
 
 }  // namespace
