@@ -33,6 +33,7 @@ int check_embedding(const hg_embedding *op) {
         return abi_fail(HG_EUNSUPPORTED, "y_dtype %d with table_dtype %d", op->y_dtype, op->table_dtype);
     if (op->m == 0) return HG_OK;
     if (op->rows > 0 && (rc = check_rows("table", op->table, op->table_stride, op->rows, op->c, op->table_dtype, true))) return rc;
+    if (op->rows > 0 && op->y == op->table) return abi_fail(HG_EINVAL, "y is a buffer of its own");
     return check_rows("y", op->y, op->y_stride, op->m, op->c, op->y_dtype, true);
 }
 
@@ -45,7 +46,9 @@ int check_embedding_grad(const hg_embedding_grad *op) {
         return abi_fail(HG_EUNSUPPORTED, "dtable_dtype %d with dy_dtype %d", op->dtable_dtype, op->dy_dtype);
     if (op->rows == 0) return HG_OK;
     if ((rc = check_rows("dtable", op->dtable, op->dtable_stride, op->rows, op->c, op->dtable_dtype, true))) return rc;
-    return op->m == 0 ? HG_OK : check_rows("dy", op->dy, op->dy_stride, op->m, op->c, op->dy_dtype, true);
+    if (op->m == 0) return HG_OK;
+    if (op->dtable == op->dy) return abi_fail(HG_EINVAL, "dtable is a buffer of its own");
+    return check_rows("dy", op->dy, op->dy_stride, op->m, op->c, op->dy_dtype, true);
 }
 
 int check_layer_norm(const hg_layer_norm *op) {
@@ -66,6 +69,7 @@ int check_layer_norm(const hg_layer_norm *op) {
     if ((rc = check_vector("y_scale", op->y_scale, eight)) || (rc = check_vector("mean", op->mean, false))) return rc;
     if ((rc = check_vector("rstd", op->rstd, false))) return rc;
     if (eight && (op->y == op->x || op->y == op->residual)) return abi_fail(HG_EINVAL, "y in place of x or residual needs their type");
+    if (op->mean && op->mean == op->rstd) return abi_fail(HG_EINVAL, "mean and rstd are one buffer");
     if (op->sum && op->sum == op->y) return abi_fail(HG_EINVAL, "sum and y are one buffer");
     if ((rc = check_in_place("y", op->y, op->y_stride, "x", op->x, op->x_stride, op->m))) return rc;
     if ((rc = check_in_place("y", op->y, op->y_stride, "residual", op->residual, op->residual_stride, op->m))) return rc;
@@ -89,6 +93,7 @@ int check_layer_norm_grad(const hg_layer_norm_grad *op) {
     if ((rc = check_in_place("dx", op->dx, op->dx_stride, "ds", op->ds, op->ds_stride, op->m))) return rc;
     if ((rc = check_vector("w", op->w, false)) || (rc = check_vector("mean", op->mean, rows))) return rc;
     if ((rc = check_vector("rstd", op->rstd, rows)) || (rc = check_vector("dw", op->dw, false))) return rc;
+    if (op->dw && op->dw == op->db) return abi_fail(HG_EINVAL, "dw and db are one buffer");
     return check_vector("db", op->db, false);
 }
 
@@ -115,6 +120,8 @@ int check_gated(const hg_gated *op) {
     if ((rc = check_rows("up", op->up, op->up_stride, op->m, op->n, op->x_dtype, false))) return rc;
     if (op->h == op->x || op->gate == op->h || op->up == op->h || (op->gate && op->gate == op->up))
         return abi_fail(HG_EINVAL, "h, gate, up and x are buffers of their own");
+    for (const void *p : {(const void *)op->h, (const void *)op->gate, (const void *)op->up})
+        if (p && (p == op->wg || p == op->wu || p == op->x)) return abi_fail(HG_EINVAL, "h, gate and up are no buffers of the operands");
     if ((rc = check_vector("x_scale", op->x_scale, eight)) || (rc = check_vector("g_scale", op->g_scale, eight))) return rc;
     if ((rc = check_vector("u_scale", op->u_scale, eight)) || (rc = check_vector("bg", op->bg, false))) return rc;
     return check_vector("bu", op->bu, false);
@@ -149,8 +156,11 @@ int check_gated_grad(const hg_gated_grad *op) {
     for (const auto &t : matrices)
         if (t.p && op->m > 1 && t.stride > kMaxGradStride)
             return abi_fail(HG_EINVAL, "%s: row stride %lld > 2^22", t.name, (long long)t.stride);
-    for (const void *p : {op->dh, op->gate, op->up, op->x})
-        if (rows && op->dx && op->dx == p) return abi_fail(HG_EINVAL, "dx is a buffer of its own");
+    for (const void *p : {(const void *)op->dh, op->gate, op->up, op->x, op->wg, op->wu})
+        for (const void *out : {(const void *)op->dx, (const void *)op->dwg, (const void *)op->dwu})
+            if (rows && out && out == p) return abi_fail(HG_EINVAL, "dx, dwg and dwu are buffers of their own");
+    if ((op->dwg && op->dwg == op->dwu) || (op->dbg && op->dbg == op->dbu))
+        return abi_fail(HG_EINVAL, "dwg and dwu, and dbg and dbu, are two buffers");
     if ((rc = check_vector("dbg", op->dbg, false))) return rc;
     return check_vector("dbu", op->dbu, false);
 }

@@ -40,7 +40,7 @@ LOOKUP = dict(m=4, rows=9, c=8, ids=P, table=P, table_stride=8, y=Q, y_stride=8,
     (dict(ids_bits=64, ids=P + 4), E, "aligned"), (dict(table=None), E, "table is NULL"), (dict(table=P + 2), E, "aligned"),
     (dict(table_stride=7), E, "stride"), (dict(y=None), E, "y is NULL"), (dict(y_stride=7), E, "stride"),
     (dict(table_dtype=R.HG_F8), U, "table_dtype"), (dict(table_dtype=B.HG_F16, y_dtype=B.HG_F32), U, "y_dtype"),
-    (dict(table_dtype=B.HG_F16, y_dtype=R.HG_BF16), U, "y_dtype"), (dict(y_dtype=R.HG_F8), U, "y_dtype"), (dict(y_dtype=9), U, "y_dtype"),
+    (dict(table_dtype=B.HG_F16, y_dtype=R.HG_BF16), U, "y_dtype"), (dict(y_dtype=R.HG_F8), U, "y_dtype"), (dict(y_dtype=9), U, "y_dtype"), (dict(y=P), E, "its own"),
 ])
 def test_embedding_forward_refuses(lib, change, code, word):
     refused(lib, "embedding", K._Embedding(**(LOOKUP | change)), code, word)
@@ -56,6 +56,7 @@ SORT = dict(m=4, rows=9, c=8, ids=P, dy=P, dy_stride=8, dtable=Q, dtable_stride=
     (dict(dy=P + 1), E, "aligned"), (dict(dy_stride=4), E, "stride"), (dict(dtable=None), E, "dtable is NULL"),
     (dict(dtable_stride=7), E, "stride"), (dict(dtable=Q + 2), E, "aligned"), (dict(dy_dtype=R.HG_F8), U, "dy_dtype"),
     (dict(dtable_dtype=R.HG_BF16), U, "dtable_dtype"), (dict(dy_dtype=B.HG_F32, dtable_dtype=B.HG_F16), U, "dtable_dtype"),
+    (dict(dtable=P), E, "its own"),
 ])
 def test_embedding_backward_refuses(lib, change, code, word):
     refused(lib, "embedding", K._EmbeddingGrad(**(SORT | change)), code, word, True)
@@ -72,20 +73,20 @@ NORM = dict(m=4, c=8, x=P, x_stride=8, w=P, b=P, y=Q, y_stride=8, eps=1e-5, dtyp
     (dict(x_stride=4), E, "stride"), (dict(residual=P, residual_stride=4), E, "stride"), (dict(sum=P + 1, sum_stride=8), E, "aligned"),
     (dict(mean=P + 1), E, "aligned"), (dict(rstd=P + 1), E, "aligned"), (dict(y=P, y_stride=16), E, "row stride"),
     (dict(sum=P, sum_stride=16), E, "row stride"), (dict(sum=Q, sum_stride=8), E, "one buffer"),
-    (dict(y=P, y_dtype=R.HG_F8, y_scale=P), E, "their type"),
+    (dict(y=P, y_dtype=R.HG_F8, y_scale=P), E, "their type"), (dict(mean=0x3000, rstd=0x3000), E, "one buffer"),
 ])
 def test_layer_norm_forward_refuses(lib, change, code, word):
     refused(lib, "layer_norm", K._LayerNorm(**(NORM | change)), code, word)
 
 
-NGRAD = dict(m=4, c=8, dy=P, dy_stride=8, sum=P, sum_stride=8, w=P, mean=P, rstd=P, dx=Q, dx_stride=8, dw=P, db=P, dtype=B.HG_F16)
+NGRAD = dict(m=4, c=8, dy=P, dy_stride=8, sum=P, sum_stride=8, w=P, mean=P, rstd=P, dx=Q, dx_stride=8, dw=0x3000, db=0x4000, dtype=B.HG_F16)
 
 
 @pytest.mark.parametrize("change,code,word", [
     (dict(m=-1), E, "m ="), (dict(c=0), E, "c ="), (dict(dtype=R.HG_F8), U, "dtype"), (dict(dy=None), E, "dy is NULL"),
     (dict(sum=None), E, "sum is NULL"), (dict(dx=None), E, "dx is NULL"), (dict(mean=None), E, "mean is NULL"),
     (dict(rstd=None), E, "rstd is NULL"), (dict(ds=P, ds_stride=4), E, "stride"), (dict(dw=P + 2), E, "aligned"), (dict(db=P + 2), E, "aligned"),
-    (dict(dx=P, dx_stride=9), E, "row stride"),
+    (dict(dx=P, dx_stride=9), E, "row stride"), (dict(dw=0x4000), E, "one buffer"),
     (dict(c=4097, dy_stride=4097, sum_stride=4097, dx=P, dx_stride=4097), E, "in place"),
 ])
 def test_layer_norm_backward_refuses(lib, change, code, word):
@@ -107,13 +108,14 @@ GATED = dict(m=4, k=8, n=8, x=P, x_stride=8, wg=P, wg_stride=8, wu=P, wu_stride=
     (dict(x_dtype=R.HG_F8, gate=0x3000, up=0x4000, gate_stride=8, up_stride=8), U, "kept"),
     (dict(x_dtype=R.HG_F8, g_scale=P, u_scale=P), E, "x_scale is NULL"), (dict(x_dtype=R.HG_F8, x_scale=P, u_scale=P), E, "g_scale is NULL"),
     (dict(x_dtype=R.HG_F8, x_scale=P, g_scale=P), E, "u_scale is NULL"), (dict(x_scale=P), E, "belong"), (dict(u_scale=P), E, "belong"),
+    (dict(x=0x3000, h=P), E, "operands"), (dict(gate=0x3000, up=P, gate_stride=8, up_stride=8), E, "operands"),
 ])
 def test_gated_forward_refuses(lib, change, code, word):
     refused(lib, "gated", K._Gated(**(GATED | change)), code, word)
 
 
 GGRAD = dict(m=4, k=8, n=8, dh=P, dh_stride=8, gate=P, up=P, gate_stride=8, up_stride=8, x=P, x_stride=8, wg=P, wu=P, wg_stride=8,
-             wu_stride=8, dx=Q, dx_stride=8, dwg=Q, dwu=Q, dwg_stride=8, dwu_stride=8, dbg=Q, dbu=Q, dtype=B.HG_F16, dw_dtype=B.HG_F32, act=2)
+             wu_stride=8, dx=Q, dx_stride=8, dwg=0x3000, dwu=0x4000, dwg_stride=8, dwu_stride=8, dbg=0x5000, dbu=0x6000, dtype=B.HG_F16, dw_dtype=B.HG_F32, act=2)
 
 
 @pytest.mark.parametrize("change,code,word", [
@@ -122,7 +124,8 @@ GGRAD = dict(m=4, k=8, n=8, dh=P, dh_stride=8, gate=P, up=P, gate_stride=8, up_s
     (dict(gate=None), E, "gate is NULL"), (dict(up=None), E, "up is NULL"), (dict(x=None), E, "x is NULL"), (dict(wg=None), E, "wg is NULL"),
     (dict(wu=None), E, "wu is NULL"), (dict(dwg=None), E, "together"), (dict(dbu=None), E, "together"), (dict(dwg_stride=4), E, "stride"),
     (dict(dx_stride=4), E, "stride"), (dict(dbg=P + 1), E, "aligned"), (dict(dh=P + 1), E, "aligned"),
-    (dict(x_stride=(1 << 22) + 1), E, "stride"), (dict(gate_stride=(1 << 22) + 1), E, "stride"), (dict(dx=P), E, "its own"),
+    (dict(x_stride=(1 << 22) + 1), E, "stride"), (dict(gate_stride=(1 << 22) + 1), E, "stride"), (dict(dx=P), E, "their own"),
+    (dict(dwg=P), E, "their own"), (dict(dwu=P), E, "their own"), (dict(dwu=0x3000), E, "two buffers"), (dict(dbu=0x5000), E, "two buffers"),
 ])
 def test_gated_backward_refuses(lib, change, code, word):
     refused(lib, "gated", K._GatedGrad(**(GGRAD | change)), code, word, True)

@@ -133,3 +133,35 @@ def test_inference_in_a_graph():
                 graph.replay()
                 torch.cuda.synchronize()
                 assert torch.equal(y, form(x, ids))
+
+
+def test_a_captured_training_pass():
+    torch.manual_seed(5)
+    head = hg.HashGridGatedHead(32, 64, 1, 4, codes=6, code_width=8)
+    x, ids = torch.randn(5000, 32, device=DEV, requires_grad=True), torch.randint(0, 6, (5000,), device=DEV)
+    c = torch.randn(5000, 4, device=DEV)
+    leaves = [x] + list(head.parameters())
+
+    def step():
+        y = head(x, ids)
+        return (y.detach(),) + torch.autograd.grad(y, leaves, c)  # (no graph lives on)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kept = step()
+    for _ in range(3):
+        with torch.no_grad():
+            x.normal_()
+            ids.random_(-1, 6)
+            c.normal_()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.detach().clone() for t in kept]
+        for a, b in zip(got, step()):
+            assert torch.equal(a, b)
