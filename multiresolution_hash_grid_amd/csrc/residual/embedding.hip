@@ -119,7 +119,10 @@ constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / 64;
 constexpr int kDigitBits = 9;                  // most of a pass
 constexpr int kBins = 1 << kDigitBits;
-constexpr int kTileKeys = 4096;                // least of a tile that is not the only one
+// A tile that is the only one needs no histograms of others: up to 4096 keys (14.4 us; four
+// tiles of 1024 18.0).  One among others has 1024 at least (2^15 keys of 16 bits: 44 us, with
+// 2048 46, with 4096 54).
+constexpr int kTileKeys = 4096, kLeastKeys = 1024;
 constexpr int kMaxTiles = 128;                 // each tile reads the histograms of all
 constexpr uint32_t kNoKey = 0xFFFFFFFFu;       // no key is as large
 
@@ -548,7 +551,7 @@ Plan plan_of(const hg_embedding_grad &op) {
     const int bits = 32 - __builtin_clz((unsigned)op.rows);
     p.passes = (int)div_up(bits, kDigitBits);
     p.tile = op.m <= kTileKeys ? (int)op.m : (int)(div_up(div_up(op.m, kMaxTiles), kSortThreads) * kSortThreads);
-    if (op.m > kTileKeys && p.tile < kTileKeys) p.tile = kTileKeys;
+    if (op.m > kTileKeys && p.tile < kLeastKeys) p.tile = kLeastKeys;
     p.tiles = (int)div_up(op.m, p.tile);
     size_t at = 0;
     auto take = [&](size_t bytes) {
@@ -612,6 +615,7 @@ hipError_t launch_embedding_backward(const hg_embedding_grad &op, void *workspac
         // (one row has no stride)
         s.fill = Fill{(char *)op.dtable, op.rows, op.c * e, op.rows > 1 ? op.dtable_stride * e : op.c * e, (int)(groups < 1024 ? groups : 1024)};
     }
+    const Fill whole = s.fill;
     if (op.m == 0) {
         if (op.accumulate) return hipSuccess;
         count_kernel<int32_t><<<dim3((unsigned)s.fill.groups), kSortThreads, 0, stream>>>(s);
@@ -623,16 +627,25 @@ hipError_t launch_embedding_backward(const hg_embedding_grad &op, void *workspac
     s.m = (int)op.m, s.tile = p.tile, s.tiles = p.tiles, s.rows = op.rows;
     const int bits = 32 - __builtin_clz((unsigned)op.rows);
     s.bits = (int)div_up(bits, p.passes);
+    int share = 0;
     for (int pass = 0; pass < p.passes; ++pass) {
         s.shift = pass * s.bits;
         s.keys_out = keys[pass & 1], s.places_out = places[pass & 1];
         s.keys = keys[~pass & 1], s.places = places[~pass & 1];
-        const dim3 fills((unsigned)(p.tiles + (pass == 0 ? s.fill.groups : 0))), none((unsigned)p.tiles);
-        const bool counted = p.tiles > 1;
+        // each launch of the sort fills its share of the table beside its tiles (2^17 x 256: 61 us, all in the first 64)
+        const int launches = p.passes * (p.tiles > 1 ? 2 : 1);
+        auto next = [&] {
+            if (whole.groups == 0) return dim3((unsigned)p.tiles);
+            const int64_t from = whole.rows * share / launches, to = whole.rows * (share + 1) / launches;
+            ++share;
+            s.fill.p = whole.p + from * whole.stride, s.fill.rows = to - from;
+            return dim3((unsigned)(p.tiles + s.fill.groups));
+        };
         auto run = [&](auto id) {
             typedef decltype(id) Id;
-            if (counted) count_kernel<Id><<<fills, kSortThreads, 0, stream>>>(s);
-            scatter_kernel<Id><<<counted ? none : fills, kSortThreads, 0, stream>>>(s);
+            dim3 grid;
+            if (p.tiles > 1) grid = next(), count_kernel<Id><<<grid, kSortThreads, 0, stream>>>(s);
+            grid = next(), scatter_kernel<Id><<<grid, kSortThreads, 0, stream>>>(s);
         };
         if (pass > 0) run(uint32_t{});
         else if (op.ids_bits == 64) run(int64_t{});
