@@ -14,11 +14,13 @@ GatedGradPlan plan_of(const hg_gated_grad &op) {
     p.kt = op.k <= 64 ? 64 : op.k <= 128 ? 128 : 256;
     if (op.n < 8 || op.k < 8) p.units = p.kt = 64;  // rows shorter than a piece take the narrowest tiles
     p.kp = p.kt / 32;
+    const bool one = op.n <= p.units && op.k <= p.kt && p.units * p.kt <= 128 * 128;
+    p.together = one && op.dx && op.dwg && op.m > 0;
     // Fewer tiles of dx than half the CUs: the units in slices, for at the least of
     // stretches / slices * 3 us and what the slices' sums cost, written and joined.
     const int64_t tiles = div_up(op.m, 256) * div_up(op.k, p.kp * 32), stretches = div_up(op.n, 32);
     p.slices = 1;
-    if (op.dx && op.m > 0 && tiles < kCus / 2) {
+    if (op.dx && op.m > 0 && !one && tiles < kCus / 2) {
         int64_t want = (int64_t)sqrt(3. * (double)stretches * 5e6 / (8. * (double)op.m * op.k));
         if (want > kCus / tiles) want = kCus / tiles;
         if (want > stretches / 2) want = stretches / 2;

@@ -12,6 +12,7 @@ namespace res {
 // dx_at on in the workspace, where there are several).
 struct GatedGradPlan {
     int units, kt, ny, nz, parts, kp, slices, per;
+    bool together;  // dx is made with the weights' gradients
     size_t dx_at, bytes;
 };
 // Rows of a step: the widest tile's sums leave registers for the pieces of 32.

@@ -337,7 +337,13 @@ __device__ __forceinline__ void put_gate_db(const GatedGradArgs &a, int n0, int 
 // others the other way around.  dW and db leave as one partial per workgroup, joined
 // in a fixed order by gated_join_kernel; a workgroup alone with its tile writes them
 // itself.
-template <typename T, int U, int KT, bool kShort>
+//
+// kDx: the tile holds all units and inputs, and dx is made here too, so that dh, g and
+// u are read once.  Both weights lie in LDS, their columns dealt as in gated_dx_kernel; a
+// wave has 16 of a step's rows and half of the inputs, and adds up in that kernel's
+// order, so that dx is the same with and without the weights' gradients.  A step's dx is stored after the next step's loads have come and before
+// those of the one after are asked for: a wait for loads never waits for young stores.
+template <typename T, int U, int KT, bool kShort, bool kDx>
 __global__ __launch_bounds__(kGateThreads) void gated_dw_kernel(const GatedGradArgs a, float *part) {
     constexpr int R = gate_rows(U, KT), NT = 2 * U, FN = NT / 64, FK = KT / 32;  // fragments of a wave
     constexpr int PN = U / 8, PK = KT / 8;                               // pieces of a row
@@ -419,6 +425,59 @@ __global__ __launch_bounds__(kGateThreads) void gated_dw_kernel(const GatedGradA
             __builtin_amdgcn_sched_barrier(0);  // one piece's values at a time: the registers hold no more
         }
     };
+    // dx of a step's rows.
+    constexpr int P = kDx ? KT / 64 : 1;  // pairs of input fragments of a wave
+    static_assert(!kDx || R == 64);
+    char *const weights = lds + 2 * kBuffer;
+    const int columns_w = columns_base<KT>(lane);
+    u32x4 dx[P];
+    if constexpr (kDx)
+        for (int i = threadIdx.x; i < NT * PK; i += kGateThreads) {
+            const int slot = i / PK, w_piece = i % PK, unit = slot < U ? slot : slot - U, row = unit < a.n ? unit : 0;
+            const T *const w = slot < U ? (const T *)a.wg + row * a.gs : (const T *)a.wu + row * a.us;
+            const Columns c = columns_of(w_piece * 8, a.k);
+            u32x4 v = shifted(load_columns<kShort>(w + c.at, c, a.k), c.drop & 7);
+            if (unit >= a.n) v = u32x4{0, 0, 0, 0};
+            const int to = tile_at<KT>(slot, (w_piece >> 2) * 4 + ((w_piece & 3) >> 1)) + (w_piece & 1) * 8;
+            *(u32x2 *)(weights + to) = u32x2{v[0], v[1]};
+            *(u32x2 *)(weights + (to ^ 32)) = u32x2{v[2], v[3]};
+        }
+    auto spread = [&](int turn) __attribute__((always_inline)) {
+        if constexpr (!kDx) return;
+        f32x4 d[P][2];
+#pragma unroll
+        for (int p = 0; p < P; ++p) d[p][0] = d[p][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+        const int z_at = turn * kBuffer + tile_at<NT>((wave & 3) * 16 + (lane & 15), lane >> 4);
+#pragma unroll
+        for (int s = 0; s < NT / 32; ++s) {  // 32 units of gate, then of up
+            const int slot = s / 2 * 32 + s % 2 * U;
+            u32x4 z = *(const u32x4 *)(lds + (z_at ^ (slot << 1)));
+            if (a.n % 8 && s / 2 * 32 + 32 > a.n) z = shifted(z, columns_of(s / 2 * 32 + (lane >> 4) * 8, a.n).drop & 7);  // (zeros past the units)
+#pragma unroll
+            for (int p = 0; p < P; ++p)
+#pragma unroll
+                for (int f = 0; f < 2; ++f)
+                    d[p][f] = mma<T>(columns_at<KT>(weights, columns_w, slot, ((wave >> 2) * P + p) * 2 + f), z, d[p][f]);
+        }
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            float v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = d[p][j / 4][j % 4];
+            dx[p] = pack8<T>(v);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    auto flush = [&](int64_t step) __attribute__((always_inline)) {
+        if constexpr (!kDx) return;
+        const int64_t m = step * R + (wave & 3) * 16 + (lane & 15);
+        if (m >= a.m) return;
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            const int k = ((wave >> 2) * P + p) * 32 + (lane >> 4) * 8;
+            put_piece((T *)a.dx + m * a.dxs + k, a.k - k, dx[p]);
+        }
+    };
     const int columns_n = columns_base<NT>(lane) ^ (2 * wn * FN << 4), columns_k = columns_base<KT>(lane) ^ (2 * wk * FK << 4);
     auto multiply = [&](int turn) __attribute__((always_inline)) {
         if (!a.dwg) return;
@@ -450,13 +509,18 @@ __global__ __launch_bounds__(kGateThreads) void gated_dw_kernel(const GatedGradA
         prepare(blockIdx.x, lds);
         fetch(blockIdx.x + by);
         int turn = 0;
+        int64_t last = blockIdx.x;
         for (int64_t step = blockIdx.x; step < steps; step += by, turn ^= 1) {
             step_barrier();  // this step's tiles are whole, and the last step's are done with
-            if constexpr (!decltype(late)::value) multiply(turn);
+            if constexpr (!decltype(late)::value) multiply(turn), spread(turn);
             prepare(step + by, lds + (turn ^ 1) * kBuffer);
+            if constexpr (!decltype(late)::value) flush(step);
+            else if (step != blockIdx.x) flush(step - by);
             fetch(step + 2 * by);
-            if constexpr (decltype(late)::value) multiply(turn);
+            if constexpr (decltype(late)::value) multiply(turn), spread(turn);
+            last = step;
         }
+        if constexpr (decltype(late)::value) flush(last);
     };
     if (wave & 2) walk(std::true_type{});
     else walk(std::false_type{});
@@ -576,8 +640,10 @@ hipError_t gated_dx_launch(const GatedGradArgs &a, const GatedGradPlan &p, float
 
 template <typename T, int U, int KT, bool kShort = false>
 hipError_t gated_dw_launch(const GatedGradArgs &a, const GatedGradPlan &p, float *part, hipStream_t stream) {
-    const auto kernel = gated_dw_kernel<T, U, KT, kShort>;
-    const int bytes = 2 * gate_rows(U, KT) * (2 * U + KT) * 2;
+    auto kernel = gated_dw_kernel<T, U, KT, kShort, false>;
+    int bytes = 2 * gate_rows(U, KT) * (2 * U + KT) * 2;
+    if constexpr (U * KT <= 128 * 128)
+        if (p.together) kernel = gated_dw_kernel<T, U, KT, kShort, true>, bytes += 2 * U * KT * 2;
     if (bytes > 65536) {
         const hipError_t e = hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != hipSuccess) return e;
@@ -609,7 +675,7 @@ hipError_t gated_grad_run(const GatedGradArgs &a, const GatedGradPlan &p, float 
         else gated_join_kernel<T, 64><<<grid_of(div_up(quads, 16)), 512, 0, stream>>>(part, parts, p.kt, p.ny, p.nz, a);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
-    if (!a.dx || a.m == 0) return hipSuccess;
+    if (!a.dx || a.m == 0 || p.together) return hipSuccess;
     float *const dx_part = (float *)((char *)part + p.dx_at);
     if (a.n < 8 || a.k < 8) return gated_dx_launch<T, 2, true>(a, p, dx_part, stream);
     return p.kp == 2 ? gated_dx_launch<T, 2>(a, p, dx_part, stream)
