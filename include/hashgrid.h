@@ -56,8 +56,8 @@ extern "C" {
 /* Element types. */
 #define HG_F32 0 /* IEEE binary32                                        */
 #define HG_F16 1 /* IEEE binary16 (storage only; all arithmetic is fp32) */
-/* The residual head's operators (hashgrid_linear_*, hashgrid_rms_norm_*,
- * hashgrid_adamw_step) also take: */
+/* The heads' operators (hashgrid_linear_*, hashgrid_rms_norm_*, hashgrid_adamw_step,
+ * hashgrid_embedding_*, hashgrid_layer_norm_*, hashgrid_gated_*) also take: */
 #define HG_BF16 2 /* bfloat16                                            */
 #define HG_F8 3   /* e4m3: 4 exponent bits (bias 7), 3 mantissa bits, no infinities, largest value 448 */
 

@@ -15,6 +15,9 @@
 //   3. a segment that crosses workgroups is joined by the workgroup it begins in.
 //
 // A frequent id so costs its rows' reads and no more: its sum is spread over the card.
+// A sort of small keys is bound by its launches and their latencies, one after another: the
+// gradient of 2^18 x 64 bf16 to 200 rows takes 30 us (count 4, move 11, sum 11, join 4; its
+// bytes 6.6), that of 2^15 x 512 to 50304 rows, two passes, 44 (its bytes 16).
 #include <type_traits>
 
 #include "device_types.h"
@@ -52,7 +55,9 @@ __device__ __forceinline__ void stream8(Y *row, Columns c, const float (&v)[8]) 
     }
 }
 
-// G lanes a row, 8 columns a lane at a time.  kStream: y is larger than the caches.
+// G lanes a row, 8 columns a lane at a time.  kStream: y is larger than the caches, and
+// stores pass them by (2^20 x 64 fp32 to bf16: 30 us, 4.6 TB/s, nearly all of it writes; 56
+// through the caches).
 template <typename T, typename Y, typename Id, int G, bool kStream>
 __global__ __launch_bounds__(kLookupThreads) void lookup_kernel(const LookupArgs a) {
     constexpr int kGroups = kLookupThreads / G;

@@ -4,9 +4,10 @@
 //   dg = dh u act'(g),  du = dh act(g)
 //   dx = dg Wg + du Wu,  dwg = dg^T x,  dwu = du^T x,  dbg, dbu = sums over the rows
 //
-// Two kernels read dh, g and u and each works dg and du out for itself, on their way
-// into a product: written once and read twice they would cost as many bytes, and a
-// workspace of two hidden layers.  They are rounded to the operands' type there, as
+// Blocks that one tile holds (up to 128 hidden units by 128 inputs, or 64 by 256) take one
+// pass.  Of larger ones two kernels read dh, g and u and each works dg and du out
+// for itself, on their way into a product: written once and read twice they would cost
+// as many bytes, and a workspace of two hidden layers.  They are rounded to the operands' type there, as
 // products of 16-bit operands need; the biases' gradients sum them unrounded.
 #pragma once
 
@@ -92,13 +93,17 @@ __device__ __forceinline__ void step_barrier() {
 // Wg and Wu lie in LDS, the next units' on their way into registers, and are read
 // transposed.  Their columns are dealt so that a lane ends with 8 consecutive inputs
 // of a row.
-// One barrier a stretch of units.  Between two of them waves 0 - 3 multiply first and
-// then work out the next dg and du, the others the other way around: of the two waves
-// of a SIMD one multiplies while the other computes.
+// One barrier a stretch of units.  Between two of them half of the waves multiply first
+// and then work out the next dg and du, the others the other way around: of the two
+// waves of a SIMD one multiplies while the other computes.
 // Both kinds of loads, weights and units, are asked for a stretch ahead and
 // unconditionally (past the end they repeat others): the two orders are loops of
 // their own and without branches around loads, so that the compiler can count those
 // in flight and a wait for the older kind leaves the younger on its way.
+// With few rows the units are cut into slices, whose sums dx_join_kernel adds
+// (256 rows, 256 -> 512: 18.7 + 4 us; the whole backward 40 instead of 57).
+// Bound by the gates' slopes and the products one after another (VALU 47 %, matrix units
+// 23 % busy): 2^18 rows, 256 -> 512 bf16 263 us; its bytes at the copy's rate take 179.
 // kShort: rows of units or inputs may be shorter than a piece.
 template <typename T, int KP, bool kShort>
 __global__ __launch_bounds__(kGateThreads) void gated_dx_kernel(const GatedGradArgs a, int tiles_k, int64_t tiles_m, int slices, int per,
@@ -136,9 +141,9 @@ __global__ __launch_bounds__(kGateThreads) void gated_dx_kernel(const GatedGradA
         }
         ahead = ahead + 1 < chunks ? ahead + 1 : 0;
     };
-    // (Columns past k become inputs that are not stored; units past n must be zero.)
-    // columns 8 b .. + 3 of 32 are columns 4 b .. of the pair's first fragment, the next four of its second;
-    // rows 16 apart lie alike
+    // Columns 8 b .. + 3 of 32 become columns 4 b .. of the pair's first fragment, the next
+    // four those of its second; rows 16 apart lie alike.  Columns past k become inputs
+    // that are not stored; units past n must be zero.
     auto stage = [&](char *to, int chunk) __attribute__((always_inline)) {
         const int t = thread(), w_row = t / kRow, w_piece = t % kRow;
         const int w_to = (kPer == 1 ? (w_row >> 5) * kHalf : 0) + tile_at<C>(w_row & 31, (w_piece >> 2) * 4 + ((w_piece & 3) >> 1)) + (w_piece & 1) * 8;
@@ -333,16 +338,22 @@ __device__ __forceinline__ void put_gate_db(const GatedGradArgs &a, int n0, int 
 // the biases, and lays them and x into LDS tiles, one of two sets; then each wave
 // adds the step's product to its part of dW, which stays in registers to the end
 // (4 x 2 waves over 2 U x KT).  Both operands are read transposed.  Between two
-// barriers waves 0 - 3 multiply this step first and prepare the next one then, the
-// others the other way around.  dW and db leave as one partial per workgroup, joined
+// barriers half of the waves multiply this step first and prepare the next one then,
+// the others the other way around.  dW and db leave as one partial per workgroup, joined
 // in a fixed order by gated_join_kernel; a workgroup alone with its tile writes them
 // itself.
 //
 // kDx: the tile holds all units and inputs, and dx is made here too, so that dh, g and
 // u are read once.  Both weights lie in LDS, their columns dealt as in gated_dx_kernel; a
 // wave has 16 of a step's rows and half of the inputs, and adds up in that kernel's
-// order, so that dx is the same with and without the weights' gradients.  A step's dx is stored after the next step's loads have come and before
-// those of the one after are asked for: a wait for loads never waits for young stores.
+// order, so that dx is the same with and without the weights' gradients.  A step's dx is
+// stored after the next step's loads have come and before those of the one after are
+// asked for: a wait for loads never waits for young stores.
+// (2^18 rows, 64 -> 128: 57 us and the join 6, 123 in two passes; 128 -> 128 87 and 154;
+// 65537 rows, 35 -> 93 f16 28 + 5, 48.)
+//
+// 2^18 rows, 256 -> 512 bf16 228 us without dx, and the join 17; its bytes at the copy's
+// rate take 179: bound by memory and, in part, by the slopes (VALU 52 %, matrix units 26 %).
 template <typename T, int U, int KT, bool kShort, bool kDx>
 __global__ __launch_bounds__(kGateThreads) void gated_dw_kernel(const GatedGradArgs a, float *part) {
     constexpr int R = gate_rows(U, KT), NT = 2 * U, FN = NT / 64, FK = KT / 32;  // fragments of a wave

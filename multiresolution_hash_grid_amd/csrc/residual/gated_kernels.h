@@ -11,6 +11,7 @@ namespace {
 // Few rows.  A workgroup computes 16 rows by 16 hidden units; its four waves share
 // the contraction and add their sums in LDS.  The rows of x, Wg and Wu come straight
 // from memory as fragments, so a single point costs one read of both weights.
+// Bound by the loads' latency: 1 x 256 -> 512 bf16 3.4 us, 256 rows of it 4.2.
 template <typename T, typename Y>
 __global__ __launch_bounds__(256) void gated_tile_kernel(const GatedArgs a) {
     __shared__ f32x4 sums[2][4][64];
@@ -58,7 +59,8 @@ __global__ __launch_bounds__(256) void gated_tile_kernel(const GatedArgs a) {
 // of gate rows and two of up rows, dealt so that a lane ends with 8 consecutive units
 // of both for each of its rows; a wave holds the fragments of 16 rows for all of the
 // contraction.  Sixteen waves of them hide each other's loads better than eight with 32
-// rows each (2^18 x 256 -> 128 51 us and 60, 65537 x 35 -> 93 8.9 and 12.3).
+// rows each (2^18 x 256 -> 128 51 us and 60, 65537 x 35 -> 93 8.9 and 12.3).  Bound by
+// memory and by the products that the loads wait for (2^18 x 256 -> 128: 4.0 TB/s).
 constexpr int kLdsBytes = 160 * 1024;
 template <typename T, int KU>
 constexpr int kSetBytes = 4 * KU * 1024 * (sizeof(T) == 1 ? 2 : 1) + 2 * 64 * 4;  // fragments, biases, scales
@@ -198,6 +200,10 @@ hipError_t rows_launch(const GatedArgs &a, const RowsPlan &p, hipStream_t stream
 // One barrier a chunk.  The last units of a chunk are stored after the next chunk's rows
 // have come and before those of the one after are asked for, so that a wait for loads
 // never waits for young stores.
+// Bound by the products and the gating, which the two waves of a SIMD hardly overlap
+// (matrix units 44 %, VALU 50 % busy): 2^20 x 256 -> 512 bf16 551 - 585 us, 0.94 - 1.0
+// PFLOP/s; 8-bit 2^17 x 512 -> 1024 257 - 286, where widening is VALU work too.  With both
+// projections kept by the writes: 2^18 x 256 -> 512 222 - 232 us, 4.1 TB/s, 806 MB written.
 constexpr int kUnitThreads = 512;
 template <int KU>
 constexpr int kUnitRows = KU <= 4 ? 128 : 64;
@@ -435,6 +441,8 @@ hipError_t rows_pick(const GatedArgs &a, hipStream_t stream) {
 // one is gated.
 // The blocks of an XCD are dealt in runs, those of one row tile next to each other, so
 // x and the weights come from its L2 after their first reader.
+// 2^16 x 1024 -> 1024 bf16 310 us, 0.89 PFLOP/s (2691 with the tile kernel): matrix units
+// 33 %, VALU 29 %, LDS 22 % busy; what is left are the steps' barriers and the blocks' ends.
 constexpr int kBlockRows = 256, kBlockUnits = 128, kBlockThreads = 512;
 template <typename T, typename Y, bool kPre>
 __global__ __launch_bounds__(kBlockThreads) void gated_block_kernel(const GatedArgs a, int tiles_n, int64_t tiles, int64_t per_xcd) {
@@ -606,8 +614,9 @@ hipError_t run_rows(const GatedArgs &a, hipStream_t stream) {
 template <typename T, typename Y>
 hipError_t gated_run(const GatedArgs &a, hipStream_t stream) {
     // The tile kernel reads both weights for every 16 rows, in whole 16 x 32 tiles; the
-    // others first bring weights in: some units' (6 us; at 2048 x 256 -> 128 7.8 against 5), or a step of 64 of the
-    // contraction at a time in 2.1 us.
+    // others first bring weights in: some units' (6 us: 256 x 256 -> 512 takes 4.2 with tiles, 512 rows of it 5.4 with
+    // weights in LDS), or a step of 64 of the contraction at a time in 2.1 us (1024 x 512 -> 512 takes 14.3 with tiles,
+    // 2048 rows of it 24 in blocks).
     const double tile_us = 2.5 + 4e-8 * (16 * div_up(a.m, 16)) * (double)(16 * div_up(a.n, 16)) * (32 * div_up(a.k, 32));
     const double block_us = 7 + 2.1 * div_up(a.k, 64) * div_up(div_up(a.m, kBlockRows) * div_up(a.n, kBlockUnits), kCus);
     if (rows_fragments<T>(a) ? tile_us > 6 : a.k >= kPiece<T> && tile_us > block_us)

@@ -10,6 +10,9 @@
 // sum is exact, have differences of 0.  Everything is fp32 between the loads and the
 // one rounding of each output; y is made from the unrounded s.  8-bit rows as the RMS
 // norm's.
+// Bound by memory: 2^18 x 256 bf16 with residual, s and statistics kept 104 us (5.2 TB/s),
+// 2^20 x 256 to 8 bits 270 (5.0); backward 2^18 x 256 110 (4.9), 200003 x 96 f16 39 (4.0, of it
+// 5 the launch that joins dw and db).
 #include "norm_common.h"
 
 namespace hg {
