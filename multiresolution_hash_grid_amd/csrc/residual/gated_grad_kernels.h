@@ -109,7 +109,8 @@ template <typename T, int KP, bool kShort>
 __global__ __launch_bounds__(kGateThreads) void gated_dx_kernel(const GatedGradArgs a, int tiles_k, int64_t tiles_m, int slices, int per,
                                                                    float *part) {
     extern __shared__ __attribute__((aligned(16))) char lds[];
-    constexpr int C = KP * 32, kHalf = 32 * C * 2, kBuffer = 2 * kHalf, kPer = C / 64;  // pieces of a thread
+    // A row of C weights and 32 bytes: eight rows in a row begin in different banks.
+    constexpr int C = KP * 32, S = C * 2 + 32, kHalf = 32 * S, kBuffer = 2 * kHalf, kPer = C / 64;  // kPer: pieces of a thread
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), row16 = lane & 15, group = lane >> 4;
     // workgroups b, b + 8, ... share an XCD: the tiles of the same rows do
     const int xcd = blockIdx.x & 7, in_xcd = blockIdx.x >> 3;
@@ -142,11 +143,14 @@ __global__ __launch_bounds__(kGateThreads) void gated_dx_kernel(const GatedGradA
         ahead = ahead + 1 < chunks ? ahead + 1 : 0;
     };
     // Columns 8 b .. + 3 of 32 become columns 4 b .. of the pair's first fragment, the next
-    // four those of its second; rows 16 apart lie alike.  Columns past k become inputs
-    // that are not stored; units past n must be zero.
+    // four those of its second.  Unit 8 g + 4 h + t lies in row 16 h + 4 g + t: the rows that
+    // a transposing read takes together, t of two g, are eight in a row, and all its
+    // places are one address and constants.  Columns past k become inputs that are not
+    // stored; units past n must be zero.
     auto stage = [&](char *to, int chunk) __attribute__((always_inline)) {
         const int t = thread(), w_row = t / kRow, w_piece = t % kRow;
-        const int w_to = (kPer == 1 ? (w_row >> 5) * kHalf : 0) + tile_at<C>(w_row & 31, (w_piece >> 2) * 4 + ((w_piece & 3) >> 1)) + (w_piece & 1) * 8;
+        const int w_to = (kPer == 1 ? (w_row >> 5) * kHalf : 0) + ((w_row >> 2 & 1) * 16 + (w_row >> 3 & 3) * 4 + (w_row & 3)) * S +
+                         (w_piece >> 2) * 64 + (w_piece & 3) * 8;
         if (a.k % 8) {
             const int drop = columns_of(k0 + w_piece * 8, a.k).drop & 7;
 #pragma unroll
@@ -159,9 +163,9 @@ __global__ __launch_bounds__(kGateThreads) void gated_dx_kernel(const GatedGradA
                 if (((kPer == 1 ? 0 : j * kStep % 32) + w_row) % 32 >= room) staged[j] = u32x4{0, 0, 0, 0};
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
-            const int skip = j * kStep / 32 * kHalf + j * kStep % 32 * (C * 2);
+            const int skip = j * kStep / 32 * kHalf + j * kStep % 32 / 2 * S;  // (units 16 on: 8 rows)
             *(u32x2 *)(to + w_to + skip) = u32x2{staged[j][0], staged[j][1]};
-            *(u32x2 *)(to + (w_to ^ 32) + skip) = u32x2{staged[j][2], staged[j][3]};
+            *(u32x2 *)(to + w_to + skip + 32) = u32x2{staged[j][2], staged[j][3]};
         }
     };
 
@@ -203,7 +207,7 @@ __global__ __launch_bounds__(kGateThreads) void gated_dx_kernel(const GatedGradA
         }
     };
 
-    const int columns = columns_base<C>(lane);
+    const int columns = (group * 4 + (row16 >> 2)) * S + (row16 & 3) * 8;
     f32x4 acc[KP][2][2];  // pairs, fragments of a pair, row fragments
     int64_t m0 = walker * 256 + wave * 32 + row16;
     auto walk = [&](auto late) __attribute__((always_inline)) {
@@ -237,12 +241,18 @@ __global__ __launch_bounds__(kGateThreads) void gated_dx_kernel(const GatedGradA
                     for (int f = 0; f < 2; ++f) acc[p][f][0] = acc[p][f][1] = f32x4{0.f, 0.f, 0.f, 0.f};
             // A weight fragment is read kAhead fragments before its products, and no earlier:
             // the registers hold no more.
-            constexpr int kAll = 4 * KP, kAhead = KP == 8 ? 2 : 4;
+            constexpr int kAll = 4 * KP, kAhead = 4;
             u32x4 w[kAhead];
-            int at = columns + (int)(q & 1) * kBuffer;
-            asm volatile("" : "+v"(at));  // each fragment's place is worked out anew: held, they would cost registers
+            char *const at = lds + columns + (int)(q & 1) * kBuffer;
             auto read = [&](int i) __attribute__((always_inline)) {
-                w[i % kAhead] = columns_at<C>(lds + i / (2 * KP) * kHalf, at, 0, i % (2 * KP));
+                union {
+                    s16x4 h[2];
+                    u32x4 v;
+                } r;
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    r.h[h] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(at + i / (2 * KP) * kHalf + i % (2 * KP) * 32 + h * 16 * S));
+                w[i % kAhead] = r.v;
             };
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) read(i);
@@ -613,8 +623,10 @@ __global__ __launch_bounds__(512) void gated_join_kernel(const float *part, int 
     for (int i = 1; i < 4; ++i) t += lds[i][slot];
     gated_join_put<T, U>(a, t, local, per, q < quads, kt, nz);
 }
-// The same of few partials, a thread a group of four values.
-constexpr int kFewParts = 16;
+// The same of few partials, a thread a group of four values (24 partials of 256 -> 512,
+// 4096 rows: 58.6 us with dW and dx, 63.8 with the other join; 256 of 64 -> 128, 2^18 rows: 69
+// and 62).
+constexpr int kFewParts = 64;
 template <typename T, int U>
 __global__ __launch_bounds__(256) void gated_join_few_kernel(const float *part, int parts, int kt, int ny, int nz, GatedGradArgs a) {
     constexpr int NT = 2 * U;
@@ -632,7 +644,7 @@ __global__ __launch_bounds__(256) void gated_join_few_kernel(const float *part, 
 template <typename T, int KP, bool kShort = false>
 hipError_t gated_dx_launch(const GatedGradArgs &a, const GatedGradPlan &p, float *part, hipStream_t stream) {
     const auto kernel = gated_dx_kernel<T, KP, kShort>;
-    const int bytes = 2 * 2 * 32 * KP * 32 * 2, tiles_k = (int)div_up(a.k, KP * 32);
+    const int bytes = 2 * 2 * 32 * (KP * 32 * 2 + 32), tiles_k = (int)div_up(a.k, KP * 32);
     if (bytes > 65536) {
         const hipError_t e = hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != hipSuccess) return e;
