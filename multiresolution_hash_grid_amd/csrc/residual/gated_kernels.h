@@ -209,13 +209,16 @@ template <int KU>
 constexpr int kUnitRows = KU <= 4 ? 128 : 64;
 template <typename T, int KU>
 constexpr int kUnitBuffer = kUnitRows<KU> * (KU * 64 * (sizeof(T) == 1 ? 2 : 1) + 4);  // fragments, scales
-template <int KU>
-constexpr int kUnitSets = KU <= 2 ? 2 : 1;  // 32 hidden units each, of a wave
+// Sets of 32 hidden units of a wave: two where registers hold their weights, sums and
+// outputs (2^18 x 64 -> 1024 bf16 145 us, one set 153; 8-bit x 128 -> 1024 to fp32, with whose
+// second set they spill, 293 and 339).
+template <typename T, typename Y, int KU>
+constexpr int kUnitSets = KU <= (sizeof(T) == 1 && sizeof(Y) == 4 ? 1 : 2) ? 2 : 1;
 
 template <typename T, typename Y, int KU, int RF, bool kPre>
 __global__ __launch_bounds__(kUnitThreads) void gated_units_kernel(const GatedArgs a, int slices, int slice_n, int64_t tiles) {
     extern __shared__ __attribute__((aligned(16))) char lds[];
-    constexpr int kHalves = sizeof(T) == 1 ? 2 : 1, HS = kUnitSets<KU>, R = kUnitRows<KU>, kPer = R / 16 * KU / 8;
+    constexpr int kHalves = sizeof(T) == 1 ? 2 : 1, HS = kUnitSets<T, Y, KU>, R = kUnitRows<KU>, kPer = R / 16 * KU / 8;
     constexpr int kBuffer = kUnitBuffer<T, KU>, kScales = R * KU * 64 * kHalves, kUnits = 256 * HS, kRounds = R / 16 / RF;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), row16 = lane & 15, group = lane >> 4;
     const int xcd = blockIdx.x & 7, in_xcd = blockIdx.x >> 3;
@@ -409,7 +412,7 @@ template <typename T, typename Y, int KU, int RF, bool kPre>
 hipError_t units_launch(const GatedArgs &a, hipStream_t stream) {
     const auto kernel = gated_units_kernel<T, Y, KU, RF, kPre>;
     const int64_t tiles = div_up(a.m, kUnitRows<KU>);
-    constexpr int most = 256 * kUnitSets<KU>;
+    constexpr int most = 256 * kUnitSets<T, Y, KU>;
     int slices = (int)div_up(a.n, most);
     const int slice_n = (int)div_up(div_up(a.n, slices), 32) * 32;
     const int bytes = 2 * kUnitBuffer<T, KU> + 2 * most * 4 * (sizeof(T) == 1 ? 2 : 1);

@@ -123,3 +123,14 @@ def test_calls_on_two_streams():
                 got.append(work(*s))
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for p, q in zip(got, want) for a, b in zip(p, q))
+
+
+@pytest.mark.parametrize("m,k,n", [(9001, 128, 1024), (5003, 100, 700), (3001, 512, 300), (4001, 64, 1100)])
+def test_gated_8bit_to_f32(m, k, n):
+    g = torch.Generator().manual_seed(k)
+    x, wg, wu = rows(g, m, k, F8, 20.0), rows(g, n, k, F8, 20.0), rows(g, n, k, F8, 20.0)
+    b = [torch.randn(n, generator=g).to(DEV) for _ in range(2)]
+    xs, gs, us = ((torch.rand(i, generator=g) * s).to(DEV) for i, s in ((m, 0.1), (n, k ** -0.5), (n, k ** -0.5)))
+    h = hg.hashgrid_gated_forward(x, wg, wu, *b, act="gelu_tanh", out_dtype=F32, x_scale=xs, gate_scale=gs, up_scale=us)
+    wh, _, _, eh, _, _ = K.gated(x, wg, wu, *b, "gelu_tanh", xs, gs, us, F32)
+    R.within(h, wh, eh)
