@@ -76,14 +76,19 @@ __global__ __launch_bounds__(1024) void gated_rows_kernel(const GatedArgs a, int
     const int n0 = in_xcd % slices * slice_n, nn = a.n - n0 < slice_n ? a.n - n0 : slice_n;
     const int64_t walker = (int64_t)(in_xcd / slices) * 8 + xcd, walkers = (int64_t)(gridDim.x >> 3) / slices * 8;
     const int sets = (nn + 31) / 32;
+    // Piece u of a row of k values; one shorter than a piece lies in the first group's.
+    auto piece = [&](const T *row, int u, int k) __attribute__((always_inline)) {
+        if (KU == 1 && k < kPiece<T>) return group ? u32x4{0, 0, 0, 0} : load_short(row, k);
+        const Cut<T> c = cut_piece<T>(u * kStretch<T> + group * kPiece<T>, k);
+        return load_loose<u32x4>(row + c.at) & c.mask;
+    };
 
     for (int b = wave; b < sets * 4 * KU; b += waves) {
         const int s = b / (4 * KU), f = b / KU % 4, u = b % KU;
         const int unit = s * 32 + (row16 >> 2) * 8 + (f & 1) * 4 + (row16 & 3);
         const int64_t n = n0 + (unit < nn ? unit : nn - 1);
         const T *const w = f >> 1 ? (const T *)a.wu + n * a.us : (const T *)a.wg + n * a.gs;
-        const Cut<T> c = cut_piece<T>(u * kStretch<T> + group * kPiece<T>, a.k);
-        const u32x4 v = load_loose<u32x4>(w + c.at) & c.mask;
+        const u32x4 v = piece(w, u, a.k);
         u32x4 *const to = (u32x4 *)(lds + s * kSetBytes<T, KU>) + (b - s * 4 * KU) * kHalves * 64 + lane;
         if constexpr (sizeof(T) == 1) {
             const Widened x = widen(v);
@@ -109,10 +114,7 @@ __global__ __launch_bounds__(1024) void gated_rows_kernel(const GatedArgs a, int
         int k = a.k;
         asm volatile("" : "+s"(k));  // where pieces are cut is worked out anew for each tile: held, it would cost registers
 #pragma unroll
-        for (int u = 0; u < KU; ++u) {
-            const Cut<T> c = cut_piece<T>(u * kStretch<T> + group * kPiece<T>, k);
-            x[u] = load_loose<u32x4>((const T *)a.x + mr * a.xs + c.at) & c.mask;
-        }
+        for (int u = 0; u < KU; ++u) x[u] = piece((const T *)a.x + mr * a.xs, u, k);
         if constexpr (sizeof(T) == 1) xsc = a.x_scale[mr];
         for (int s = 0; s < sets; ++s) {
             const char *const buffer = lds + s * kSetBytes<T, KU>;
@@ -595,11 +597,13 @@ hipError_t run_block(const GatedArgs &a, hipStream_t stream) {
     return block_launch<T, Y, false>(a, stream);
 }
 
-// Fragments of the contraction: those that are instantiated.
+// Fragments of the contraction: those that are instantiated.  0: more, or rows shorter than a
+// piece and weights too large for LDS.
 template <typename T>
 int rows_fragments(const GatedArgs &a) {
     const int64_t u = div_up(a.k, kStretch<T>);
-    return a.k < kPiece<T> || u > 8 ? 0 : u <= 4 ? (int)u : u <= 6 ? 6 : 8;
+    if (a.k < kPiece<T> && rows_plan<T, 1>(a).bytes > kLdsBytes) return 0;
+    return u > 8 ? 0 : u <= 4 ? (int)u : u <= 6 ? 6 : 8;
 }
 
 template <typename T, typename Y>

@@ -134,3 +134,25 @@ def test_gated_8bit_to_f32(m, k, n):
     h = hg.hashgrid_gated_forward(x, wg, wu, *b, act="gelu_tanh", out_dtype=F32, x_scale=xs, gate_scale=gs, up_scale=us)
     wh, _, _, eh, _, _ = K.gated(x, wg, wu, *b, "gelu_tanh", xs, gs, us, F32)
     R.within(h, wh, eh)
+
+
+# rows shorter than a piece (8 values, 16 of 8 bits): with weights that LDS holds, and without
+@pytest.mark.parametrize("k", [1, 3, 7, 15])
+@pytest.mark.parametrize("m,n", [(70001, 64), (9001, 35), (5003, 1300)])
+@pytest.mark.parametrize("dtype", [F16, BF16, F8])
+def test_gated_of_few_inputs(m, k, n, dtype):
+    g = torch.Generator().manual_seed(m + k)
+    eight = dtype == F8
+    x, wg, wu = (rows(g, i, k, dtype, 20.0 if eight else 1.0) for i in (m, n, n))
+    b = [torch.randn(n, generator=g).to(DEV) for _ in range(2)]
+    sc = [(torch.rand(i, generator=g) * 0.1).to(DEV) for i in (m, n, n)] if eight else [None] * 3
+    out = BF16 if eight else dtype
+    h = hg.hashgrid_gated_forward(x, wg, wu, *b, out_dtype=out, x_scale=sc[0], gate_scale=sc[1], up_scale=sc[2])
+    at = torch.cat([torch.arange(500), torch.randint(0, m, (1500,), generator=g), torch.arange(m - 500, m)]).to(DEV)
+    wh, zg, zu, eh, eg, eu = K.gated(x[at], wg, wu, *b, "silu", sc[0][at] if eight else None, sc[1], sc[2], out)
+    R.within(h[at], wh, eh)
+    if not eight:
+        h2, gate, up = hg.hashgrid_gated_forward(x, wg, wu, *b, save_pre=True)
+        assert torch.equal(h2, h)
+        R.within(gate[at], zg, R.rounded(zg, eg, dtype))
+        R.within(up[at], zu, R.rounded(zu, eu, dtype))
