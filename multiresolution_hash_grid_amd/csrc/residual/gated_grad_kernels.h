@@ -102,8 +102,9 @@ __device__ __forceinline__ void step_barrier() {
 // in flight and a wait for the older kind leaves the younger on its way.
 // With few rows the units are cut into slices, whose sums dx_join_kernel adds
 // (256 rows, 256 -> 512: 18.7 + 4 us; the whole backward 40 instead of 57).
-// Bound by the gates' slopes and the products one after another (VALU 47 %, matrix units
-// 23 % busy): 2^18 rows, 256 -> 512 bf16 263 us; its bytes at the copy's rate take 179.
+// 2^18 rows, 256 -> 512 bf16 254 us; its bytes at the copy's rate take 179.  Bound by the
+// loads of one stretch on their way (48 KB a workgroup; a second stretch's leave no
+// registers), less by the slopes and the products (VALU 47 %, matrix units 23 % busy).
 // kShort: rows of units or inputs may be shorter than a piece.
 template <typename T, int KP, bool kShort>
 __global__ __launch_bounds__(kGateThreads) void gated_dx_kernel(const GatedGradArgs a, int tiles_k, int64_t tiles_m, int slices, int per,

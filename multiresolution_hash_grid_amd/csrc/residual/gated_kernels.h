@@ -59,7 +59,8 @@ __global__ __launch_bounds__(256) void gated_tile_kernel(const GatedArgs a) {
 // of gate rows and two of up rows, dealt so that a lane ends with 8 consecutive units
 // of both for each of its rows; a wave holds the fragments of 16 rows for all of the
 // contraction.  Sixteen waves of them hide each other's loads better than eight with 32
-// rows each (2^18 x 256 -> 128 51 us and 60, 65537 x 35 -> 93 8.9 and 12.3).  Bound by
+// rows each (2^18 x 256 -> 128 51 us and 60, 65537 x 35 -> 93 8.9 and 12.3).  Rows shorter
+// than a piece are read value by value (2^18 x 3 -> 64 bf16 13 us, in tiles 69).  Bound by
 // memory and by the products that the loads wait for (2^18 x 256 -> 128: 4.0 TB/s).
 constexpr int kLdsBytes = 160 * 1024;
 template <typename T, int KU>
