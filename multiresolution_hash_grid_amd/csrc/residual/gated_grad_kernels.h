@@ -103,7 +103,7 @@ __device__ __forceinline__ void step_barrier() {
 // With few rows the units are cut into slices, whose sums dx_join_kernel adds
 // (256 rows, 256 -> 512: 18.7 + 4 us; the whole backward 40 instead of 57).
 // 2^18 rows, 256 -> 512 bf16 254 us; its bytes at the copy's rate take 179.  Bound by memory:
-// a stretch is half a line of each row of dh, g and u, and half of the lines are fetched
+// a stretch is half a line of each row of dh, g and u, and most lines are fetched
 // again for the other half (1499 MB of 805); one stretch's loads (48 KB a workgroup) are
 // on their way, a second's leave no registers.  Less by the slopes and the products
 // (VALU 40 %, matrix units 22 % busy).
