@@ -341,6 +341,12 @@ def _needs(ctx, n) -> tuple:
     return ctx.needs_input_grad + (False,) * (n - len(ctx.needs_input_grad))
 
 
+def _recorded(*args) -> bool:
+    """Whether autograd records a call of these arguments, whose forward then keeps what the backward reads.  (Inside a
+    Function's forward it cannot be seen: grad mode is off there, and needs_input_grad does not go by it.)"""
+    return torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad for t in args)
+
+
 class HashGridEmbeddingFunction(torch.autograd.Function):
     """Autograd of hashgrid_embedding_forward in the table; its gradient is dense and of the table's type.  The gradient
     cannot be differentiated again: autograd raises."""
@@ -383,13 +389,18 @@ class HashGridCodedInputFunction(torch.autograd.Function):
 
 class HashGridLayerNormFunction(torch.autograd.Function):
     """Autograd of hashgrid_layer_norm_forward: returns y, or (y, s) with a residual, s = x + residual in x's type.
-    Weight and bias may be None.  The gradients cannot be differentiated again: autograd raises."""
+    Weight and bias may be None.  The statistics are kept only where autograd records the call.  The gradients cannot be
+    differentiated again: autograd raises."""
+
+    @classmethod
+    def apply(cls, *args):
+        return super().apply(_recorded(*args), *args)
 
     @staticmethod
-    def forward(ctx, x, weight, bias=None, residual=None, eps=1e-5):
-        out = hashgrid_layer_norm_forward(x, weight, bias, residual=residual, eps=eps, save_sum=residual is not None, save_stats=True)
-        s = x if residual is None else out.sum
-        ctx.save_for_backward(s, weight, out.mean, out.rstd)
+    def forward(ctx, keep, x, weight, bias=None, residual=None, eps=1e-5):
+        out = hashgrid_layer_norm_forward(x, weight, bias, residual=residual, eps=eps, save_sum=residual is not None, save_stats=keep)
+        if keep:
+            ctx.save_for_backward(x if residual is None else out.sum, weight, out.mean, out.rstd)
         ctx.set_materialize_grads(False)  # an output that nothing reads has no gradient, not one of zeros
         return out.y if residual is None else (out.y, out.sum)
 
@@ -397,25 +408,29 @@ class HashGridLayerNormFunction(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dy, ds=None):
         s, weight, mean, rstd = ctx.saved_tensors
-        need = _needs(ctx, 5)
+        need = _needs(ctx, 6)[1:]
         if dy is None:  # s alone goes on
             zero = lambda n: torch.zeros(s.shape[1], device=s.device) if n else None  # noqa: E731
-            return ds, zero(need[1]), zero(need[2]), ds if need[3] else None, None
+            return None, ds, zero(need[1]), zero(need[2]), ds if need[3] else None, None
         dx, dw, db = hashgrid_layer_norm_backward(dy.contiguous(), s, weight, mean, rstd, ds=None if ds is None else ds.contiguous(),
                                                   need_dw=need[1], need_db=need[2])
-        return dx, dw, db, dx if need[3] else None, None
+        return None, dx, dw, db, dx if need[3] else None, None
 
 
 class HashGridGatedFunction(torch.autograd.Function):
     """Autograd of hashgrid_gated_forward: x in a 16-bit type, the weights fp32 masters that the products read rounded to
-    it, biases fp32 or None.  Gradients of the masters are fp32.  The gradients cannot be differentiated again: autograd
-    raises."""
+    it, biases fp32 or None.  Gradients of the masters are fp32.  The projections are kept only where autograd records the
+    call.  The gradients cannot be differentiated again: autograd raises."""
+
+    @classmethod
+    def apply(cls, *args):
+        return super().apply(_recorded(*args), *args)
 
     @staticmethod
-    def forward(ctx, x, w_gate, w_up, b_gate=None, b_up=None, act="silu"):
+    def forward(ctx, keep, x, w_gate, w_up, b_gate=None, b_up=None, act="silu"):
         wg, wu = w_gate.to(x.dtype), w_up.to(x.dtype)
         ctx.act = act
-        if not any(ctx.needs_input_grad):
+        if not keep:
             return hashgrid_gated_forward(x, wg, wu, b_gate, b_up, act=act)
         h, gate, up = hashgrid_gated_forward(x, wg, wu, b_gate, b_up, act=act, save_pre=True)
         ctx.save_for_backward(x, wg, wu, gate, up)
@@ -425,10 +440,10 @@ class HashGridGatedFunction(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dh):
         x, wg, wu, gate, up = ctx.saved_tensors
-        need = _needs(ctx, 6)
+        need = _needs(ctx, 7)[1:]
         out = hashgrid_gated_backward(dh.contiguous(), x, wg, wu, gate, up, act=ctx.act, need_dx=need[0], need_dw=need[1] or need[2],
                                       need_db=need[3] or need[4])
-        return tuple(t if n else None for t, n in zip(out, need)) + (None,)
+        return (None,) + tuple(t if n else None for t, n in zip(out, need)) + (None,)
 
 
 # ------------------------------------------------------------------ modules
@@ -505,7 +520,10 @@ class HashGridGatedHead(torch.nn.Module):
             (wg, bg), (wu, bu) = self._layer(f"gate{i}"), self._layer(f"up{i}")
             f = gated(norm(h, *self._layer(f"norm{i}"), None, self.eps), wg, wu, bg, bu, self.act)
             h = linear(f, *self._layer(f"down{i}"), "none", h)
-        y, _ = norm(h, *self._layer("norm_out"), stem, self.eps)
+        if _recorded(h, stem, *self._layer("norm_out")):
+            y, _ = norm(h, *self._layer("norm_out"), stem, self.eps)
+        else:  # nobody reads the sum
+            y = hashgrid_layer_norm_forward(h, *self._layer("norm_out"), residual=stem, eps=self.eps).y
         return linear(y, *self._layer("out"), "none", None, torch.float32)
 
     def quantized(self) -> "HashGridGatedHead8":
