@@ -13,8 +13,8 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from .hashgrid import _check, _dev, _keep_for_stream
-from .residual import (_CODES, _F, _HALF, _I32, _I64, _P, F8, HashGridLinearFunction, _act, _here, _matrix, _packer, _rows, _vector,
-                       hashgrid_linear_forward, quantize_rows)
+from .residual import (_CODES, _F, _HALF, _I32, _I64, _P, F8, HashGridLinearFunction, _act, _here, _matrix, _packer, _recorded, _rows,
+                       _vector, hashgrid_linear_forward, quantize_rows)
 from .residual import _lib as _residual_lib
 
 _IDS = {torch.int32: 32, torch.int64: 64}
@@ -339,12 +339,6 @@ def hashgrid_gated_backward(dh: torch.Tensor, x: torch.Tensor, w_gate: torch.Ten
 def _needs(ctx, n) -> tuple:
     """needs_input_grad of n arguments, some of which may have been left out."""
     return ctx.needs_input_grad + (False,) * (n - len(ctx.needs_input_grad))
-
-
-def _recorded(*args) -> bool:
-    """Whether autograd records a call of these arguments, whose forward then keeps what the backward reads.  (Inside a
-    Function's forward it cannot be seen: grad mode is off there, and needs_input_grad does not go by it.)"""
-    return torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad for t in args)
 
 
 class HashGridEmbeddingFunction(torch.autograd.Function):

@@ -445,43 +445,57 @@ def hashgrid_adamw_step(tensors, **kw) -> None:
     HashGridAdamWPlan(tensors).step(**kw)
 
 
+def _recorded(*args) -> bool:
+    """Whether autograd records a call of these arguments, whose forward then keeps what the backward reads.  (Inside a
+    Function's forward it cannot be seen: grad mode is off there, and needs_input_grad does not go by it.)"""
+    return torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad for t in args)
+
+
 class HashGridLinearFunction(torch.autograd.Function):
     """Autograd of hashgrid_linear_forward: x in a 16-bit type, the weight an fp32 master that the products read
-    rounded to it, bias fp32, residual in the output's type.  Gradients of the masters are fp32.  The gradients cannot
-    be differentiated again: autograd raises."""
+    rounded to it, bias fp32, residual in the output's type.  Gradients of the masters are fp32.  The pre-activation is
+    kept only where autograd records the call.  The gradients cannot be differentiated again: autograd raises."""
+
+    @classmethod
+    def apply(cls, *args):
+        return super().apply(_recorded(*args), *args)
 
     @staticmethod
-    def forward(ctx, x, weight, bias, act="none", residual=None, out_dtype=None):
+    def forward(ctx, train, x, weight, bias, act="none", residual=None, out_dtype=None):
         w = weight.to(x.dtype)
-        train = any(ctx.needs_input_grad)
         # ReLU's slope can be read from y itself where no residual was added
         keep = train and act != "none" and not (act == "relu" and residual is None and out_dtype in (None, x.dtype))
         out = hashgrid_linear_forward(x, w, bias, act=act, residual=residual, out_dtype=out_dtype, save_pre=keep)
         y, pre = out if keep else (out, out if train and act == "relu" else None)
         ctx.act = act
-        ctx.save_for_backward(x, w, pre)
+        if train:
+            ctx.save_for_backward(x, w, pre)
         return y
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dy):
         x, w, pre = ctx.saved_tensors
-        need = ctx.needs_input_grad + (False,) * (6 - len(ctx.needs_input_grad))  # arguments may have been left out
+        need = ctx.needs_input_grad[1:] + (False,) * (7 - len(ctx.needs_input_grad))  # arguments may have been left out
         dy = dy.contiguous()
         dx, dw, db = hashgrid_linear_backward(dy, x, w, act=ctx.act, pre=pre, need_dx=need[0], need_dw=need[1],
                                               need_db=need[2])
-        return dx, dw, db, None, dy if need[4] else None, None
+        return None, dx, dw, db, None, dy if need[4] else None, None
 
 
 class HashGridRmsNormFunction(torch.autograd.Function):
     """Autograd of hashgrid_rms_norm_forward: returns y, or (y, s) with a residual, s = x + residual in x's type.
-    The gradients cannot be differentiated again: autograd raises."""
+    1 / rms is kept only where autograd records the call.  The gradients cannot be differentiated again: autograd raises."""
+
+    @classmethod
+    def apply(cls, *args):
+        return super().apply(_recorded(*args), *args)
 
     @staticmethod
-    def forward(ctx, x, weight, residual=None, eps=1e-6):
-        out = hashgrid_rms_norm_forward(x, weight, residual=residual, eps=eps, save_sum=residual is not None, save_rstd=True)
-        s = x if residual is None else out.sum
-        ctx.save_for_backward(s, weight, out.rstd)
+    def forward(ctx, keep, x, weight, residual=None, eps=1e-6):
+        out = hashgrid_rms_norm_forward(x, weight, residual=residual, eps=eps, save_sum=residual is not None, save_rstd=keep)
+        if keep:
+            ctx.save_for_backward(x if residual is None else out.sum, weight, out.rstd)
         ctx.set_materialize_grads(False)  # an output that nothing reads has no gradient, not one of zeros
         return out.y if residual is None else (out.y, out.sum)
 
@@ -489,12 +503,12 @@ class HashGridRmsNormFunction(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dy, ds=None):
         s, weight, rstd = ctx.saved_tensors
-        need = ctx.needs_input_grad + (False,) * (4 - len(ctx.needs_input_grad))
+        need = ctx.needs_input_grad[1:] + (False,) * (5 - len(ctx.needs_input_grad))
         if dy is None:  # s alone goes on
-            return ds, torch.zeros_like(weight) if need[1] else None, ds if need[2] else None, None
+            return None, ds, torch.zeros_like(weight) if need[1] else None, ds if need[2] else None, None
         dx, dw = hashgrid_rms_norm_backward(dy.contiguous(), s, weight, rstd, ds=None if ds is None else ds.contiguous(),
                                             need_dw=need[1])
-        return dx, dw, dx if need[2] else None, None
+        return None, dx, dw, dx if need[2] else None, None
 
 
 class HashGridResidualHead(torch.nn.Module):
@@ -540,7 +554,10 @@ class HashGridResidualHead(torch.nn.Module):
         for i in range(self.blocks):
             u = linear(norm(h, getattr(self, f"norm{i}"), None, self.eps), *self._layer(f"up{i}"), self.act)
             h = linear(u, *self._layer(f"down{i}"), "none", h)
-        y, _ = norm(h, self.norm_out, stem, self.eps)
+        if _recorded(h, stem, self.norm_out):
+            y, _ = norm(h, self.norm_out, stem, self.eps)
+        else:  # nobody reads the sum
+            y = hashgrid_rms_norm_forward(h, self.norm_out, residual=stem, eps=self.eps).y
         return linear(y, *self._layer("out"), "none", None, torch.float32)
 
     def quantized(self) -> "HashGridResidualHead8":
