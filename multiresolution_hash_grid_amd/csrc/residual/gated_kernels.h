@@ -46,7 +46,8 @@ __global__ __launch_bounds__(256) void gated_tile_kernel(const GatedArgs a) {
     if (m >= a.m || n >= a.n) return;
     float zg = 0.f, zu = 0.f;
     for (int i = 0; i < 4; ++i) zg += sums[0][i][(col >> 2) * 16 + row][col & 3], zu += sums[1][i][(col >> 2) * 16 + row][col & 3];
-    if constexpr (sizeof(T) == 1) zg *= a.x_scale[m] * a.g_scale[n], zu *= a.x_scale[m] * a.u_scale[n];
+    // (one after the other: two scales of usable rows may multiply to 0 or infinity)
+    if constexpr (sizeof(T) == 1) zg = zg * a.x_scale[m] * a.g_scale[n], zu = zu * a.x_scale[m] * a.u_scale[n];
     if (a.bg) zg += a.bg[n];
     if (a.bu) zu += a.bu[n];
     if constexpr (sizeof(T) == 2)
