@@ -341,6 +341,16 @@ def _needs(ctx, n) -> tuple:
     return ctx.needs_input_grad + (False,) * (n - len(ctx.needs_input_grad))
 
 
+_GRAD_STRIDE = 1 << 22  # the longest row stride that every backward takes
+
+
+def _as_rows(t: torch.Tensor) -> torch.Tensor:
+    """An upstream gradient as the kernels take it: itself where its rows lie apart and their columns together, as those
+    of a slice of a wider gradient do, else a contiguous copy (of one value expanded, for instance)."""
+    (m, c), (row, column) = t.shape, t.stride()
+    return t if (column == 1 or c == 1) and (m == 1 or c <= row <= _GRAD_STRIDE) else t.contiguous()
+
+
 class HashGridEmbeddingFunction(torch.autograd.Function):
     """Autograd of hashgrid_embedding_forward in the table; its gradient is dense and of the table's type.  The gradient
     cannot be differentiated again: autograd raises."""
@@ -355,7 +365,7 @@ class HashGridEmbeddingFunction(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dy):
         rows, dtype = ctx.table
-        return hashgrid_embedding_backward(dy.contiguous(), *ctx.saved_tensors, rows, scale=ctx.scale, table_dtype=dtype), None, None, None
+        return hashgrid_embedding_backward(_as_rows(dy), *ctx.saved_tensors, rows, scale=ctx.scale, table_dtype=dtype), None, None, None
 
 
 class HashGridCodedInputFunction(torch.autograd.Function):
@@ -376,7 +386,7 @@ class HashGridCodedInputFunction(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dx):
         (ids,), f, (rows, dtype) = ctx.saved_tensors, ctx.width, ctx.table
-        need, dx = _needs(ctx, 5), dx.contiguous()
+        need, dx = _needs(ctx, 5), _as_rows(dx)
         dtable = hashgrid_embedding_backward(dx[:, f:], ids, rows, scale=ctx.scale, table_dtype=dtype) if need[1] else None
         return dx[:, :f].to(ctx.kind) if need[0] else None, dtable, None, None, None
 
@@ -406,7 +416,7 @@ class HashGridLayerNormFunction(torch.autograd.Function):
         if dy is None:  # s alone goes on
             zero = lambda n: torch.zeros(s.shape[1], device=s.device) if n else None  # noqa: E731
             return None, ds, zero(need[1]), zero(need[2]), ds if need[3] else None, None
-        dx, dw, db = hashgrid_layer_norm_backward(dy.contiguous(), s, weight, mean, rstd, ds=None if ds is None else ds.contiguous(),
+        dx, dw, db = hashgrid_layer_norm_backward(_as_rows(dy), s, weight, mean, rstd, ds=None if ds is None else _as_rows(ds),
                                                   need_dw=need[1], need_db=need[2])
         return None, dx, dw, db, dx if need[3] else None, None
 
@@ -435,7 +445,7 @@ class HashGridGatedFunction(torch.autograd.Function):
     def backward(ctx, dh):
         x, wg, wu, gate, up = ctx.saved_tensors
         need = _needs(ctx, 7)[1:]
-        out = hashgrid_gated_backward(dh.contiguous(), x, wg, wu, gate, up, act=ctx.act, need_dx=need[0], need_dw=need[1] or need[2],
+        out = hashgrid_gated_backward(_as_rows(dh), x, wg, wu, gate, up, act=ctx.act, need_dx=need[0], need_dw=need[1] or need[2],
                                       need_db=need[3] or need[4])
         return (None,) + tuple(t if n else None for t, n in zip(out, need)) + (None,)
 
