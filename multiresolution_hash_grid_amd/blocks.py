@@ -302,7 +302,9 @@ def hashgrid_gated_backward(dh: torch.Tensor, x: torch.Tensor, w_gate: torch.Ten
     """(dx, dw_gate, dw_up, db_gate, db_up) of hashgrid_gated_forward for upstream ``dh`` [m, n], from the projections
     ``gate`` and ``up`` it kept, all in x's type.  dx has x's type, the weights' gradients ``weight_dtype`` (float32 or
     x's type), the biases' float32.  ``need_*`` leave outputs out (None).  ``dx``, ``dw_*``, ``db_*`` receive the
-    outputs (of a pair both or neither); with ``accumulate`` dw_* and db_*, which must be given, are added to."""
+    outputs (of a pair both or neither); with ``accumulate`` dw_* and db_*, which must be given, are added to.  The
+    gradients of gate and up enter the products in x's type: in float16, upstream gradients below some 2^-14 (a mean
+    loss over many points has them) need a loss scale."""
     m, k = _matrix(x, "x").shape
     n = _matrix(w_gate, "w_gate").shape[0]
     dtype, device, mn, nk = x.dtype, x.device, (m, n), (n, k)
@@ -475,7 +477,9 @@ class HashGridGatedHead(torch.nn.Module):
 
     norm is the layer norm.  ``hidden`` is the blocks' width between (2 * width by default).  Weights, biases, codes and
     the norms' weights are fp32 masters; activations and the weights' copies that the matrix cores read are ``dtype``
-    (bfloat16 or float16).  ``quantized()`` is the same head for inference with 8-bit operands behind the blocks' norms."""
+    (bfloat16 or float16; gradients pass in it too, so in float16 the loss of many points needs a scale, whose inverse
+    HashGridAdamW.step takes as ``grad_scale``).  Without a graph to record, as under torch.no_grad(), nothing is kept
+    for a backward.  ``quantized()`` is the same head for inference with 8-bit operands behind the blocks' norms."""
 
     def __init__(self, in_features=32, width=256, blocks=2, out_features=4, hidden=None, act="silu", codes=0, code_width=64,
                  dtype=torch.bfloat16, eps=1e-5, device="cuda"):
