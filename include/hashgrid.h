@@ -723,14 +723,14 @@ int hashgrid_gated_forward(const hg_gated *op, void *stream);
  * dg and du are rounded to the operands' type where they enter a product; dbg and
  * dbu sum them unrounded; sums are fp32, outputs are rounded once.  With HG_F16 dg
  * and du have binary16's range there: below 2^-14 they keep steps of 2^-24, and past
- * 65504 they are infinite.  A dh of 4e-6, which a mean over 2^18 points has, so leaves
- * dx, dwg and dwu off by 0.8 % in the 2-norm, one of 1e-6 by 3 % (larger ones by
- * 0.03 %): scale such a dh, or the loss, by a power of two, and the gradients back.  Where ReLU's g
- * is 0 or below, dg and du are 0 whatever dh and u hold.  The weights' and biases'
- * gradients are WRITTEN, or added to with accumulate; with m == 0 they are zero (or
- * unchanged).  The order of every sum is fixed by the sizes.  Row strides of dh,
- * gate, up, x and dx are at most 2^22 (with one row they are not looked at).
- * Outputs overlap no input. */
+ * 65504 they are infinite.  A dh of 4e-6, which a mean over 2^18 points has, so
+ * leaves dx, dwg and dwu off by 0.8 % in the 2-norm, one of 1e-6 by 3 % (larger ones
+ * by 0.03 %): scale such a dh, or the loss, by a power of two, and the gradients
+ * back.  Where ReLU's g is 0 or below, dg and du are 0 whatever dh and u hold.  The
+ * weights' and biases' gradients are WRITTEN, or added to with accumulate; with
+ * m == 0 they are zero (or unchanged).  The order of every sum is fixed by the sizes.
+ * Row strides of dh, gate, up, x and dx are at most 2^22 (with one row they are not
+ * looked at).  Outputs overlap no input. */
 typedef struct {
     int64_t m;
     int32_t k, n;
